@@ -16,8 +16,9 @@ OUT = os.path.join(HERE, "libsvdq.so")
 BUILD = os.path.join(HERE, "_build")
 ARCH = "gfx950"
 
-DEVICE_SOURCES = ["k1_quant_lora_down.hip", "k2_gemm_w4a4.hip", "k3_lora_up.hip", "k4_w4a16.hip", "api.cpp", "noalloc.hip"]
-HOST_SOURCES = ["pack.cpp", "status.cpp"]
+DEVICE_SOURCES = ["k1_quant_lora_down.hip", "k2_gemm_w4a4.hip", "k3_lora_up.hip", "k4_w4a16.hip", "k5_quant_int8.hip",
+                  "k6_gemm_w8a8.hip", "k7_group_norm.hip", "api.cpp", "api_int8.cpp", "noalloc.hip"]
+HOST_SOURCES = ["pack.cpp", "pack_int8.cpp", "status.cpp"]
 
 HIP_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17",

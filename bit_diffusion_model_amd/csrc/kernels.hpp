@@ -80,4 +80,34 @@ hipError_t launch_k2_debug(const KernelLayer& L, int64_t M, const uint8_t* qX, b
 hipError_t launch_w4a16(int64_t M, int64_t K, int64_t N, const uint16_t* X, int64_t ldx, const uint8_t* qW,
                         const uint16_t* sW, void* Y, int64_t ldy, int ydtype, hipStream_t st);
 
+// ---- the 8-bit layer (rows of codes are i8_ld(K) bytes long, zeros past K)
+
+// 8-bit codes and one scale per token of X [M][ldx] (xdtype 0 fp32, 1 bf16) times inv_s (may be NULL).
+hipError_t launch_quant_i8(int64_t M, int64_t K, const void* X, int xdtype, int64_t ldx, const float* inv_s, int8_t* qX,
+                           float* sX, hipStream_t st);
+// Y = (qX qW^T) sX sW + bias (bias may be NULL); ydtype 0 fp32, 1 bf16, 2 bf16 of GELU.
+hipError_t launch_w8a8(int64_t M, int64_t K, int64_t N, const int8_t* qX, const float* sX, const int8_t* qW,
+                       const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype, hipStream_t st);
+
+// ---- the channels-last group norm
+
+struct NormArgs {
+  int64_t B, S;
+  int C, G, act;  // act: svdq_gn_act
+  float eps;
+  const float *gamma, *beta;  // either may be NULL
+  const void* X;
+  int xdtype;  // 0 fp32, 1 bf16
+  int64_t bsx, ldx;
+};
+// The statistics' split: blocks of `chunk` positions, `parts` of them per image, `bytes` of workspace.
+struct NormPlan {
+  int64_t chunk;
+  uint32_t parts;
+  size_t bytes;
+};
+NormPlan plan_norm(int64_t B, int64_t S, int C, int G);
+hipError_t launch_norm(const NormArgs& a, void* Y, int ydtype, int64_t bsy, int64_t ldy, void* ws, hipStream_t st);
+hipError_t launch_norm_quant(const NormArgs& a, const float* inv_s, int8_t* qX, float* sX, void* ws, hipStream_t st);
+
 }  // namespace svdq

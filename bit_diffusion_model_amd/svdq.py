@@ -24,6 +24,7 @@ MLP_CHAINED, MLP_SEPARATE = 0, 1  # svdq_mlp_mode
 FMT = {"int4": INT4_G64, "mxfp4": MXFP4_G32, "nvfp4": NVFP4_G16}
 GROUP = {INT4_G64: 64, MXFP4_G32: 32, NVFP4_G16: 16}
 MAX_RANK = 128
+GN_NONE, GN_SILU, GN_GELU = 0, 1, 2  # svdq_gn_act
 
 
 class SvdqError(RuntimeError):
@@ -38,6 +39,16 @@ class _Layer(ctypes.Structure):
     ]
 
 
+class _Int8Layer(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int64), ("N", ctypes.c_int64), ("inv_s", ctypes.c_void_p), ("qW", ctypes.c_void_p),
+                ("sW", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class _GroupNorm(ctypes.Structure):
+    _fields_ = [("C", ctypes.c_int64), ("groups", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p)]
+
+
 _lib = None
 
 EXPORTS = [
@@ -48,6 +59,10 @@ EXPORTS = [
     "svdq_linear_forward", "svdq_linear_forward_unfused", "svdq_debug_group_sums", "svdq_linear_forward_noalloc",
     "svdq_mlp_workspace_bytes", "svdq_mlp_forward", "svdq_mlp_chain_gemm", "svdq_mlp_chain_reduce",
     "svdq_w4a16_gemm", "svdq_forward_k1_parts",
+    "svdq_int8_ld", "svdq_pack_weights_int8", "svdq_quantize_act_int8", "svdq_gemm_w8a8_workspace_bytes",
+    "svdq_int8_workspace_bytes", "svdq_gemm_w8a8", "svdq_linear_forward_int8", "svdq_group_norm_workspace_bytes",
+    "svdq_group_norm", "svdq_group_norm_quantize_int8", "svdq_norm_linear_int8_workspace_bytes",
+    "svdq_norm_linear_forward_int8",
 ]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -86,6 +101,21 @@ def lib():
         "svdq_mlp_chain_gemm": (I32, [P, P, I64, P, P, P, P, P, P, P, I64, P]),
         "svdq_mlp_chain_reduce": (I32, [P, P, I64, P, P, P]),
         "svdq_w4a16_gemm": (I32, [I64, I64, I64, P, I64, P, P, P, I64, I32, P]),
+    }
+    SZ = ctypes.c_size_t
+    sig |= {
+        "svdq_int8_ld": (I64, [I64]),
+        "svdq_pack_weights_int8": (I32, [I64, I64, P, P, F, P, P, P, P]),
+        "svdq_quantize_act_int8": (I32, [I64, I64, P, I32, I64, P, P, P, P]),
+        "svdq_gemm_w8a8_workspace_bytes": (SZ, [P, I64]),
+        "svdq_int8_workspace_bytes": (SZ, [P, I64]),
+        "svdq_gemm_w8a8": (I32, [P, I64, P, P, P, I64, I32, P, SZ, P]),
+        "svdq_linear_forward_int8": (I32, [P, I64, P, I32, I64, P, I64, I32, P, SZ, P]),
+        "svdq_group_norm_workspace_bytes": (SZ, [P, I64, I64]),
+        "svdq_group_norm": (I32, [P, I64, I64, P, I32, I64, I64, P, I32, I64, I64, P, SZ, P]),
+        "svdq_group_norm_quantize_int8": (I32, [P, I64, I64, P, I32, I64, I64, P, P, P, P, SZ, P]),
+        "svdq_norm_linear_int8_workspace_bytes": (SZ, [P, P, I64, I64]),
+        "svdq_norm_linear_forward_int8": (I32, [P, P, I64, I64, P, I32, I64, I64, P, I64, I32, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -512,4 +542,229 @@ class WeightOnlyLinear:
                               device=self.device)
         _check(lib().svdq_w4a16_gemm(M, self.K, self.N, _dptr(X), X.stride(0), _dptr(self.qW), _dptr(self.sW),
                                      _dptr(out), out.stride(0), ydtype, _stream()))
+        return out
+
+
+# ------------------------------------------------------------------ the 8-bit layer (W8A8) and the group norm
+
+def int8_ld(K: int) -> int:
+    """Bytes of a row of 8-bit codes: K rounded up to a multiple of 128."""
+    return (K + 127) // 128 * 128
+
+
+def pack_weights_int8(W_bits: np.ndarray, act_absmax_: Optional[np.ndarray] = None, alpha: float = 0.5):
+    """svdq_pack_weights_int8 on W (bf16 bits [K][N]): (s, inv_s, qW int8 [N][int8_ld(K)], sW fp32 [N])."""
+    W = np.ascontiguousarray(W_bits, dtype=np.uint16)
+    K, N = W.shape
+    s, inv = np.empty(K, np.float32), np.empty(K, np.float32)
+    qW, sW = np.empty((N, int8_ld(K)), np.int8), np.empty(N, np.float32)
+    a = None if act_absmax_ is None else np.ascontiguousarray(act_absmax_, dtype=np.float32)
+    _check(lib().svdq_pack_weights_int8(K, N, _ptr(W), _ptr(a), float(alpha), _ptr(s), _ptr(inv), _ptr(qW), _ptr(sW)))
+    return s, inv, qW, sW
+
+
+_cfg = None
+
+
+def _rt():
+    """torch, the dtypes' svdq_dtype and the raw-stream lookup, found once (the 8-bit calls can be
+    shorter than the lookups)."""
+    global _cfg
+    if _cfg is None:
+        torch = _torch()
+        _cfg = (torch, {torch.float32: F32, torch.bfloat16: BF16}, {F32: torch.float32, BF16: torch.bfloat16,
+                                                                   BF16_GELU: torch.bfloat16}, lib())
+    return _cfg
+
+
+def _dev_tensor(t, name: str, dtype, device, n=None):
+    """A numpy array uploaded, or a device tensor checked: contiguous, of dtype, of n values."""
+    torch = _torch()
+    if t is None:
+        return None
+    if isinstance(t, np.ndarray):
+        t = torch.from_numpy(np.ascontiguousarray(t)).to(device)
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise SvdqError(f"{name} must be a contiguous {dtype} device tensor" + ("" if n is None else f" of {n} values"))
+    return t
+
+
+def _on_current_device(torch, t):
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise SvdqError(f"the tensor is on {t.device}, the current HIP device is {torch.cuda.current_device()}")
+
+
+class Int8Linear:
+    """The 8-bit layer on the GPU: codes qW int8 [N][int8_ld(K)] (zeros past K), sW fp32 [N], inv_s fp32 [K]
+    and bias fp32 [N] or None; numpy arrays are uploaded, device tensors are used as they are."""
+
+    def __init__(self, qW, sW, K: int, inv_s=None, bias=None, device="cuda:0"):
+        torch = _torch()
+        self.K, self.N = int(K), int(qW.shape[0])
+        if qW.ndim != 2 or qW.shape[1] != int8_ld(self.K):
+            raise SvdqError(f"qW must be [N][{int8_ld(self.K)}]")
+        self.qW = _dev_tensor(qW, "qW", torch.int8, device)
+        self.sW = _dev_tensor(sW, "sW", torch.float32, device, self.N)
+        self.inv_s = _dev_tensor(inv_s, "inv_s", torch.float32, device, self.K)
+        self.bias = _dev_tensor(bias, "bias", torch.float32, device, self.N)
+        self.device = self.qW.device
+        self._c = _Int8Layer(self.K, self.N, _dptr(self.inv_s), _dptr(self.qW), _dptr(self.sW), _dptr(self.bias))
+        self._ref = ctypes.addressof(self._c)
+
+    @classmethod
+    def from_weights(cls, W_bits: np.ndarray, act_absmax_: Optional[np.ndarray] = None, alpha: float = 0.5, bias=None,
+                     device="cuda:0") -> "Int8Linear":
+        """Pack W (bf16 bits [K][N]) with svdq_pack_weights_int8 and upload the result."""
+        _, inv, qW, sW = pack_weights_int8(W_bits, act_absmax_, alpha)
+        return cls(qW, sW, W_bits.shape[0], None if act_absmax_ is None else inv, bias, device)
+
+    def quantize(self, X, out=None):
+        """(qX int8 [M][int8_ld(K)], sX fp32 [M]) of X [M][K] under the layer's smoothing."""
+        return quantize_act_int8(X, self.inv_s, out)
+
+    def _out(self, M, ydtype, out, X):
+        torch, _, ty, L = _rt()
+        _on_current_device(torch, X)
+        if out is None:
+            return torch.empty((M, self.N), dtype=ty[ydtype], device=X.device)
+        if out.shape != (M, self.N) or out.dtype != ty[ydtype] or out.stride(1) != 1 or not out.is_cuda:
+            raise SvdqError(f"out must be a [{M}][{self.N}] {ty[ydtype]} device tensor with unit column stride")
+        return out
+
+    def gemm(self, qX, sX, ydtype: int = F32, out=None, workspace=None):
+        """svdq_gemm_w8a8: Y [M][N] from codes qX int8 [M][int8_ld(K)] and their scales sX fp32 [M]."""
+        torch, _, _, L = _rt()
+        M = qX.shape[0]
+        if qX.dtype != torch.int8 or sX.dtype != torch.float32 or qX.shape[1] != int8_ld(self.K) or sX.numel() != M or \
+                not qX.is_contiguous() or not sX.is_contiguous():
+            raise SvdqError(f"qX must be contiguous int8 [M][{int8_ld(self.K)}] and sX contiguous fp32 [M]")
+        out = self._out(M, ydtype, out, qX)
+        n = L.svdq_gemm_w8a8_workspace_bytes(self._ref, M)
+        ws = workspace if workspace is not None or n == 0 else torch.empty(n, dtype=torch.uint8, device=qX.device)
+        _check(L.svdq_gemm_w8a8(self._ref, M, qX.data_ptr(), sX.data_ptr(), out.data_ptr(),
+                                _ld(M, out.stride(0), self.N), ydtype, None if ws is None else ws.data_ptr(),
+                                0 if ws is None else ws.numel(), _raw_stream(qX)))
+        return out
+
+    def workspace(self, M: int):
+        torch, _, _, L = _rt()
+        return torch.empty(max(L.svdq_int8_workspace_bytes(self._ref, M), 256), dtype=torch.uint8, device=self.device)
+
+    def forward(self, X, ydtype: int = F32, out=None, workspace=None):
+        """svdq_linear_forward_int8: quantizer and product on X [M][K], fp32 or bf16, any row stride."""
+        torch, xt, _, L = _rt()
+        M = _check_rows(X, self.K, xt)
+        out = self._out(M, ydtype, out, X)
+        ws = workspace if workspace is not None else self.workspace(M)
+        _check(L.svdq_linear_forward_int8(self._ref, M, X.data_ptr(), xt[X.dtype], _ld(M, X.stride(0), self.K),
+                                          out.data_ptr(), _ld(M, out.stride(0), self.N), ydtype, ws.data_ptr(), ws.numel(), _raw_stream(X)))
+        return out
+
+
+def _ld(n: int, stride: int, length: int) -> int:
+    """The stride of n rows of `length` values; a single row's is not used, whatever torch says."""
+    return stride if n > 1 else max(stride, length)
+
+
+def _check_rows(X, K, xt) -> int:
+    if X.dim() != 2 or X.shape[1] != K or X.dtype not in xt or (K > 1 and X.stride(1) != 1):
+        raise SvdqError(f"X must be an fp32 or bf16 [M][{K}] tensor with unit column stride")
+    return X.shape[0]
+
+
+def _raw_stream(t) -> int:
+    return _cfg[0].cuda.current_stream(t.device).cuda_stream
+
+
+def quantize_act_int8(X, inv_s=None, out=None):
+    """svdq_quantize_act_int8: (qX int8 [M][int8_ld(K)], sX fp32 [M]) of X [M][K] times inv_s."""
+    torch, xt, _, L = _rt()
+    K = X.shape[-1]
+    M = _check_rows(X, K, xt)
+    _on_current_device(torch, X)
+    inv_s = _dev_tensor(inv_s, "inv_s", torch.float32, X.device, K)
+    if out is None:
+        out = (torch.empty((M, int8_ld(K)), dtype=torch.int8, device=X.device),
+               torch.empty(M, dtype=torch.float32, device=X.device))
+    _check(L.svdq_quantize_act_int8(M, K, X.data_ptr(), xt[X.dtype], _ld(M, X.stride(0), K),
+                                    None if inv_s is None else inv_s.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
+                                    _raw_stream(X)))
+    return out
+
+
+class GroupNorm:
+    """Channels-last group norm with an activation (GN_NONE, GN_SILU, GN_GELU): X [B][S][C] or [B][H][W][C], fp32
+    or bf16, unit channel stride; gamma and beta fp32 [C] device tensors (or numpy), or None."""
+
+    def __init__(self, groups: int, C: int, gamma=None, beta=None, eps: float = 1e-5, act: int = GN_NONE,
+                 device="cuda:0"):
+        torch = _torch()
+        self.C, self.groups, self.eps, self.act = int(C), int(groups), float(eps), int(act)
+        self.gamma = _dev_tensor(gamma, "gamma", torch.float32, device, self.C)
+        self.beta = _dev_tensor(beta, "beta", torch.float32, device, self.C)
+        self._c = _GroupNorm(self.C, self.groups, self.act, self.eps, _dptr(self.gamma), _dptr(self.beta))
+        self._ref = ctypes.addressof(self._c)
+
+    def _geometry(self, X, what="X"):
+        """(B, S, bs, ld): images, positions, image and position stride of X."""
+        _, xt, _, _ = _rt()
+        if X.dim() not in (3, 4) or X.shape[-1] != self.C or X.dtype not in xt or (self.C > 1 and X.stride(-1) != 1):
+            raise SvdqError(f"{what} must be an fp32 or bf16 [B][S][{self.C}] or [B][H][W][{self.C}] tensor with unit "
+                            "channel stride")
+        if X.dim() == 4:
+            B, H, W, _ = X.shape
+            if H > 1 and W > 1 and X.stride(1) != W * X.stride(2):
+                raise SvdqError(f"{what}'s rows of positions must follow each other at one stride")
+            return B, H * W, X.stride(0), _ld(H * W, X.stride(2) if W > 1 else X.stride(1), self.C)
+        return X.shape[0], X.shape[1], X.stride(0), _ld(X.shape[1], X.stride(1), self.C)
+
+    def workspace(self, B: int, S: int, device):
+        torch, _, _, L = _rt()
+        n = L.svdq_group_norm_workspace_bytes(self._ref, B, S)
+        return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+    def forward(self, X, ydtype: int = BF16, out=None, workspace=None):
+        """svdq_group_norm: act(norm(X)) in X's shape, fp32 or bf16."""
+        torch, xt, ty, L = _rt()
+        B, S, bs, ld = self._geometry(X)
+        _on_current_device(torch, X)
+        if ydtype not in (F32, BF16):
+            raise SvdqError("the norm's output is F32 or BF16")
+        if out is None:
+            out = torch.empty(X.shape, dtype=ty[ydtype], device=X.device)
+        elif out.shape != X.shape or out.dtype != ty[ydtype] or not out.is_cuda:
+            raise SvdqError(f"out must be a {tuple(X.shape)} {ty[ydtype]} device tensor")
+        _, _, bsy, ldy = self._geometry(out, "out")
+        ws = workspace if workspace is not None else self.workspace(B, S, X.device)
+        _check(L.svdq_group_norm(self._ref, B, S, X.data_ptr(), xt[X.dtype], bs, ld, out.data_ptr(),
+                                 ydtype, bsy, ldy, ws.data_ptr(), ws.numel(), _raw_stream(X)))
+        return out
+
+    def quantize(self, X, inv_s=None, out=None, workspace=None):
+        """svdq_group_norm_quantize_int8: (qX int8 [B S][int8_ld(C)], sX fp32 [B S]) of act(norm(X)) inv_s."""
+        torch, xt, _, L = _rt()
+        B, S, bs, ld = self._geometry(X)
+        _on_current_device(torch, X)
+        inv_s = _dev_tensor(inv_s, "inv_s", torch.float32, X.device, self.C)
+        if out is None:
+            out = (torch.empty((B * S, int8_ld(self.C)), dtype=torch.int8, device=X.device),
+                   torch.empty(B * S, dtype=torch.float32, device=X.device))
+        ws = workspace if workspace is not None else self.workspace(B, S, X.device)
+        _check(L.svdq_group_norm_quantize_int8(self._ref, B, S, X.data_ptr(), xt[X.dtype], bs, ld,
+                                               None if inv_s is None else inv_s.data_ptr(), out[0].data_ptr(),
+                                               out[1].data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(X)))
+        return out
+
+    def forward_linear(self, X, layer: Int8Linear, ydtype: int = BF16, out=None, workspace=None):
+        """svdq_norm_linear_forward_int8: layer(act(norm(X))) [B S][N], the norm's output in 8-bit codes."""
+        torch, xt, _, L = _rt()
+        B, S, bs, ld = self._geometry(X)
+        out = layer._out(B * S, ydtype, out, X)
+        ws = workspace
+        if ws is None:
+            n = L.svdq_norm_linear_int8_workspace_bytes(self._ref, layer._ref, B, S)
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=X.device)
+        _check(L.svdq_norm_linear_forward_int8(self._ref, layer._ref, B, S, X.data_ptr(), xt[X.dtype], bs, ld,
+                                               out.data_ptr(), _ld(B * S, out.stride(0), layer.N), ydtype,
+                                               ws.data_ptr(), ws.numel(), _raw_stream(X)))
         return out

@@ -436,6 +436,111 @@ svdq_status svdq_mlp_chain_gemm(const svdq_layer* fc1, const svdq_layer* fc2, in
 svdq_status svdq_mlp_chain_reduce(const svdq_layer* fc1, const svdq_layer* fc2, int64_t M, const float* lora_part,
                                   void* lora_act2, void* stream);
 
+/* --------------------------------------------------- the 8-bit layer (W8A8) ---- */
+/* The 8-bit predecessor of the layer (ch3chohch3.github.io post, section "Smooth Quant
+ * （W8A8）"): smoothed activations in 8 bits with one scale per token, weights in 8 bits with
+ * one scale per output channel, for the layers that 4 bits would hurt.
+ *   quantize  v = x inv_s;  a = max(max_k |v|, 2^-96);  s_X = a / 127;  r = 127 / a;
+ *             q = round_half_even(v r), in [-127, 127]; every operation one fp32 rounding.  A
+ *             row that holds a NaN or an infinity gets a NaN scale and zero codes, so its
+ *             outputs are NaN and no other row's change.
+ *   product   Y = ((float)(sum_k qX qW) s_X[m]) s_W[n] + bias[n], the sum exact in 32-bit
+ *             integers, the rest in fp32, then GELU if asked, rounded once to Y's type.
+ * Rows of codes, of activations and weights alike, are svdq_int8_ld(K) = K rounded up to 128
+ * bytes long; the bytes past K are zero.  X is fp32 or bf16 (svdq_dtype SVDQ_F32 /
+ * SVDQ_BF16) of any K >= 1 and any row stride ldx >= K; rows that are 16-byte aligned are
+ * read by wide loads.  Limits: K <= 131072 (the integer sums stay below 2^31), M and N
+ * below 2^31, ldy < 2^31 (EUNSUPPORTED beyond). */
+typedef struct svdq_int8_layer {
+  int64_t K, N;
+  const float* inv_s; /* [K] fp32 reciprocal smoothing factor, or NULL for none */
+  const int8_t* qW;   /* [N][svdq_int8_ld(K)] codes, row n = output channel n along K */
+  const float* sW;    /* [N] fp32 */
+  const float* bias;  /* [N] fp32, or NULL for none */
+} svdq_int8_layer;    /* device pointers, 16-byte aligned, owned by the caller */
+
+/* Bytes of a row of 8-bit codes: K rounded up to a multiple of 128 (0 for K < 1). */
+int64_t svdq_int8_ld(int64_t K);
+
+/* Offline pack (host): smoothing as svdq_pack_weights (s = 1 when act_absmax is NULL), W_hat =
+ * diag(s) W in fp64, per output channel n: sW = fp32(max_k |W_hat| / 127), q =
+ * round_half_even(W_hat / sW) clamped to [-127, 127] (all 0 where sW is 0).
+ * W host bf16 [K][N]; outputs (host): s_out, inv_s_out [K] fp32; qW_out [N][svdq_int8_ld(K)],
+ * zero past K; sW_out [N] fp32.  EINVAL on NULL, K < 1, N < 1, alpha outside [0, 1];
+ * EUNSUPPORTED on K > 131072; ENUMERIC on non-finite W or act_absmax. */
+svdq_status svdq_pack_weights_int8(int64_t K, int64_t N, const uint16_t* W, const float* act_absmax, float alpha,
+                                   float* s_out, float* inv_s_out, int8_t* qW_out, float* sW_out);
+
+/* The quantizer alone: X [M][ldx] (device, svdq_dtype xdtype) -> qX [M][svdq_int8_ld(K)] (16-byte
+ * aligned), sX [M] fp32.  inv_s [K] (16-byte aligned) or NULL.  One launch; M == 0 is a no-op.
+ * EINVAL on NULL, misalignment, sizes; EUNSUPPORTED on another xdtype or a limit; EHIP. */
+svdq_status svdq_quantize_act_int8(int64_t M, int64_t K, const void* X, int32_t xdtype, int64_t ldx,
+                                   const float* inv_s, int8_t* qX, float* sX, void* stream);
+
+/* Bytes of device workspace svdq_gemm_w8a8 / svdq_linear_forward_int8 need for M rows (0: none, or
+ * bad arguments). */
+size_t svdq_gemm_w8a8_workspace_bytes(const svdq_int8_layer* layer, int64_t M);
+size_t svdq_int8_workspace_bytes(const svdq_int8_layer* layer, int64_t M);
+
+/* The product alone on codes as svdq_quantize_act_int8 writes them (qX 16-byte aligned; the bytes
+ * past K may hold anything: the weights' are zero).  Y device [M][ldy], svdq_dtype ydtype,
+ * overwritten; columns >= N are not touched.  workspace: >= svdq_gemm_w8a8_workspace_bytes,
+ * 256-byte aligned (NULL where that is 0).  M == 0 is a no-op.  Errors as above. */
+svdq_status svdq_gemm_w8a8(const svdq_int8_layer* layer, int64_t M, const int8_t* qX, const float* sX, void* Y,
+                           int64_t ldy, int32_t ydtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* The layer: quantizer, then product, on `stream`, the codes in `workspace` (>=
+ * svdq_int8_workspace_bytes, 256-byte aligned, contents on entry irrelevant).  The same result,
+ * bit for bit, as the two calls above. */
+svdq_status svdq_linear_forward_int8(const svdq_int8_layer* layer, int64_t M, const void* X, int32_t xdtype,
+                                     int64_t ldx, void* Y, int64_t ldy, int32_t ydtype, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
+/* --------------------------------------- group norm with an activation, channels last ---- */
+/* X [B][S][C] (image, position, channel; position stride ldx, image stride bsx, in elements), C =
+ * groups * cpg.  Per image and group over all positions and the group's channels: mean and
+ * biased variance in fp32 (sums of differences to a pivot, joined pairwise: no cancellation
+ * however far the mean lies from zero); y = act((x - mean) / sqrt(var + eps) gamma_c + beta_c).
+ * A NaN or an infinity makes its group's outputs NaN, as the formula does.  Limits: C <= 4096,
+ * B <= 65535 (EUNSUPPORTED beyond).  B == 0 or S == 0 is a no-op. */
+typedef enum { SVDQ_GN_NONE = 0, SVDQ_GN_SILU = 1, SVDQ_GN_GELU = 2 } svdq_gn_act;
+typedef struct svdq_group_norm_desc {
+  int64_t C;
+  int32_t groups;
+  int32_t act;        /* svdq_gn_act */
+  float eps;          /* > 0 */
+  const float* gamma; /* device [C] fp32, or NULL for 1 */
+  const float* beta;  /* device [C] fp32, or NULL for 0 */
+} svdq_group_norm_desc;
+
+/* Bytes of device workspace of the calls below for B images of S positions (0 on bad arguments). */
+size_t svdq_group_norm_workspace_bytes(const svdq_group_norm_desc* norm, int64_t B, int64_t S);
+
+/* Y [B][S][C] (position stride ldy, image stride bsy), SVDQ_F32 or SVDQ_BF16; X fp32 or bf16.
+ * Y may be X itself (same type and strides).  workspace >= svdq_group_norm_workspace_bytes,
+ * 256-byte aligned.  EINVAL on NULL, misalignment, sizes; EUNSUPPORTED on another type or a
+ * limit; EHIP on launch error. */
+svdq_status svdq_group_norm(const svdq_group_norm_desc* norm, int64_t B, int64_t S, const void* X, int32_t xdtype,
+                            int64_t bsx, int64_t ldx, void* Y, int32_t ydtype, int64_t bsy, int64_t ldy,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/* The norm leaving as 8-bit codes: y as above kept in fp32, then the quantizer of the 8-bit
+ * layer on each position's C channels (inv_s [C], 16-byte aligned, or NULL): qX
+ * [B S][svdq_int8_ld(C)], sX [B S].  The 16-bit norm output never goes to memory. */
+svdq_status svdq_group_norm_quantize_int8(const svdq_group_norm_desc* norm, int64_t B, int64_t S, const void* X,
+                                          int32_t xdtype, int64_t bsx, int64_t ldx, const float* inv_s, int8_t* qX,
+                                          float* sX, void* workspace, size_t ws_bytes, void* stream);
+
+/* The norm, its codes and the 8-bit layer on them: Y [B S][ldy] = layer(norm(X)), layer->K == norm->C,
+ * smoothed by layer->inv_s.  Bit for bit the two calls svdq_group_norm_quantize_int8 and
+ * svdq_gemm_w8a8.  workspace >= svdq_norm_linear_int8_workspace_bytes, 256-byte aligned. */
+size_t svdq_norm_linear_int8_workspace_bytes(const svdq_group_norm_desc* norm, const svdq_int8_layer* layer,
+                                             int64_t B, int64_t S);
+svdq_status svdq_norm_linear_forward_int8(const svdq_group_norm_desc* norm, const svdq_int8_layer* layer, int64_t B,
+                                          int64_t S, const void* X, int32_t xdtype, int64_t bsx, int64_t ldx, void* Y,
+                                          int64_t ldy, int32_t ydtype, void* workspace, size_t ws_bytes,
+                                          void* stream);
+
 /* Diagnostic: the exact integer group sums I[g][m][n] = sum_{k in group g} qX[m][k]
  * qW[n][k] (INT4 only; the review's section 3 product Q_X Q_W, taken per group) for the
  * window rows [m0, m0+mt) x cols [n0, n0+nt).  out: device int32 [K/64][mt][nt].

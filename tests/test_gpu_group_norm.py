@@ -1,0 +1,241 @@
+"""GPU tests of the channels-last group norm and the norm into 8-bit codes, against oracle/int8.py (fp64).
+
+Bound of an output, derived (u = 2^-24).  Sums of n values run in chains of at most L additions (a block's positions
+per thread, then its threads, then the blocks: L = 400 covers every size here), so the group's mean is off by at most
+L u mean|x - pivot| <= 4 L u sigma and its variance by a relative 2 L u; with z = (x - mean) / sqrt(var + eps) that
+moves z by at most 4 L u + L u |z|, and the roundings of mean and x - mean by u (|x| + 2 |mean|) / sqrt(var + eps).
+Then 4 roundings of gamma z + beta; the activations' slope is at most 1.13, SiLU's own error at most 8 u (1 + |y|) of
+its value, GELU's 2e-5 of its value; bf16 adds half a step.
+"""
+import numpy as np
+import pytest
+
+from bit_diffusion_model_amd import svdq
+from oracle import int8 as o8
+from test_gpu_int8 import host
+
+pytestmark = pytest.mark.gpu
+U, L = 2.0 ** -24, 400
+ACTS = {"none": svdq.GN_NONE, "silu": svdq.GN_SILU, "gelu": svdq.GN_GELU}
+
+
+def _torch():
+    import torch
+
+    return torch
+
+
+def make_x(B, S, C, dtype, seed, pad=0, offset=0.0, rows_pad=0):
+    torch = _torch()
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((B, S, C)) * np.exp(0.5 * rng.standard_normal(C)) + rng.standard_normal(C) + offset
+    buf = torch.full((B, S + rows_pad, C + pad), 1e30, dtype=dtype, device="cuda:0")
+    buf[:, :S, :C] = torch.from_numpy(x.astype(np.float32)).to("cuda:0").to(dtype)
+    return buf[:, :S, :C]
+
+
+def affine(C, seed):
+    rng = np.random.default_rng(seed)
+    return (1 + 0.3 * rng.standard_normal(C)).astype(np.float32), (0.3 * rng.standard_normal(C)).astype(np.float32)
+
+
+def reference(x, G, gamma, beta, eps, act):
+    """(y, bound of its fp32 evaluation)."""
+    y, mean, var = o8.group_norm(x, G, gamma, beta, eps, act)
+    lin, _, _ = o8.group_norm(x, G, gamma, beta, eps, "none")
+    sd = np.sqrt(var + eps)
+    z = (x - mean) / sd
+    g = np.abs(np.ones(x.shape[-1]) if gamma is None else gamma.astype(np.float64))
+    b = np.abs(np.zeros(x.shape[-1]) if beta is None else beta.astype(np.float64))
+    dz = 4 * L * U + L * U * np.abs(z) + U * (np.abs(x) + 2 * np.abs(mean)) / sd
+    tol = 1.13 * (g * dz + 4 * U * (g * np.abs(z) + b))
+    tol += {"none": 0.0, "silu": 8 * U * (1 + np.abs(lin)) * np.abs(y), "gelu": 2e-5 * np.abs(y)}[act]
+    return y, tol
+
+
+# positions from 1 up, groups of 1 channel up, group sizes that no vector width divides, one group for all channels
+SHAPES = [(1, 1, 1, 1), (1, 1, 32, 64), (2, 3, 4, 8), (1, 5, 3, 9), (2, 64, 32, 1280), (1, 100, 32, 320), (3, 257, 8, 48),
+          (2, 1000, 32, 32), (1, 4096, 32, 320), (2, 1024, 32, 640), (1, 33, 1, 77), (4, 77, 7, 77), (1, 20, 32, 4096),
+          (1, 7, 32, 2560), (2, 2049, 16, 208), (1, 40000, 8, 64), (70, 9, 2, 16)]
+
+
+@pytest.mark.parametrize("B,S,G,C", SHAPES)
+@pytest.mark.parametrize("xd,yd,act", [("bf16", "bf16", "silu"), ("bf16", "f32", "none"), ("f32", "f32", "silu"),
+                                       ("f32", "f32", "gelu"), ("f32", "bf16", "none")])
+def test_group_norm(B, S, G, C, xd, yd, act):
+    torch = _torch()
+    X = make_x(B, S, C, {"bf16": torch.bfloat16, "f32": torch.float32}[xd], B + S + C)
+    gamma, beta = affine(C, C) if act != "none" else (None, None)
+    gn = svdq.GroupNorm(G, C, gamma, beta, 1e-5, ACTS[act])
+    Y = host(gn.forward(X, svdq.F32 if yd == "f32" else svdq.BF16))
+    ref, tol = reference(host(X), G, gamma, beta, 1e-5, act)
+    tol = tol + (2.0 ** -8 * np.abs(ref) if yd == "bf16" else 0.0) + 1e-37
+    err = np.abs(Y - ref)
+    assert (err <= tol).all(), f"worst {np.max(err / tol)} of the bound"
+
+
+@pytest.mark.parametrize("pad,rows_pad", [(8, 0), (1, 0), (3, 2), (0, 5), (16, 1)])
+@pytest.mark.parametrize("xd", ["bf16", "f32"])
+def test_strides(pad, rows_pad, xd):
+    """Positions and images further apart than their values, aligned for wide loads or not; Y strided too, or X itself."""
+    torch = _torch()
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[xd]
+    B, S, G, C = 3, 150, 8, 96
+    X = make_x(B, S, C, dt, 5, pad, rows_pad=rows_pad)
+    gamma, beta = affine(C, 2)
+    gn = svdq.GroupNorm(G, C, gamma, beta, 1e-6, svdq.GN_SILU)
+    ref = gn.forward(X.contiguous(), svdq.F32)
+    assert torch.allclose(gn.forward(X, svdq.F32), ref, rtol=0, atol=1e-5)
+    want, tol = reference(host(X), G, gamma, beta, 1e-6, "silu")
+    buf = torch.full((B, S, C + 4), 9.0, device="cuda:0")
+    Y = gn.forward(X, svdq.F32, out=buf[:, :, :C])
+    assert (buf[:, :, C:] == 9.0).all()
+    assert (np.abs(host(Y) - want) <= tol).all()
+    own = X.clone() if pad == 0 and rows_pad == 0 else X
+    gn.forward(own, svdq.F32 if xd == "f32" else svdq.BF16, out=own)
+    assert (np.abs(host(own) - want) <= tol + (0 if xd == "f32" else 2.0 ** -8 * np.abs(want))).all()
+
+
+def test_images_of_positions():
+    """[B][H][W][C], and a channels-last tensor seen as such."""
+    torch = _torch()
+    x = torch.randn(2, 64, 12, 10, device="cuda:0").to(memory_format=torch.channels_last)  # [B][C][H][W]
+    gn = svdq.GroupNorm(8, 64)
+    Y = gn.forward(x.permute(0, 2, 3, 1), svdq.F32)
+    ref, tol = reference(host(x.permute(0, 2, 3, 1).reshape(2, 120, 64)), 8, None, None, 1e-5, "none")
+    assert (np.abs(host(Y).reshape(2, 120, 64) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("S,C", [(64, 128), (5000, 64)])
+def test_large_mean(S, C):
+    """A mean far from zero costs no more than the rounding of x itself: no cancellation in the variance."""
+    torch = _torch()
+    X = make_x(2, S, C, torch.float32, 3, offset=3000.0)
+    gn = svdq.GroupNorm(8, C)
+    ref, tol = reference(host(X), 8, None, None, 1e-5, "none")
+    assert (np.abs(host(gn.forward(X, svdq.F32)) - ref) <= tol).all()
+
+
+def test_first_rows_unlike_the_rest():
+    """The first positions hold one value and outliers: the pivot they give must not spoil the variance."""
+    torch = _torch()
+    X = make_x(1, 6000, 64, torch.float32, 8)
+    X[:, :100] = 500.0
+    X[:, 0, ::3] = -4000.0
+    gn = svdq.GroupNorm(4, 64)
+    ref, tol = reference(host(X), 4, None, None, 1e-5, "none")
+    assert (np.abs(host(gn.forward(X, svdq.F32)) - ref) <= tol).all()
+
+
+def test_constant_and_non_finite_groups():
+    """A constant group gives beta; a NaN or an infinity makes its own group of its own image NaN and no other."""
+    torch = _torch()
+    for S in (16, 3000):
+        X = make_x(2, S, 64, torch.float32, 4)
+        X[0, :, :8] = 7.25
+        X[1, 3, 9] = float("nan")
+        X[0, S - 1, 63] = float("inf")
+        gamma, beta = affine(64, 1)
+        Y = host(svdq.GroupNorm(8, 64, gamma, beta).forward(X, svdq.F32))
+        np.testing.assert_allclose(Y[0, :, :8], np.broadcast_to(beta[:8], (S, 8)), rtol=1e-6)
+        bad = np.zeros((2, S, 64), bool)
+        bad[1, :, 8:16] = True
+        bad[0, :, 56:] = True
+        assert np.isnan(Y[bad]).all() and np.isfinite(Y[~bad]).all()
+
+
+@pytest.mark.parametrize("B,S,G,C", SHAPES)
+@pytest.mark.parametrize("xd,act,smooth,pad", [("bf16", "silu", True, 0), ("f32", "none", False, 3), ("bf16", "gelu", True, 8)])
+def test_norm_quantize(B, S, G, C, xd, act, smooth, pad):
+    """Codes and scales of the norm: the scale within the norm's bound, the codes within the half step that they
+    stand for plus the norm's bound (a value near a tie may take either code)."""
+    torch = _torch()
+    X = make_x(B, S, C, {"bf16": torch.bfloat16, "f32": torch.float32}[xd], B + S + C + 1, pad)
+    gamma, beta = affine(C, C + 1)
+    inv = (0.3 + np.random.default_rng(C).random(C)).astype(np.float32) if smooth else None
+    gn = svdq.GroupNorm(G, C, gamma, beta, 1e-5, ACTS[act])
+    qX, sX = gn.quantize(X, None if inv is None else torch.from_numpy(inv).to("cuda:0"))
+    q, s = qX.cpu().numpy(), sX.cpu().numpy().astype(np.float64)
+    assert (q[:, C:] == 0).all()
+    y, tol = reference(host(X), G, gamma, beta, 1e-5, act)
+    f = 1.0 if inv is None else inv.astype(np.float64)
+    y, tol = (y * f).reshape(B * S, C), (tol * f + U * np.abs(y * f)).reshape(B * S, C)
+    a = np.maximum(np.abs(y).max(axis=1), o8.FLOOR)
+    da = tol.max(axis=1)
+    assert (np.abs(s - a / 127) <= da / 127 + U * a / 127).all()
+    step = s[:, None]
+    assert (np.abs(q[:, :C] * step - y) <= step * (0.5 + 127 * 4 * U) + tol).all()
+
+
+def test_norm_linear():
+    """The norm with the layer equals the two calls, and the oracle within 8 bits' flips of a code."""
+    torch = _torch()
+    rng = np.random.default_rng(2)
+    for B, S, G, C, N in [(2, 64, 32, 320, 200), (1, 1000, 8, 72, 130), (1, 1, 4, 16, 9), (2, 8, 32, 1280, 320)]:
+        X = make_x(B, S, C, torch.bfloat16, 6)
+        gamma, beta = affine(C, 3)
+        gn = svdq.GroupNorm(G, C, gamma, beta, 1e-5, svdq.GN_SILU)
+        W = (rng.standard_normal((C, N)) / np.sqrt(C)).astype(np.float32)
+        Wb = ((W.view(np.uint32) + 0x8000) >> 16).astype(np.uint16)
+        amax = (1 + rng.random(C)).astype(np.float32)
+        lin = svdq.Int8Linear.from_weights(Wb, amax, 0.5, bias=rng.standard_normal(N).astype(np.float32))
+        Y = gn.forward_linear(X, lin, svdq.F32)
+        q, s = gn.quantize(X, lin.inv_s)
+        assert torch.equal(Y, lin.gemm(q, s))
+        p = o8.product(q.cpu().numpy()[:, :C], s.cpu().numpy(), lin.qW.cpu().numpy()[:, :C], lin.sW.cpu().numpy())
+        b = lin.bias.cpu().numpy().astype(np.float64)
+        assert (np.abs(host(Y) - p - b) <= 5 * U * (np.abs(p) + np.abs(b)) + 1e-37).all()
+
+
+def test_empty_streams_and_repeats():
+    torch = _torch()
+    gn = svdq.GroupNorm(8, 64, act=svdq.GN_SILU)
+    assert gn.forward(torch.empty((0, 5, 64), device="cuda:0")).shape == (0, 5, 64)
+    assert gn.forward(torch.empty((3, 0, 64), device="cuda:0")).shape == (3, 0, 64)
+    X = make_x(2, 3000, 64, torch.bfloat16, 9)
+    ref = gn.forward(X)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        Y = gn.forward(X)
+    s.synchronize()
+    assert torch.equal(Y, ref) and torch.equal(gn.forward(X), ref)
+
+
+def test_in_a_graph():
+    torch = _torch()
+    gn = svdq.GroupNorm(32, 320, act=svdq.GN_SILU)
+    for S in (64, 3000):
+        X = make_x(2, S, 320, torch.bfloat16, 1)
+        ws, out = gn.workspace(2, S, X.device), torch.empty_like(X)
+        gn.forward(X, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            gn.forward(X, out=out, workspace=ws)
+        for k in range(4):
+            X.copy_(make_x(2, S, 320, torch.bfloat16, 20 + k))
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, gn.forward(X)), (S, k)
+
+
+def test_refusals():
+    torch = _torch()
+    gn = svdq.GroupNorm(8, 64)
+    X = make_x(2, 10, 64, torch.float32, 1)
+    for bad in (X[..., :63], X.half(), X.permute(0, 2, 1), X[0, 0], X.cpu(), X[:, :1].expand(2, 10, 64)):
+        with pytest.raises(svdq.SvdqError):
+            gn.forward(bad)
+    with pytest.raises(svdq.SvdqError):
+        gn.forward(X, svdq.BF16_GELU)
+    with pytest.raises(svdq.SvdqError):
+        gn.forward(X, out=torch.empty((2, 10, 63), device="cuda:0"))
+    with pytest.raises(svdq.SvdqError):
+        gn.forward(X, workspace=torch.empty(8, dtype=torch.uint8, device="cuda:0"))
+    with pytest.raises(svdq.SvdqError):
+        svdq.GroupNorm(7, 64).forward(X)
+    with pytest.raises(svdq.SvdqError):
+        svdq.GroupNorm(8, 64, eps=0.0).forward(X)
+    with pytest.raises(svdq.SvdqError):
+        gn.forward_linear(X, svdq.Int8Linear(np.zeros((4, 128), np.int8), np.ones(4, np.float32), 65))
