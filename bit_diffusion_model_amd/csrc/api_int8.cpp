@@ -112,7 +112,7 @@ svdq_status run_gemm(const svdq_int8_layer* L, int64_t M, const int8_t* qX, cons
                      int32_t ydtype, void* ws, size_t ws_bytes, void* stream) {
   svdq_status st = check_codes(qX, sX);
   if (st != SVDQ_OK || (st = check_out(Y, ldy, L->N, ydtype)) != SVDQ_OK) return st;
-  hipError_t e = launch_w8a8(M, L->K, L->N, qX, sX, L->qW, L->sW, L->bias, Y, ldy, ydtype, (hipStream_t)stream);
+  hipError_t e = launch_w8a8(M, L->K, L->N, qX, sX, L->qW, L->sW, L->bias, Y, ldy, ydtype, ws, (hipStream_t)stream);
   if (e != hipSuccess) return fail(SVDQ_EHIP, "W8A8 product launch: %s", hipGetErrorString(e));
   return ok();
 }
@@ -125,12 +125,13 @@ using namespace svdq;
 extern "C" {
 
 size_t svdq_gemm_w8a8_workspace_bytes(const svdq_int8_layer* layer, int64_t M) {
-  (void)layer, (void)M;
-  return 0;
+  if (M < 1 || check_dims_int8(layer) != SVDQ_OK || check_rows(M) != SVDQ_OK) return 0;
+  return rup(plan_w8a8(M, layer->K, layer->N).bytes);
 }
 
-size_t svdq_int8_workspace_bytes(const svdq_int8_layer* layer, int64_t M) {
-  if (M < 1 || check_dims_int8(layer) != SVDQ_OK || check_rows(M) != SVDQ_OK) return 0;
+size_t svdq_int8_workspace_bytes(const svdq_int8_layer* layer, int64_t M, int32_t xdtype) {
+  if (M < 1 || check_dims_int8(layer) != SVDQ_OK || check_rows(M) != SVDQ_OK || check_xdtype(xdtype) != SVDQ_OK) return 0;
+  if (few_layer(M, layer->K)) return 0;
   return act_bytes(M, layer->K) + svdq_gemm_w8a8_workspace_bytes(layer, M);
 }
 
@@ -162,12 +163,19 @@ svdq_status svdq_linear_forward_int8(const svdq_int8_layer* layer, int64_t M, co
   if (st != SVDQ_OK || (st = check_rows(M)) != SVDQ_OK) return st;
   if (M == 0) return ok();
   if ((st = check_in(X, xdtype, ldx, layer->K)) != SVDQ_OK || (st = check_out(Y, ldy, layer->N, ydtype)) != SVDQ_OK) return st;
-  if ((st = check_ws(workspace, ws_bytes, svdq_int8_workspace_bytes(layer, M))) != SVDQ_OK) return st;
+  if ((st = check_ws(workspace, ws_bytes, svdq_int8_workspace_bytes(layer, M, xdtype))) != SVDQ_OK) return st;
+  hipError_t e;
+  if (few_layer(M, layer->K)) {
+    e = launch_few_layer(M, layer->K, layer->N, X, xdtype, ldx, layer->inv_s, layer->qW, layer->sW, layer->bias, Y, ldy,
+                         ydtype, (hipStream_t)stream);
+    if (e != hipSuccess) return fail(SVDQ_EHIP, "8-bit layer launch: %s", hipGetErrorString(e));
+    return ok();
+  }
   uint8_t* base = static_cast<uint8_t*>(workspace);
   int8_t* qX = reinterpret_cast<int8_t*>(base);
   float* sX = reinterpret_cast<float*>(base + rup((size_t)M * (size_t)i8_ld(layer->K)));
   const size_t used = act_bytes(M, layer->K);
-  hipError_t e = launch_quant_i8(M, layer->K, X, xdtype, ldx, layer->inv_s, qX, sX, (hipStream_t)stream);
+  e = launch_quant_i8(M, layer->K, X, xdtype, ldx, layer->inv_s, qX, sX, (hipStream_t)stream);
   if (e != hipSuccess) return fail(SVDQ_EHIP, "8-bit quantizer launch: %s", hipGetErrorString(e));
   return run_gemm(layer, M, qX, sX, Y, ldy, ydtype, base + used, ws_bytes - used, stream);
 }
@@ -214,7 +222,7 @@ size_t svdq_norm_linear_int8_workspace_bytes(const svdq_group_norm_desc* norm, c
                                              int64_t B, int64_t S) {
   const size_t n = svdq_group_norm_workspace_bytes(norm, B, S);
   if (n == 0 || check_dims_int8(layer) != SVDQ_OK || layer->K != norm->C) return 0;
-  return n + svdq_int8_workspace_bytes(layer, B * S);
+  return n + act_bytes(B * S, layer->K) + svdq_gemm_w8a8_workspace_bytes(layer, B * S);
 }
 
 svdq_status svdq_norm_linear_forward_int8(const svdq_group_norm_desc* norm, const svdq_int8_layer* layer, int64_t B,

@@ -9,34 +9,64 @@
 
 namespace svdq {
 
-// Eight consecutive values k .. k+7 of a row as fp32; values at or past K are 0.  VEC: the
-// row is 16-byte aligned at k (two 16-byte loads for fp32, one for bf16).
-template <typename T>
-__device__ __forceinline__ float load1(const T* p);
-template <>
-__device__ __forceinline__ float load1<float>(const float* p) { return *p; }
-template <>
-__device__ __forceinline__ float load1<uint16_t>(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
-
-__device__ __forceinline__ void load8_vec(const uint16_t* p, float v[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  v[0] = bf16_lo_to_f32(w.x), v[1] = bf16_hi_to_f32(w.x), v[2] = bf16_lo_to_f32(w.y), v[3] = bf16_hi_to_f32(w.y);
-  v[4] = bf16_lo_to_f32(w.z), v[5] = bf16_hi_to_f32(w.z), v[6] = bf16_lo_to_f32(w.w), v[7] = bf16_hi_to_f32(w.w);
-}
-__device__ __forceinline__ void load8_vec(const float* p, float v[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-
+// Row reads without branches, so that all of a row's loads can be issued before the first is
+// waited for.  A Row covers K values from p; load(k) starts the read of values k .. k+7 and
+// value() turns it into fp32; what lies at or past K reads as 0 (the buffer's range).
+// VEC: p is 4-byte aligned (16-byte loads need no more); otherwise bf16 values are loaded one by one.
+// The range of an odd number of bf16 values ends in the middle of a word whose first half
+// is the row's, and value() drops the second half.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, int64_t k, int64_t K, float v[8]) {
-  if (VEC && k + 8 <= K) {
-    load8_vec(row + k, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = k + e < K ? load1(row + k + e) : 0.0f;
+struct Row;
+
+template <bool VEC>
+struct Row<float, VEC> {
+  typedef struct { uint4 a, b; } Raw;
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Row(const float* p, int K) : r(make_rsrc(p, (uint32_t)K * 4)) {}
+  __device__ __forceinline__ Raw load(int k) const {
+    return Raw{buf_load16(r, (uint32_t)k * 4), buf_load16(r, (uint32_t)k * 4 + 16)};
   }
-}
+  __device__ __forceinline__ void value(const Raw& w, int, float v[8]) const {
+    v[0] = __uint_as_float(w.a.x), v[1] = __uint_as_float(w.a.y), v[2] = __uint_as_float(w.a.z), v[3] = __uint_as_float(w.a.w);
+    v[4] = __uint_as_float(w.b.x), v[5] = __uint_as_float(w.b.y), v[6] = __uint_as_float(w.b.z), v[7] = __uint_as_float(w.b.w);
+  }
+};
+
+template <>
+struct Row<uint16_t, true> {
+  typedef uint4 Raw;
+  __amdgpu_buffer_rsrc_t r;
+  int odd_end;  // K if K is odd, else past every k
+  __device__ __forceinline__ Row(const uint16_t* p, int K)
+      : r(make_rsrc(p, ((uint32_t)K + 1) / 2 * 4)), odd_end(K & 1 ? K : 0x7FFFFFFF) {}
+  __device__ __forceinline__ Raw load(int k) const { return buf_load16(r, (uint32_t)k * 2); }
+  __device__ __forceinline__ void value(const Raw& w, int k, float v[8]) const {
+    v[0] = bf16_lo_to_f32(w.x), v[1] = bf16_hi_to_f32(w.x), v[2] = bf16_lo_to_f32(w.y), v[3] = bf16_hi_to_f32(w.y);
+    v[4] = bf16_lo_to_f32(w.z), v[5] = bf16_hi_to_f32(w.z), v[6] = bf16_lo_to_f32(w.w), v[7] = bf16_hi_to_f32(w.w);
+    if (odd_end != 0x7FFFFFFF) {
+#pragma unroll
+      for (int e = 1; e < 8; e += 2)
+        if (k + e == odd_end) v[e] = 0.0f;
+    }
+  }
+};
+
+template <>
+struct Row<uint16_t, false> {
+  typedef struct { uint32_t h[8]; } Raw;
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Row(const uint16_t* p, int K) : r(make_rsrc(p, (uint32_t)K * 2)) {}
+  __device__ __forceinline__ Raw load(int k) const {
+    Raw w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w.h[e] = buf_load2(r, (uint32_t)(k + e) * 2);
+    return w;
+  }
+  __device__ __forceinline__ void value(const Raw& w, int, float v[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w.h[e] << 16);
+  }
+};
 
 // Magnitudes are compared as unsigned bit patterns: their order is the order of the values,
 // and a NaN or an infinity (0x7F800000 and above) is larger than every finite value.

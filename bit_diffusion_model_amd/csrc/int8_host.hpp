@@ -12,4 +12,9 @@ constexpr int64_t kMaxInt8K = 131072;
 // the norm keeps per-channel values of a row in LDS
 constexpr int64_t kMaxNormC = 4096;
 
+// Whether every row (from p, ld values apart; xdtype 0 fp32, 1 bf16) is 4-byte aligned.
+inline bool rows_aligned4(const void* p, int64_t ld, int xdtype) {
+  return reinterpret_cast<uintptr_t>(p) % 4 == 0 && (xdtype == 0 || ld % 2 == 0);
+}
+
 }  // namespace svdq

@@ -4,8 +4,8 @@
 // a = max(max_k |v_k|, 2^-96); s = a / 127; r = 127 / a; q_k = round_half_even(v_k r).
 //
 // Design (gfx950): bound by HBM (x read once, a byte per value written).  A row stays in
-// registers between the maximum and the codes, so x is read once: one wave per row up to
-// 4096 values (8 per lane and 16-byte load, up to 8 loads in flight), four waves per row
+// registers between the maximum and the codes, so x is read once, all of its loads in
+// flight together: one wave per row up to 1024 values (8 per lane and load), four waves per row
 // up to 16384; longer rows are read twice (the second time from L2).
 #include "int8.hpp"
 #include "kernels.hpp"
@@ -16,26 +16,28 @@ namespace {
 constexpr int Q_NT = 256;
 
 // WPR waves per row, NC chunks of 8 values per lane (NC = 0: any length, read twice)
-template <typename T, bool VEC, int WPR, int NC>
-__global__ __launch_bounds__(Q_NT) void k5_quant(const T* __restrict__ X, int64_t ldx, int64_t M, int64_t K,
-                                                 const float* __restrict__ inv_s, int8_t* __restrict__ qX, int64_t ldq,
+template <typename T, bool VEC, bool SMOOTH, int WPR, int NC>
+__global__ __launch_bounds__(Q_NT) void k5_quant(const T* __restrict__ X, int64_t ldx, int64_t M, int K,
+                                                 const float* __restrict__ inv_s, int8_t* __restrict__ qX, int ldq,
                                                  float* __restrict__ sX) {
   __shared__ uint32_t part[4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row = (int64_t)blockIdx.x * (4 / WPR) + wave / WPR;
   if (WPR == 1 && row >= M) return;  // WPR == 4: one row per block, the grid has M blocks
-  const T* x = X + row * ldx;
+  typedef Row<T, VEC> RowX;
+  typedef Row<float, true> RowS;
+  const RowX x(X + row * ldx, K);
+  const RowS f(inv_s, SMOOTH ? K : 0);
   int8_t* q = qX + row * ldq;
   const int li = (wave % WPR) * 64 + lane;
   constexpr int STEP = 8 * 64 * WPR;
 
-  auto smoothed = [&](int64_t k, float v[8]) {
-    load8<T, VEC>(x, k, K, v);
-    if (inv_s) {
-      float f[8];
-      load8<float, true>(inv_s, k, K, f);
+  auto smooth = [&](const typename RowS::Raw& w, int k, float v[8]) {
+    if constexpr (SMOOTH) {
+      float s[8];
+      f.value(w, k, s);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= f[e];
+      for (int e = 0; e < 8; ++e) v[e] *= s[e];
     }
   };
   auto amax8 = [](const float v[8], uint32_t a) {
@@ -52,7 +54,7 @@ __global__ __launch_bounds__(Q_NT) void k5_quant(const T* __restrict__ X, int64_
     }
     return a;
   };
-  auto store8 = [&](int64_t k, const float v[8], float r) {
+  auto store8 = [&](int k, const float v[8], float r) {
     if (k < ldq)
       *reinterpret_cast<uint2*>(q + k) = make_uint2(codes4(v[0], v[1], v[2], v[3], r), codes4(v[4], v[5], v[6], v[7], r));
   };
@@ -60,57 +62,74 @@ __global__ __launch_bounds__(Q_NT) void k5_quant(const T* __restrict__ X, int64_
   uint32_t a = 0;
   float s, r;
   if constexpr (NC > 0) {
+    typename RowX::Raw w[NC];
+    typename RowS::Raw u[SMOOTH ? NC : 1];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) w[j] = x.load(8 * li + j * STEP);
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      if (SMOOTH) u[j] = f.load(8 * li + j * STEP);
     float v[NC][8];
 #pragma unroll
-    for (int j = 0; j < NC; ++j) smoothed(8 * li + j * STEP, v[j]);
-#pragma unroll
-    for (int j = 0; j < NC; ++j) a = amax8(v[j], a);
+    for (int j = 0; j < NC; ++j) {
+      x.value(w[j], 8 * li + j * STEP, v[j]);
+      smooth(u[SMOOTH ? j : 0], 8 * li + j * STEP, v[j]);
+      a = amax8(v[j], a);
+    }
     row_scale(row_max(a), s, r);
 #pragma unroll
     for (int j = 0; j < NC; ++j) store8(8 * li + j * STEP, v[j], r);
   } else {
-    for (int64_t k = 8 * li; k < K; k += STEP) {
+    auto at = [&](int k, float v[8]) {
+      const auto w = x.load(k);
+      typename RowS::Raw u = {};
+      if (SMOOTH) u = f.load(k);
+      x.value(w, k, v);
+      smooth(u, k, v);
+    };
+    for (int k = 8 * li; k < K; k += STEP) {
       float v[8];
-      smoothed(k, v);
+      at(k, v);
       a = amax8(v, a);
     }
     row_scale(row_max(a), s, r);
-    for (int64_t k = 8 * li; k < ldq; k += STEP) {
+    for (int k = 8 * li; k < ldq; k += STEP) {
       float v[8];
-      smoothed(k, v);
+      at(k, v);
       store8(k, v, r);
     }
   }
   if (li == 0) sX[row] = s;
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool SMOOTH>
 void launch(int64_t M, int64_t K, const T* X, int64_t ldx, const float* inv_s, int8_t* qX, float* sX, hipStream_t st) {
-  const int64_t ldq = i8_ld(K);
-  const dim3 g4((uint32_t)((M + 3) / 4)), g1((uint32_t)M), b(Q_NT);
-  if (ldq <= 512) hipLaunchKernelGGL((k5_quant<T, VEC, 1, 1>), g4, b, 0, st, X, ldx, M, K, inv_s, qX, ldq, sX);
-  else if (ldq <= 1024) hipLaunchKernelGGL((k5_quant<T, VEC, 1, 2>), g4, b, 0, st, X, ldx, M, K, inv_s, qX, ldq, sX);
-  else if (ldq <= 2048) hipLaunchKernelGGL((k5_quant<T, VEC, 1, 4>), g4, b, 0, st, X, ldx, M, K, inv_s, qX, ldq, sX);
-  else if (ldq <= 4096) hipLaunchKernelGGL((k5_quant<T, VEC, 1, 8>), g4, b, 0, st, X, ldx, M, K, inv_s, qX, ldq, sX);
-  else if (ldq <= 8192) hipLaunchKernelGGL((k5_quant<T, VEC, 4, 4>), g1, b, 0, st, X, ldx, M, K, inv_s, qX, ldq, sX);
-  else if (ldq <= 16384) hipLaunchKernelGGL((k5_quant<T, VEC, 4, 8>), g1, b, 0, st, X, ldx, M, K, inv_s, qX, ldq, sX);
-  else hipLaunchKernelGGL((k5_quant<T, VEC, 4, 0>), g1, b, 0, st, X, ldx, M, K, inv_s, qX, ldq, sX);
+  const int ldq = (int)i8_ld(K);
+  auto go = [&](auto kernel, int64_t blocks) {
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)blocks), dim3(Q_NT), 0, st, X, ldx, M, (int)K, inv_s, qX, ldq, sX);
+  };
+  if (ldq <= 512) go(k5_quant<T, VEC, SMOOTH, 1, 1>, (M + 3) / 4);
+  else if (ldq <= 1024) go(k5_quant<T, VEC, SMOOTH, 1, 2>, (M + 3) / 4);
+  else if (ldq <= 2048) go(k5_quant<T, VEC, SMOOTH, 4, 1>, M);
+  else if (ldq <= 4096) go(k5_quant<T, VEC, SMOOTH, 4, 2>, M);
+  else if (ldq <= 8192) go(k5_quant<T, VEC, SMOOTH, 4, 4>, M);
+  else if (ldq <= 16384) go(k5_quant<T, VEC, SMOOTH, 4, 8>, M);
+  else go(k5_quant<T, VEC, SMOOTH, 4, 0>, M);
+}
+
+template <typename T, bool VEC>
+void launch_any(int64_t M, int64_t K, const void* X, int64_t ldx, const float* inv_s, int8_t* qX, float* sX, hipStream_t st) {
+  const T* x = static_cast<const T*>(X);
+  inv_s ? launch<T, VEC, true>(M, K, x, ldx, inv_s, qX, sX, st) : launch<T, VEC, false>(M, K, x, ldx, inv_s, qX, sX, st);
 }
 
 }  // namespace
 
 hipError_t launch_quant_i8(int64_t M, int64_t K, const void* X, int xdtype, int64_t ldx, const float* inv_s, int8_t* qX,
                            float* sX, hipStream_t st) {
-  // 16-byte loads need every row 16-byte aligned; other rows are loaded value by value
-  const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % (xdtype == 0 ? 4 : 8) == 0;
-  if (xdtype == 0) {
-    const float* x = static_cast<const float*>(X);
-    vec ? launch<float, true>(M, K, x, ldx, inv_s, qX, sX, st) : launch<float, false>(M, K, x, ldx, inv_s, qX, sX, st);
-  } else {
-    const uint16_t* x = static_cast<const uint16_t*>(X);
-    vec ? launch<uint16_t, true>(M, K, x, ldx, inv_s, qX, sX, st)
-        : launch<uint16_t, false>(M, K, x, ldx, inv_s, qX, sX, st);
-  }
+  if (xdtype == 0) launch_any<float, true>(M, K, X, ldx, inv_s, qX, sX, st);
+  else if (rows_aligned4(X, ldx, xdtype)) launch_any<uint16_t, true>(M, K, X, ldx, inv_s, qX, sX, st);
+  else launch_any<uint16_t, false>(M, K, X, ldx, inv_s, qX, sX, st);
   return hipGetLastError();
 }
 

@@ -2,14 +2,12 @@
 //
 // Mathematics: I[m][n] = sum_k qX[m][k] qW[n][k], exact in 32-bit integers (K <= 131072:
 // 127^2 K < 2^31); y = ((float)I s_X[m]) s_W[n] + bias[n], in fp32, then optionally GELU,
-// rounded once to the output type.
-//
-// Design (gfx950): v_mfma_i32_32x32x32_i8; a block of 4 waves owns a 64 x 64 tile of Y
-// (one 32 x 32 accumulator per wave) and walks K in stages of 128 bytes; both operands
-// go global -> LDS by LDS-destination buffer loads, one stage ahead, into two buffers, the
-// 16-byte slots of a row XOR-swizzled so that the operand reads of 16 consecutive rows
-// fall in distinct bank groups.  Rows past M and channels past N lie beyond the buffers'
-// ranges: they read as zeros and are not stored.
+// rounded once to the output type.  qX comes as rows of ld bytes; qW in the fragment order of
+// svdq_prepare_weights_int8: [N / 16][ld / 64] fragments of 1 KB, lane l of a fragment holding
+// channel l & 15 and the 16 codes k = 16 (l >> 4) .., N padded to 16 with zeros.  Integer sums do not depend on their order, so tiles,
+// K ranges and kernels may be chosen freely: every choice gives the same bits.
+#include <type_traits>
+
 #include "int8.hpp"
 #include "kernels.hpp"
 
@@ -31,43 +29,145 @@ __device__ __forceinline__ void wait_vm_lgkm0() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
 
-// TI x TJ accumulators of 32 x 32 per wave, WM x WN waves
-template <int WM, int WN, int TI, int TJ>
-__global__ __launch_bounds__(64 * WM * WN) void k6_gemm(const int8_t* __restrict__ qX, int64_t ld, int64_t M,
-                                                        const int8_t* __restrict__ qW, int64_t N,
-                                                        const float* __restrict__ sX, const float* __restrict__ sW,
-                                                        const float* __restrict__ bias, void* __restrict__ Y,
-                                                        int64_t ldy, int ydtype, uint32_t tiles_n) {
-  constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN, NW = WM * WN;
-  constexpr int AB = BM * 128, BB = BN * 128;
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  const b2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+struct Out {
+  const float *sX, *sW, *bias;
+  void* Y;
+  int64_t ldy, M, N;
+  int ydtype;
+  bool wide;  // Y's rows are 16-byte aligned
+};
+
+__device__ __forceinline__ void store1(const Out& o, int64_t m, int64_t n, float y) {
+  if (o.ydtype == 0) static_cast<float*>(o.Y)[m * o.ldy + n] = y;
+  else static_cast<__bf16*>(o.Y)[m * o.ldy + n] = (__bf16)(o.ydtype == 2 ? gelu_erf(y) : y);
+}
+
+// Eight outputs n .. n+7 (n a multiple of 8) of row m from their integer sums; sw, bb: those
+// channels' scales and biases, sx the row's scale.
+__device__ __forceinline__ void store8(const Out& o, int64_t m, int64_t n, const int I[8], float sx, const float sw[8],
+                                       const float bb[8]) {
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    y[e] = (float)I[e] * sx * sw[e];
+    if (o.bias) y[e] += bb[e];
+  }
+  if (o.wide && n + 8 <= o.N) {
+    if (o.ydtype == 0) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(o.Y) + m * o.ldy + n);
+      p[0] = make_float4(y[0], y[1], y[2], y[3]);
+      p[1] = make_float4(y[4], y[5], y[6], y[7]);
+    } else {
+      if (o.ydtype == 2) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = gelu_erf(y[e]);
+      }
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.Y) + m * o.ldy + n) =
+          make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]), bf16_pair(y[4], y[5]), bf16_pair(y[6], y[7]));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (n + e < o.N) store1(o, m, n + e, y[e]);
+  }
+}
+
+__device__ __forceinline__ void load_channels(const Out& o, int64_t n, float sw[8], float bb[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    sw[e] = n + e < o.N ? o.sW[n + e] : 0.0f;
+    bb[e] = o.bias && n + e < o.N ? o.bias[n + e] : 0.0f;
+  }
+}
+
+// ---- tiles: v_mfma_i32_32x32x32_i8, both operands through LDS
+//
+// A block owns BM x BN outputs, WM x WN waves with TI x TJ accumulators of 32 x 32 each, and
+// walks K in stages of 128 bytes.  KG K groups of such waves (where there are fewer tiles than
+// compute units) take the stages in turn, each with its own buffers, and meet in the epilogue.  Both operands go global -> LDS by LDS-destination
+// buffer loads into two buffers: the weights in their fragment order, whose reads are
+// contiguous; a token row's eight 16-byte slots XOR-swizzled by the row so that the operand
+// reads of 16 consecutive rows fall in distinct bank groups.  A stage has
+// four steps of 32 bytes of K; a step's operands are read into registers during the step
+// before it.  The one barrier of a stage lies before its last step: by then every wave
+// has read the whole buffer (its last step waits in registers), so the loads of stage k+2
+// can go into it, a whole stage ahead of their use, and the next stage's first
+// operands are read under the last step's MFMAs.
+// Rows past M and channel blocks past N lie beyond the buffers' ranges: they read as zeros
+// and are not stored.  Blocks are numbered so that each XCD (own L2; blocks go to the eight XCDs in
+// turn) gets a contiguous run of tiles in strips of 8 tile rows, whose operand panels it
+// then shares.
+// P > 1 parts: blockIdx.y takes a range of the stages and stores raw sums to part[y].
+// Outputs leave through a wave-private LDS strip of 32 rows, so that stores are whole
+// 16-byte pieces of consecutive columns.
+template <int WM, int WN, int TI, int TJ, int KG>
+__global__ __launch_bounds__(64 * WM * WN * KG) void k6_tiles(const int8_t* __restrict__ qX, int64_t ld,
+                                                         const int8_t* __restrict__ qW, Out o, uint32_t tiles_m,
+                                                         uint32_t tiles_n, int* __restrict__ part, int64_t ldp) {
+  constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN, NW = WM * WN;  // NW waves per K group
+  constexpr int AB = BM * 128, BB = BN * 128, NA = AB / 1024 / NW, NB = BB / 1024 / NW, NL = NA + NB;
   static_assert(AB % (1024 * NW) == 0 && BB % (1024 * NW) == 0, "whole 1 KB loads per wave");
-  constexpr int NA = AB / 1024 / NW, NB = BB / 1024 / NW;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * (AB + BB)];
+  // separate arrays, addressed statically: the compiler then knows that operand reads do not
+  // touch the buffer whose loads are in flight, and does not wait for them
+  __shared__ __attribute__((aligned(1024))) uint8_t la0[KG * AB];
+  __shared__ __attribute__((aligned(1024))) uint8_t la1[KG * AB];
+  __shared__ __attribute__((aligned(1024))) uint8_t lb0[KG * BB];
+  __shared__ __attribute__((aligned(1024))) uint8_t lb1[KG * BB];
+  __shared__ float lsx[BM], lsw[BN], lbb[BN];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6), wave = wid % NW, g = wid / NW;
   const int l32 = lane & 31, kh = lane >> 5;
   const int wr = (wave / WN) * 32 * TI, wc = (wave % WN) * 32 * TJ;
-  const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * BM, n0 = (int64_t)(blockIdx.x % tiles_n) * BN;
-  const uint32_t rows = (uint32_t)(M - m0 < BM ? M - m0 : BM), cols = (uint32_t)(N - n0 < BN ? N - n0 : BN);
-  const int nst = (int)(ld / 128);
-  const __amdgpu_buffer_rsrc_t rA = make_rsrc(qX + m0 * ld, rows * (uint32_t)ld);
-  const __amdgpu_buffer_rsrc_t rB = make_rsrc(qW + n0 * ld, cols * (uint32_t)ld);
+
+  const uint32_t T = tiles_m * tiles_n, xcd = blockIdx.x & 7, t8 = T >> 3, r8 = T & 7;
+  const uint32_t t = xcd * t8 + (xcd < r8 ? xcd : r8) + (blockIdx.x >> 3);
+  constexpr uint32_t GM = 8;
+  const uint32_t grp = t / (GM * tiles_n), fm = grp * GM, gs = tiles_m - fm < GM ? tiles_m - fm : GM;
+  const uint32_t in = t - grp * GM * tiles_n;
+  const int64_t m0 = (int64_t)(fm + in % gs) * BM, n0 = (int64_t)(in / gs) * BN;
+
+  const uint32_t rows = (uint32_t)(o.M - m0 < BM ? o.M - m0 : BM), cols = (uint32_t)(o.N - n0 < BN ? o.N - n0 : BN);
+  const uint32_t blocks = (cols + 15) / 16;  // channel blocks of 16 (the last one zero past N)
+  const int all = (int)(ld / 128), per = (all + (int)gridDim.y - 1) / (int)gridDim.y;
+  const int s0 = (int)blockIdx.y * per, nst = all - s0 < per ? all - s0 : per;  // this part's stages (>= 1)
+  const int turns = (nst + KG - 1) / KG;  // stages per K group: group g takes g, g + KG, ..
   uint32_t va[NA], vb[NB];
+#pragma unroll
+  for (int q = 0; q < NB; ++q) {
+    const uint32_t f = wave + NW * q;  // fragment f & 1 of the stage of channel block f >> 1
+    vb[q] = (uint32_t)lane * 16 + (f >> 1) * 16 * (uint32_t)ld + (f & 1) * 1024;
+  }
 #pragma unroll
   for (int q = 0; q < NA; ++q) {
     const int row = (wave + NW * q) * 8 + (lane >> 3);
     va[q] = (uint32_t)row * (uint32_t)ld + (uint32_t)(((lane & 7) ^ swz8(row)) * 16);
   }
-#pragma unroll
-  for (int q = 0; q < NB; ++q) {
-    const int row = (wave + NW * q) * 8 + (lane >> 3);
-    vb[q] = (uint32_t)row * (uint32_t)ld + (uint32_t)(((lane & 7) ^ swz8(row)) * 16);
+  // the tile's scales and biases (a global load in the epilogue would be waited for there)
+  if (!part) {
+    for (int i = tid; i < BM; i += 64 * NW * KG) lsx[i] = i < (int)rows ? o.sX[m0 + i] : 0.0f;
+    for (int i = tid; i < BN; i += 64 * NW * KG) {
+      lsw[i] = i < (int)cols ? o.sW[n0 + i] : 0.0f;
+      lbb[i] = o.bias && i < (int)cols ? o.bias[n0 + i] : 0.0f;
+    }
   }
-  auto issue = [&](int k, uint8_t* buf) {
+  // past the end the buffers have no range: nothing is read and the LDS gets zeros
+  auto issue = [&](int k, uint8_t* a, uint8_t* b) {
+    const int s = k * KG + g;
+    const uint32_t on = s < nst ? 0xFFFFFFFFu : 0u;
+    const __amdgpu_buffer_rsrc_t rA = make_rsrc(qX + m0 * ld, (rows * (uint32_t)ld) & on);
+    const __amdgpu_buffer_rsrc_t rB = make_rsrc(qW + n0 * ld, (blocks * 16 * (uint32_t)ld) & on);
 #pragma unroll
-    for (int q = 0; q < NA; ++q) dma16(rA, buf + (wave + NW * q) * 1024, va[q], (uint32_t)k * 128);
+    for (int q = 0; q < NA; ++q) dma16(rA, a + g * AB + (wave + NW * q) * 1024, va[q], (uint32_t)(s0 + s) * 128);
+    // channel block c of the tile: 16 ld bytes from the one before it, 2 KB (two fragments) per stage
 #pragma unroll
-    for (int q = 0; q < NB; ++q) dma16(rB, buf + AB + (wave + NW * q) * 1024, vb[q], (uint32_t)k * 128);
+    for (int q = 0; q < NB; ++q)
+      dma16(rB, b + g * BB + (wave + NW * q) * 1024, vb[q], (uint32_t)(s0 + s) * 2048);
   };
 
   v16i acc[TI][TJ];
@@ -75,61 +175,460 @@ __global__ __launch_bounds__(64 * WM * WN) void k6_gemm(const int8_t* __restrict
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = v16i{};
-
-  issue(0, lds);
-  for (int k = 0; k < nst; ++k) {
-    uint8_t* cur = lds + (k & 1) * (AB + BB);
-    // stage k has arrived; every wave is done with the other buffer
-    wait_vm_lgkm0<0>();
-    __syncthreads();
-    if (k + 1 < nst) issue(k + 1, lds + ((k + 1) & 1) * (AB + BB));
+  v4i A[2][TI], B[2][TJ];
+  auto read = [&](const uint8_t* a, const uint8_t* b, int s, v4i* fa, v4i* fb) {
+    a += g * AB, b += g * BB;
+    auto ra = [&](int i) {
+      const int r = wr + 32 * i + l32;
+      fa[i] = *reinterpret_cast<const v4i*>(a + r * 128 + (((2 * s + kh) ^ swz8(r)) * 16));
+    };
+    ra(0);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      v4i A[TI], B[TJ];
-#pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        const int r = wr + 32 * i + l32;
-        A[i] = *reinterpret_cast<const v4i*>(cur + r * 128 + (((2 * s + kh) ^ swz8(r)) * 16));
-      }
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        const int c = wc + 32 * j + l32;
-        B[j] = *reinterpret_cast<const v4i*>(cur + AB + c * 128 + (((2 * s + kh) ^ swz8(c)) * 16));
-      }
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(A[i], B[j], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < TJ; ++j) {
+      const int c = wc + 32 * j + l32, k16 = 2 * s + kh;  // lane (c % 16) + 16 (k16 % 4) of a fragment
+      fb[j] = *reinterpret_cast<const v4i*>(b + (c >> 4) * 2048 + (k16 >> 2) * 1024 + (k16 & 3) * 256 + (c & 15) * 16);
     }
+#pragma unroll
+    for (int i = 1; i < TI; ++i) ra(i);
+  };
+  auto multiply = [&](const v4i* fa, const v4i* fb) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
+  };
+  // a step's order: one MFMA, the next step's reads, the other MFMAs (each ahead of one load)
+  auto order = [&](bool loads) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, TI + TJ, 0);
+    if (loads) {
+#pragma unroll
+      for (int x = 1; x < TI * TJ; ++x) {
+        __builtin_amdgcn_sched_group_barrier(0x020, (NL + TI * TJ - 2) / (TI * TJ > 1 ? TI * TJ - 1 : 1), 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      }
+    } else {
+      __builtin_amdgcn_sched_group_barrier(0x008, TI * TJ, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto stage = [&](int k, uint8_t* ca, uint8_t* cb, const uint8_t* na, const uint8_t* nb) {
+    read(ca, cb, 1, A[1], B[1]);
+    multiply(A[0], B[0]);
+    order(false);
+    read(ca, cb, 2, A[0], B[0]);
+    multiply(A[1], B[1]);
+    order(false);
+    read(ca, cb, 3, A[1], B[1]);
+    multiply(A[0], B[0]);
+    order(false);
+    wait_vm_lgkm0<0>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    issue(k + 2, ca, cb);
+    read(na, nb, 0, A[0], B[0]);
+    multiply(A[1], B[1]);
+    order(true);
+  };
+  issue(0, la0, lb0);
+  issue(1, la1, lb1);
+  wait_vm_lgkm0<NL>();
+  __builtin_amdgcn_s_barrier();
+  read(la0, lb0, 0, A[0], B[0]);
+  int k = 0;
+  for (; k + 2 <= turns; k += 2) {
+    stage(k, la0, lb0, la1, lb1);
+    stage(k + 1, la1, lb1, la0, lb0);
   }
+  if (k < turns) stage(k, la0, lb0, la1, lb1);
+  wait_vm_lgkm0<0>();
+  __builtin_amdgcn_s_barrier();  // the buffers are free
 
+  constexpr int CW = 32 * TJ, LS = CW + 4, CL = CW / 8, RP = 64 / CL;  // CL lanes of 8 columns, RP rows at once
+  constexpr int PW = NW * KG / 4, NP = 32 / RP;                       // waves per array; passes per strip
+  static_assert(32 * LS * 4 * PW <= KG * (AB < BB ? AB : BB) && PW * 4 == NW * KG, "a strip per wave");
+  auto strip_of = [&](int w) {
+    uint8_t* base = w / PW == 0 ? la0 : w / PW == 1 ? la1 : w / PW == 2 ? lb0 : lb1;
+    return reinterpret_cast<int*>(base) + (w % PW) * 32 * LS;
+  };
+  int* strip = strip_of(wid);
+  const int rl = lane / CL, cl = lane % CL;
+  const int64_t n = n0 + wc + cl * 8;
+  float sw[8], bb[8];
 #pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    const int64_t n = n0 + wc + 32 * j + l32;
-    if (n >= N) continue;
-    const float sw = sW[n], b = bias ? bias[n] : 0.0f;
+  for (int e = 0; e < 8; ++e) sw[e] = lsw[wc + cl * 8 + e], bb[e] = lbb[wc + cl * 8 + e];
 #pragma unroll
-    for (int i = 0; i < TI; ++i) {
+  for (int i = 0; i < TI; ++i) {
 #pragma unroll
-      for (int a = 0; a < 16; ++a) {
-        const int64_t m = m0 + wr + 32 * i + 8 * (a >> 2) + 4 * kh + (a & 3);
-        if (m >= M) continue;
-        float y = (float)acc[i][j][a] * sX[m] * sw;
-        if (bias) y += b;
-        if (ydtype == 0) static_cast<float*>(Y)[m * ldy + n] = y;
-        else static_cast<__bf16*>(Y)[m * ldy + n] = (__bf16)(ydtype == 2 ? gelu_erf(y) : y);
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int a = 0; a < 16; ++a) strip[(8 * (a >> 2) + 4 * kh + (a & 3)) * LS + 32 * j + l32] = acc[i][j][a];
+    if (KG > 1) __syncthreads();
+    // the K groups share the strip's passes; each adds all groups' sums
+    int I[NP][8];
+    float sx[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      if (KG > 1 && p % KG != g) continue;
+      const int at = (p * RP + rl) * LS + cl * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) I[p][e] = 0;
+#pragma unroll
+      for (int h = 0; h < KG; ++h) {
+        const int4* q = reinterpret_cast<const int4*>((KG > 1 ? strip_of(h * NW + wave) : strip) + at);
+        const int4 u = q[0], v = q[1];
+        I[p][0] += u.x, I[p][1] += u.y, I[p][2] += u.z, I[p][3] += u.w;
+        I[p][4] += v.x, I[p][5] += v.y, I[p][6] += v.z, I[p][7] += v.w;
+      }
+      sx[p] = lsx[wr + 32 * i + p * RP + rl];
+    }
+    if (KG > 1 && i + 1 < TI) __syncthreads();
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      if (KG > 1 && p % KG != g) continue;
+      const int64_t m = m0 + wr + 32 * i + p * RP + rl;
+      if (part) {
+        if (m < o.M && n < ldp) {
+          int4* q = reinterpret_cast<int4*>(part + ((int64_t)blockIdx.y * o.M + m) * ldp + n);
+          q[0] = make_int4(I[p][0], I[p][1], I[p][2], I[p][3]);
+          q[1] = make_int4(I[p][4], I[p][5], I[p][6], I[p][7]);
+        }
+      } else if (m < o.M) {
+        store8(o, m, n, I[p], sx[p], sw, bb);
       }
     }
   }
 }
 
+// The second step of a K split: the parts' sums, then the scales.  A thread owns 8 columns.
+__global__ __launch_bounds__(256) void k6_join(const int* __restrict__ part, int parts, int64_t ldp, Out o) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = ldp / 8;
+  if (i >= o.M * per) return;
+  const int64_t m = i / per, n = i % per * 8;
+  int I[8] = {};
+  for (int p = 0; p < parts; ++p) {
+    const int4* q = reinterpret_cast<const int4*>(part + ((int64_t)p * o.M + m) * ldp + n);
+    const int4 u = q[0], v = q[1];
+    I[0] += u.x, I[1] += u.y, I[2] += u.z, I[3] += u.w, I[4] += v.x, I[5] += v.y, I[6] += v.z, I[7] += v.w;
+  }
+  float sw[8], bb[8];
+  load_channels(o, n, sw, bb);
+  store8(o, m, n, I, o.sX[m], sw, bb);
+}
+
+// ---- few tokens: v_mfma_i32_16x16x64_i8, weights straight from memory
+//
+// Bound by the weights' read.  A block of 8 waves owns 16 channels (one channel block of the
+// weights' fragment order) and up to 16 NT tokens; its waves take the fragments of 64 along K in
+// turn, U loads of 1 KB in flight each, and add their integer sums in LDS.  The weights are
+// the A operand, the tokens the B operand: lane l holds token l & 15 and k = 16 (l >> 4) .. + 15.
+constexpr int FEW_NW = 8, FEW_U = 6;
+constexpr uint32_t kNoLoad = 0x7FFFFF00u;  // past the token rows' range (32 rows of at most 128 KB)
+
+template <int NT>
+struct FewSums {
+  int v[FEW_NW][NT][64][4];
+};
+
+template <int NT>
+__device__ __forceinline__ void few_finish(const v4i acc[NT], FewSums<NT>& sums, int wave, int lane, const Out& o,
+                                           const float* sx, int64_t n0) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) *reinterpret_cast<v4i*>(&sums.v[wave][t][lane][0]) = acc[t];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 256 * NT; i += 64 * FEW_NW) {
+    const int c = i & 15, m = i >> 4;  // consecutive threads: consecutive channels
+    const int64_t n = n0 + c;
+    if (m >= o.M || n >= o.N) continue;
+    int I = 0;
+#pragma unroll
+    for (int w = 0; w < FEW_NW; ++w) I += sums.v[w][m >> 4][(m & 15) + 16 * (c >> 2)][c & 3];
+    float y = (float)I * sx[m] * o.sW[n];
+    if (o.bias) y += o.bias[n];
+    store1(o, m, n, y);
+  }
+}
+
+template <int NT>
+__global__ __launch_bounds__(64 * FEW_NW) void k6_few(const int8_t* __restrict__ qX, int64_t ld,
+                                                      const int8_t* __restrict__ qW, Out o) {
+  __shared__ FewSums<NT> sums;
+  constexpr int U = FEW_U;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int8_t* wl = qW + n0 * ld + lane * 16;
+  const __amdgpu_buffer_rsrc_t rX = make_rsrc(qX, (uint32_t)o.M * (uint32_t)ld);  // tokens past M read zeros
+  const uint32_t xoff = (uint32_t)(lane & 15) * (uint32_t)ld + (uint32_t)(lane >> 4) * 16;
+  const int frags = (int)(ld / 64);
+  v4i acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = v4i{};
+  for (int f = wave; f < frags; f += FEW_NW * U) {
+    uint4 w[U], x[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = f + u * FEW_NW;  // past the end: any weights, zero tokens
+      w[u] = *reinterpret_cast<const uint4*>(wl + (at < frags ? at : frags - 1) * 1024);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        x[u][t] = buf_load16(rX, at < frags ? (uint32_t)at * 64 + (uint32_t)(16 * t) * (uint32_t)ld + xoff : kNoLoad);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, w[u]), __builtin_bit_cast(v4i, x[u][t]),
+                                                       acc[t], 0, 0, 0);
+  }
+  few_finish<NT>(acc, sums, wave, lane, o, o.sX, n0);
+}
+
+// The whole layer for few tokens in one launch: every block quantizes the tokens' rows for
+// itself (X is small and in L2; the first weights are already on their way).  All 512 threads
+// share each row, 8 values each (ld <= 4096), so the smoothing factors are read once for all
+// rows and the rows' maxima meet in one barrier.  Codes stand in LDS, rows 16 bytes longer
+// than ld so that a fragment's 16 rows fall in distinct bank groups.  RM: most rows.  80
+// registers let three blocks share a CU: all blocks of 12288 channels run at once.
+template <typename T, bool VEC, bool SMOOTH, int RM>
+__global__ __launch_bounds__(64 * FEW_NW) __attribute__((amdgpu_waves_per_eu(6, 6))) void k6_few_layer(
+    const T* __restrict__ X, int64_t ldx, int K, const float* __restrict__ inv_s, int64_t ld,
+    const int8_t* __restrict__ qW, Out o) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t codes[];
+  __shared__ FewSums<1> sums;
+  __shared__ uint32_t tops[RM][FEW_NW];
+  __shared__ float sx[RM], rx[RM];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int8_t* wl = qW + n0 * ld + lane * 16;
+  const int frags = (int)(ld / 64), M = (int)o.M;
+  const uint32_t row_bytes = (uint32_t)ld + 16;
+  const int k0 = 8 * (int)threadIdx.x;
+  float v[RM][8];
+  uint32_t top[RM];
+  uint4 w[FEW_U];
+  auto load_w = [&](int g) {
+#pragma unroll
+    for (int u = 0; u < FEW_U; ++u) {
+      const int at = g + u * FEW_NW;
+      w[u] = *reinterpret_cast<const uint4*>(wl + (at < frags ? at : frags - 1) * 1024);
+    }
+  };
+  {
+    typedef Row<T, VEC> RowX;
+    typedef Row<float, true> RowS;
+    auto row = [&](int m) { return RowX(X + (m < M ? m : 0) * ldx, m < M ? K : 0); };  // past M: no range, zeros
+    const RowS f(inv_s, SMOOTH ? K : 0);
+    typename RowX::Raw raw[RM];
+#pragma unroll
+    for (int m = 0; m < RM; ++m) raw[m] = row(m).load(k0);
+    typename RowS::Raw u0 = {};
+    if (SMOOTH) u0 = f.load(k0);
+    load_w(wave);
+    float s[8];
+    if (SMOOTH) f.value(u0, k0, s);
+#pragma unroll
+    for (int m = 0; m < RM; ++m) {
+      row(m).value(raw[m], k0, v[m]);
+      top[m] = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (SMOOTH) v[m][e] *= s[e];
+        top[m] = umax(top[m], abs_bits(v[m][e]));
+      }
+    }
+  }
+  // the rows' reductions side by side: one shuffle's latency per step, not one per row
+#pragma unroll
+  for (int step = 32; step >= 1; step >>= 1)
+#pragma unroll
+    for (int m = 0; m < RM; ++m) top[m] = umax(top[m], (uint32_t)__shfl_xor((int)top[m], step, 64));
+  if (lane == 0) {
+#pragma unroll
+    for (int m = 0; m < RM; ++m) tops[m][wave] = top[m];
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < RM) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < FEW_NW; ++i) a = umax(a, tops[threadIdx.x][i]);
+    row_scale(a, sx[threadIdx.x], rx[threadIdx.x]);
+  }
+  __syncthreads();
+  if (k0 < ld) {
+#pragma unroll
+    for (int m = 0; m < RM; ++m)
+      if (m < M) {
+        const float r = rx[m];
+        *reinterpret_cast<uint2*>(codes + (uint32_t)m * row_bytes + k0) =
+            make_uint2(codes4(v[m][0], v[m][1], v[m][2], v[m][3], r), codes4(v[m][4], v[m][5], v[m][6], v[m][7], r));
+      }
+  }
+  __syncthreads();
+  v4i acc[1] = {};
+  const bool on = (lane & 15) < M;
+  const uint8_t* xl = codes + (uint32_t)(on ? lane & 15 : 0) * row_bytes + (uint32_t)(lane >> 4) * 16;
+  for (int g = wave; g < frags; g += FEW_NW * FEW_U) {
+    if (g != wave) load_w(g);
+#pragma unroll
+    for (int u = 0; u < FEW_U; ++u) {
+      const int at = g + u * FEW_NW;
+      if (at >= frags) break;
+      v4i x = *reinterpret_cast<const v4i*>(xl + at * 64);
+      if (!on) x = v4i{};  // tokens past M
+      acc[0] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, w[u]), x, acc[0], 0, 0, 0);
+    }
+  }
+  few_finish<1>(acc, sums, wave, lane, o, sx, n0);
+}
+
+// Compute units of the current device, asked once per thread and device.
+int device_cus() {
+  static thread_local int dev_of = -1, cus = 0;
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return 256;
+  if (dev != dev_of) {
+    int n = 0;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1) n = 256;
+    cus = n;
+    dev_of = dev;
+  }
+  return cus;
+}
+
+template <int WM, int WN, int TI, int TJ, int KG>
+void launch_tiles(const W8A8Plan& p, int64_t ld, const int8_t* qX, const int8_t* qW, const Out& o, int* part,
+                  hipStream_t st) {
+  constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN;
+  const uint32_t tm = (uint32_t)((o.M + BM - 1) / BM), tn = (uint32_t)((o.N + BN - 1) / BN);
+  hipLaunchKernelGGL((k6_tiles<WM, WN, TI, TJ, KG>), dim3(tm * tn, (uint32_t)p.parts), dim3(64 * WM * WN * KG), 0, st, qX, ld, qW,
+                     o, tm, tn, part, p.ldp);
+}
+
+// ---- the choice of kernel
+//
+// Every choice gives the same bits, so it is made by estimated time alone (us; S = stages of
+// 128 along K, c = blocks that share a compute unit).  The estimates are straight lines
+// through measured times (256 CUs, 20 launches back to back; M x K x N):
+//   few     2.3 + weight bytes x (0.075 + 0.006 M) / MB: 1x3072x9216 4.1 (64 x 2: 7.6), 16x3072x9216 7.1 (7.9),
+//           32x3072x9216 11.2 (8.1), 32x1280x1280 4.1 (5.3), 16x12288x3072 9.6 (64 x 4 in 4 parts: 14.6)
+//   64      one K group: 0.30 S + 1.6 alone on its CU, then 0.38, 0.58, 0.79 S for 2, 3, 4 blocks:
+//           512x3072x3072 10.6, 1024x3072x3072 16.4, 512x320x1280 4.1
+//   64 x 2  two K groups (blocks of 8 waves, tiles <= CUs): 0.24 S + 2: 64x3072x9216 8.2 (one group
+//           10.1, four 8.3), 128x1280x1280 5.4 (6.0, 6.3)
+//   64 x 4  four K groups: 0.20 S + 3: 128x12288x3072 26.1 (one group 48.3, two 32.0)
+//   128     0.62 S + 2.5 alone, 1.04 S for two: 512x3072x9216 24.3, 2048x12288x3072 80.5
+//   128 x 2 two K groups (tiles <= CUs): 0.53 S + 2: 1024x12288x3072 53.1 (one group 67.2)
+//   256     1.38 S + 9 (1.15 S where at most 5/8 of the CUs have a tile): 4608x12288x3072 143 (128: 176),
+//           1024x3072x9216 38.8 (46.8), 2048x3072x9216 81.7 (71.6)
+// K parts (tiles of 64 with four groups, S / parts >= 24, all parts on the CUs at once) add the
+// partial sums' traffic and a launch, 4 + 12 bytes x M N parts / 6 TB/s: 64x12288x3072 15.7 in 4 parts, 26.6 in one.
+struct Cost {
+  double us;
+  int tile, groups, parts;
+};
+
+Cost tiles_cost(int64_t M, int64_t N, int S, int cus, int tile, int groups) {
+  const double T = (double)((M + tile - 1) / tile) * (double)((N + tile - 1) / tile);
+  const double rounds = T / cus;
+  double us = 0.0;
+  auto by_line = [&](const double* a, int most, double b) {  // a[c - 1] per stage with c blocks on a CU
+    const double full = (double)(int64_t)(rounds / most), rest = rounds - full * most;
+    us = full * (a[most - 1] * S + b);
+    if (rest > 0) us += a[(int)(rest + 0.999999) - 1] * S + b;
+  };
+  static const double a64[] = {0.30, 0.38, 0.58, 0.79}, a642[] = {0.24}, a644[] = {0.20}, a128[] = {0.62, 1.04},
+                      a1282[] = {0.53};
+  if (tile == 64) groups == 1 ? by_line(a64, 4, 1.6) : groups == 2 ? by_line(a642, 1, 2.0) : by_line(a644, 1, 3.0);
+  else if (tile == 128) groups == 1 ? by_line(a128, 2, 2.5) : by_line(a1282, 1, 2.0);
+  else {
+    const double full = (double)(int64_t)rounds, rest = rounds - full;
+    us = full * (1.38 * S + 9.0) + (rest > 0.625 ? 1.38 * S + 9.0 : rest > 0 ? 1.15 * S + 9.0 : 0.0);
+  }
+  return Cost{us, tile, groups, 1};
+}
+
 }  // namespace
 
+W8A8Plan plan_w8a8(int64_t M, int64_t K, int64_t N) {
+  const int cus = device_cus();
+  const int64_t ld = i8_ld(K), ldp = (N + 7) / 8 * 8;
+  const int S = (int)(ld / 128);
+  Cost best{1e30, 64, 1, 1};
+  auto take = [&](const Cost& c) {
+    if (c.us < best.us) best = c;
+  };
+  take(tiles_cost(M, N, S, cus, 64, 1));
+  take(tiles_cost(M, N, S, cus, 128, 1));
+  take(tiles_cost(M, N, S, cus, 256, 1));
+  const int64_t T64 = ((M + 63) / 64) * ((N + 63) / 64), T128 = ((M + 127) / 128) * ((N + 127) / 128);
+  if (T128 <= cus) take(tiles_cost(M, N, S, cus, 128, 2));
+  if (T64 <= cus) {
+    take(tiles_cost(M, N, S, cus, 64, 2));
+    for (int parts = 1; parts <= 8 && parts * T64 <= cus && (parts == 1 || S / parts >= 24); parts *= 2) {
+      const int per = (S + parts - 1) / parts;
+      Cost c = tiles_cost(M, N, per, cus, 64, 4);
+      c.parts = (S + per - 1) / per;  // no empty part
+      if (c.parts > 1) c.us += 4.0 + 12.0 * (double)(M * ldp) * c.parts / 6e6;
+      take(c);
+    }
+  }
+  if (M <= 32) take(Cost{2.3 + (double)(N * ld) * 1e-6 * (0.075 + 0.006 * (double)M), 0, 1, 1});
+  W8A8Plan p{best.tile, best.groups, best.parts, ldp, 0};
+  if (p.parts > 1) p.bytes = (size_t)p.parts * (size_t)M * (size_t)ldp * 4;
+  return p;
+}
+
+// Measured against the quantizer's launch and k6_few (us): 4x3072x9216 6.6 against 2.6 + 4.9, 4x3072x12288
+// 8.1 against 3.1 + 6.3, 2x1280x1280 3.8 against 2.9 + 2.7; at 6 and 8 rows the values no longer fit 80
+// registers (8x3072x3072 10.7 against 2.8 + 3.2).
+bool few_layer(int64_t M, int64_t K) {
+  return M <= 4 && i8_ld(K) <= 4096;
+}
+
+hipError_t launch_few_layer(int64_t M, int64_t K, int64_t N, const void* X, int xdtype, int64_t ldx, const float* inv_s,
+                            const int8_t* qW, const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype,
+                            hipStream_t st) {
+  const Out o{nullptr, sW, bias, Y, ldy, M, N, ydtype, false};
+  const int64_t ld = i8_ld(K);
+  const dim3 g((uint32_t)((N + 15) / 16)), b(64 * FEW_NW);
+  const size_t lds = (size_t)M * (size_t)(ld + 16);
+  auto go = [&](auto kernel, auto x) { hipLaunchKernelGGL(kernel, g, b, lds, st, x, ldx, (int)K, inv_s, ld, qW, o); };
+  const uint16_t* x16 = static_cast<const uint16_t*>(X);
+  const float* x32 = static_cast<const float*>(X);
+  auto rows = [&](auto rm) {
+    constexpr int RM = decltype(rm)::value;
+    if (xdtype == 0) inv_s ? go(k6_few_layer<float, true, true, RM>, x32) : go(k6_few_layer<float, true, false, RM>, x32);
+    else if (rows_aligned4(X, ldx, xdtype))
+      inv_s ? go(k6_few_layer<uint16_t, true, true, RM>, x16) : go(k6_few_layer<uint16_t, true, false, RM>, x16);
+    else inv_s ? go(k6_few_layer<uint16_t, false, true, RM>, x16) : go(k6_few_layer<uint16_t, false, false, RM>, x16);
+  };
+  if (M <= 1) rows(std::integral_constant<int, 1>{});
+  else if (M <= 2) rows(std::integral_constant<int, 2>{});
+  else rows(std::integral_constant<int, 4>{});
+  return hipGetLastError();
+}
+
 hipError_t launch_w8a8(int64_t M, int64_t K, int64_t N, const int8_t* qX, const float* sX, const int8_t* qW,
-                       const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype, hipStream_t st) {
-  const uint32_t tiles_m = (uint32_t)((M + 63) / 64), tiles_n = (uint32_t)((N + 63) / 64);
-  hipLaunchKernelGGL((k6_gemm<2, 2, 1, 1>), dim3(tiles_m * tiles_n), dim3(256), 0, st, qX, i8_ld(K), M, qW, N, sX, sW,
-                     bias, Y, ldy, ydtype, tiles_n);
+                       const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype, void* ws, hipStream_t st) {
+  const int64_t ld = i8_ld(K);
+  const bool wide = reinterpret_cast<uintptr_t>(Y) % 16 == 0 && ldy % (ydtype == 0 ? 4 : 8) == 0;
+  const Out o{sX, sW, bias, Y, ldy, M, N, ydtype, wide};
+  const W8A8Plan p = plan_w8a8(M, K, N);
+  if (p.tile == 0) {
+    const dim3 g((uint32_t)((N + 15) / 16)), b(64 * FEW_NW);
+    if (M <= 16) hipLaunchKernelGGL(k6_few<1>, g, b, 0, st, qX, ld, qW, o);
+    else hipLaunchKernelGGL(k6_few<2>, g, b, 0, st, qX, ld, qW, o);
+    return hipGetLastError();
+  }
+  int* part = p.parts > 1 ? static_cast<int*>(ws) : nullptr;
+  if (p.tile == 256) launch_tiles<2, 4, 4, 2, 1>(p, ld, qX, qW, o, part, st);
+  else if (p.tile == 128 && p.groups == 1) launch_tiles<2, 2, 2, 2, 1>(p, ld, qX, qW, o, part, st);
+  else if (p.tile == 128) launch_tiles<2, 2, 2, 2, 2>(p, ld, qX, qW, o, part, st);
+  else if (p.groups == 1) launch_tiles<2, 2, 1, 1, 1>(p, ld, qX, qW, o, part, st);
+  else if (p.groups == 2) launch_tiles<2, 2, 1, 1, 2>(p, ld, qX, qW, o, part, st);
+  else launch_tiles<2, 2, 1, 1, 4>(p, ld, qX, qW, o, part, st);
+  if (p.parts > 1)
+    hipLaunchKernelGGL(k6_join, dim3((uint32_t)((M * (p.ldp / 8) + 255) / 256)), dim3(256), 0, st, part, p.parts, p.ldp, o);
   return hipGetLastError();
 }
 

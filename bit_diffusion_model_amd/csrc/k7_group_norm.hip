@@ -23,6 +23,18 @@ namespace {
 constexpr int GN_NT = 256;
 constexpr int GN_ROWS = 8;  // positions a thread holds at once
 
+__device__ __forceinline__ void load8_vec(const uint16_t* p, float v[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  v[0] = bf16_lo_to_f32(w.x), v[1] = bf16_hi_to_f32(w.x), v[2] = bf16_lo_to_f32(w.y), v[3] = bf16_hi_to_f32(w.y);
+  v[4] = bf16_lo_to_f32(w.z), v[5] = bf16_hi_to_f32(w.z), v[6] = bf16_lo_to_f32(w.w), v[7] = bf16_hi_to_f32(w.w);
+}
+__device__ __forceinline__ void load8_vec(const float* p, float v[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+
 // V consecutive channels (V = 8: 16-byte aligned; V = 1: any alignment)
 template <typename T, int V>
 __device__ __forceinline__ void loadv(const T* p, float v[V]) {
@@ -243,10 +255,10 @@ __global__ __launch_bounds__(GN_NT) void k7_apply_quant(const T* __restrict__ X,
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t r0 = (int64_t)blockIdx.x * chunk, r1 = r0 + chunk < S ? r0 + chunk : S;
   for (int64_t i = r0 + wave; i < r1; i += 4) {
-    const T* x = X + blockIdx.y * bsx + i * ldx;
+    const Row<T, VEC> x(X + blockIdx.y * bsx + i * ldx, C);
     const int64_t row = blockIdx.y * S + i;
     auto value8 = [&](int k8, float v[8]) {
-      load8<T, VEC>(x, 8 * (int64_t)k8, C, v);
+      x.value(x.load(8 * k8), 8 * k8, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float4 f = coef[e * c8 + k8];

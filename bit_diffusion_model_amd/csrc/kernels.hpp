@@ -85,9 +85,23 @@ hipError_t launch_w4a16(int64_t M, int64_t K, int64_t N, const uint16_t* X, int6
 // 8-bit codes and one scale per token of X [M][ldx] (xdtype 0 fp32, 1 bf16) times inv_s (may be NULL).
 hipError_t launch_quant_i8(int64_t M, int64_t K, const void* X, int xdtype, int64_t ldx, const float* inv_s, int8_t* qX,
                            float* sX, hipStream_t st);
-// Y = (qX qW^T) sX sW + bias (bias may be NULL); ydtype 0 fp32, 1 bf16, 2 bf16 of GELU.
+// How the product runs on the current device: tile 0 (few tokens, no tiles), 64, 128 or 256, `groups`
+// of waves sharing a tile's K, `parts` ranges of K, whose int32 partial sums [parts][M][ldp] take
+// `bytes` of workspace (0 when parts == 1).
+struct W8A8Plan {
+  int tile, groups, parts;
+  int64_t ldp;
+  size_t bytes;
+};
+W8A8Plan plan_w8a8(int64_t M, int64_t K, int64_t N);
+// Whether the layer runs as one launch for few tokens (which quantizes inside), and that launch.
+bool few_layer(int64_t M, int64_t K);
+hipError_t launch_few_layer(int64_t M, int64_t K, int64_t N, const void* X, int xdtype, int64_t ldx, const float* inv_s,
+                            const int8_t* qW, const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype,
+                            hipStream_t st);
+// Y = (qX qW^T) sX sW + bias (bias may be NULL), qW in fragment order; ydtype 0 fp32, 1 bf16, 2 bf16 of GELU.
 hipError_t launch_w8a8(int64_t M, int64_t K, int64_t N, const int8_t* qX, const float* sX, const int8_t* qW,
-                       const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype, hipStream_t st);
+                       const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype, void* ws, hipStream_t st);
 
 // ---- the channels-last group norm
 

@@ -109,3 +109,24 @@ extern "C" svdq_status svdq_pack_weights_int8(int64_t K, int64_t N, const uint16
   });
   return ok();
 }
+
+extern "C" size_t svdq_int8_weight_bytes(int64_t K, int64_t N) {
+  return K < 1 || N < 1 ? 0 : (size_t)((N + 15) / 16 * 16) * (size_t)i8_ld(K);
+}
+
+extern "C" svdq_status svdq_prepare_weights_int8(int64_t K, int64_t N, const int8_t* qW, int8_t* qW_out) {
+  if (!qW || !qW_out) return fail(SVDQ_EINVAL, "qW and qW_out must be non-NULL");
+  if (K < 1 || N < 1) return fail(SVDQ_EINVAL, "K and N must be >= 1 (got %lld, %lld)", (long long)K, (long long)N);
+  if (K > kMaxInt8K) return fail(SVDQ_EUNSUPPORTED, "K must be <= %lld (got %lld)", (long long)kMaxInt8K, (long long)K);
+  const int64_t ld = i8_ld(K);
+  run_blocks((N + 15) / 16, [&](int64_t b) {
+    int8_t* out = qW_out + b * 16 * ld;
+    for (int64_t k = 0; k < ld; k += 16)  // 16 codes of each of the block's 16 channels
+      for (int64_t c = 0; c < 16; ++c, out += 16) {
+        const int64_t n = b * 16 + c;
+        if (n < N) std::memcpy(out, qW + n * ld + k, 16);
+        else std::memset(out, 0, 16);
+      }
+  });
+  return ok();
+}

@@ -59,7 +59,8 @@ EXPORTS = [
     "svdq_linear_forward", "svdq_linear_forward_unfused", "svdq_debug_group_sums", "svdq_linear_forward_noalloc",
     "svdq_mlp_workspace_bytes", "svdq_mlp_forward", "svdq_mlp_chain_gemm", "svdq_mlp_chain_reduce",
     "svdq_w4a16_gemm", "svdq_forward_k1_parts",
-    "svdq_int8_ld", "svdq_pack_weights_int8", "svdq_quantize_act_int8", "svdq_gemm_w8a8_workspace_bytes",
+    "svdq_int8_ld", "svdq_pack_weights_int8", "svdq_int8_weight_bytes", "svdq_prepare_weights_int8",
+    "svdq_quantize_act_int8", "svdq_gemm_w8a8_workspace_bytes",
     "svdq_int8_workspace_bytes", "svdq_gemm_w8a8", "svdq_linear_forward_int8", "svdq_group_norm_workspace_bytes",
     "svdq_group_norm", "svdq_group_norm_quantize_int8", "svdq_norm_linear_int8_workspace_bytes",
     "svdq_norm_linear_forward_int8",
@@ -108,7 +109,9 @@ def lib():
         "svdq_pack_weights_int8": (I32, [I64, I64, P, P, F, P, P, P, P]),
         "svdq_quantize_act_int8": (I32, [I64, I64, P, I32, I64, P, P, P, P]),
         "svdq_gemm_w8a8_workspace_bytes": (SZ, [P, I64]),
-        "svdq_int8_workspace_bytes": (SZ, [P, I64]),
+        "svdq_int8_weight_bytes": (SZ, [I64, I64]),
+        "svdq_prepare_weights_int8": (I32, [I64, I64, P, P]),
+        "svdq_int8_workspace_bytes": (SZ, [P, I64, I32]),
         "svdq_gemm_w8a8": (I32, [P, I64, P, P, P, I64, I32, P, SZ, P]),
         "svdq_linear_forward_int8": (I32, [P, I64, P, I32, I64, P, I64, I32, P, SZ, P]),
         "svdq_group_norm_workspace_bytes": (SZ, [P, I64, I64]),
@@ -563,6 +566,14 @@ def pack_weights_int8(W_bits: np.ndarray, act_absmax_: Optional[np.ndarray] = No
     return s, inv, qW, sW
 
 
+def prepare_weights_int8(K: int, qW: np.ndarray) -> np.ndarray:
+    """svdq_prepare_weights_int8: codes [N][int8_ld(K)] in the kernel layout (flat, N rounded up to 16)."""
+    qW = np.ascontiguousarray(qW, dtype=np.int8)
+    out = np.empty(lib().svdq_int8_weight_bytes(K, qW.shape[0]), np.int8)
+    _check(lib().svdq_prepare_weights_int8(K, qW.shape[0], _ptr(qW), _ptr(out)))
+    return out
+
+
 _cfg = None
 
 
@@ -572,9 +583,12 @@ def _rt():
     global _cfg
     if _cfg is None:
         torch = _torch()
+        # the raw handle of the current stream, without making a Stream object (2 us)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
         _cfg = (torch, {torch.float32: F32, torch.bfloat16: BF16}, {F32: torch.float32, BF16: torch.bfloat16,
-                                                                   BF16_GELU: torch.bfloat16}, lib())
-    return _cfg
+                                                                   BF16_GELU: torch.bfloat16}, lib(), raw)
+    return _cfg[:4]
 
 
 def _dev_tensor(t, name: str, dtype, device, n=None):
@@ -590,20 +604,26 @@ def _dev_tensor(t, name: str, dtype, device, n=None):
 
 
 def _on_current_device(torch, t):
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise SvdqError(f"the tensor is on {t.device}, the current HIP device is {torch.cuda.current_device()}")
 
 
 class Int8Linear:
     """The 8-bit layer on the GPU: codes qW int8 [N][int8_ld(K)] (zeros past K), sW fp32 [N], inv_s fp32 [K]
-    and bias fp32 [N] or None; numpy arrays are uploaded, device tensors are used as they are."""
+    and bias fp32 [N] or None, as numpy arrays or device tensors.  The codes are laid out once for the kernels
+    (a copy); the other tensors are used as they are."""
 
     def __init__(self, qW, sW, K: int, inv_s=None, bias=None, device="cuda:0"):
         torch = _torch()
         self.K, self.N = int(K), int(qW.shape[0])
         if qW.ndim != 2 or qW.shape[1] != int8_ld(self.K):
             raise SvdqError(f"qW must be [N][{int8_ld(self.K)}]")
-        self.qW = _dev_tensor(qW, "qW", torch.int8, device)
+        if isinstance(qW, np.ndarray):
+            self.qW = torch.from_numpy(prepare_weights_int8(self.K, qW)).to(device)
+        else:  # the layout of svdq_prepare_weights_int8, on the device
+            qW = _dev_tensor(qW, "qW", torch.int8, device)
+            rows = torch.nn.functional.pad(qW, (0, 0, 0, -self.N % 16)) if self.N % 16 else qW
+            self.qW = rows.view(-1, 16, qW.shape[1] // 16, 16).permute(0, 2, 1, 3).contiguous().view(-1)
         self.sW = _dev_tensor(sW, "sW", torch.float32, device, self.N)
         self.inv_s = _dev_tensor(inv_s, "inv_s", torch.float32, device, self.K)
         self.bias = _dev_tensor(bias, "bias", torch.float32, device, self.N)
@@ -646,18 +666,22 @@ class Int8Linear:
                                 0 if ws is None else ws.numel(), _raw_stream(qX)))
         return out
 
-    def workspace(self, M: int):
+    def workspace(self, M: int, xdtype: int = BF16):
+        """Device scratch of forward() for M rows of X (None when unused)."""
         torch, _, _, L = _rt()
-        return torch.empty(max(L.svdq_int8_workspace_bytes(self._ref, M), 256), dtype=torch.uint8, device=self.device)
+        n = L.svdq_int8_workspace_bytes(self._ref, M, xdtype)
+        return torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
 
     def forward(self, X, ydtype: int = F32, out=None, workspace=None):
         """svdq_linear_forward_int8: quantizer and product on X [M][K], fp32 or bf16, any row stride."""
         torch, xt, _, L = _rt()
         M = _check_rows(X, self.K, xt)
         out = self._out(M, ydtype, out, X)
-        ws = workspace if workspace is not None else self.workspace(M)
-        _check(L.svdq_linear_forward_int8(self._ref, M, X.data_ptr(), xt[X.dtype], _ld(M, X.stride(0), self.K),
-                                          out.data_ptr(), _ld(M, out.stride(0), self.N), ydtype, ws.data_ptr(), ws.numel(), _raw_stream(X)))
+        xd = xt[X.dtype]
+        ws = workspace if workspace is not None else self.workspace(M, xd)
+        _check(L.svdq_linear_forward_int8(self._ref, M, X.data_ptr(), xd, _ld(M, X.stride(0), self.K), out.data_ptr(),
+                                          _ld(M, out.stride(0), self.N), ydtype, None if ws is None else ws.data_ptr(),
+                                          0 if ws is None else ws.numel(), _raw_stream(X)))
         return out
 
 
@@ -673,7 +697,7 @@ def _check_rows(X, K, xt) -> int:
 
 
 def _raw_stream(t) -> int:
-    return _cfg[0].cuda.current_stream(t.device).cuda_stream
+    return _cfg[4](t.get_device())
 
 
 def quantize_act_int8(X, inv_s=None, out=None):

@@ -454,7 +454,7 @@ svdq_status svdq_mlp_chain_reduce(const svdq_layer* fc1, const svdq_layer* fc2, 
 typedef struct svdq_int8_layer {
   int64_t K, N;
   const float* inv_s; /* [K] fp32 reciprocal smoothing factor, or NULL for none */
-  const int8_t* qW;   /* [N][svdq_int8_ld(K)] codes, row n = output channel n along K */
+  const int8_t* qW;   /* codes in the kernel layout of svdq_prepare_weights_int8 */
   const float* sW;    /* [N] fp32 */
   const float* bias;  /* [N] fp32, or NULL for none */
 } svdq_int8_layer;    /* device pointers, 16-byte aligned, owned by the caller */
@@ -471,16 +471,23 @@ int64_t svdq_int8_ld(int64_t K);
 svdq_status svdq_pack_weights_int8(int64_t K, int64_t N, const uint16_t* W, const float* act_absmax, float alpha,
                                    float* s_out, float* inv_s_out, int8_t* qW_out, float* sW_out);
 
+/* Offline device layout of the weights (host pointers): the matrix core's operand order, so that
+ * every load of the product is contiguous.  With ld = svdq_int8_ld(K), code (n, k) of qW
+ * [N][ld] goes to byte (n / 16) 16 ld + (k / 64) 1024 + ((k / 16) % 4) 256 + (n % 16) 16 + k % 16; channels past N
+ * up to a multiple of 16 are zero. qW_out: svdq_int8_weight_bytes (N rounded up to 16, times ld). */
+size_t svdq_int8_weight_bytes(int64_t K, int64_t N);
+svdq_status svdq_prepare_weights_int8(int64_t K, int64_t N, const int8_t* qW, int8_t* qW_out);
+
 /* The quantizer alone: X [M][ldx] (device, svdq_dtype xdtype) -> qX [M][svdq_int8_ld(K)] (16-byte
  * aligned), sX [M] fp32.  inv_s [K] (16-byte aligned) or NULL.  One launch; M == 0 is a no-op.
  * EINVAL on NULL, misalignment, sizes; EUNSUPPORTED on another xdtype or a limit; EHIP. */
 svdq_status svdq_quantize_act_int8(int64_t M, int64_t K, const void* X, int32_t xdtype, int64_t ldx,
                                    const float* inv_s, int8_t* qX, float* sX, void* stream);
 
-/* Bytes of device workspace svdq_gemm_w8a8 / svdq_linear_forward_int8 need for M rows (0: none, or
- * bad arguments). */
+/* Bytes of device workspace svdq_gemm_w8a8 / svdq_linear_forward_int8 need for M rows (and X's type)
+ * on the current device (0: none, or bad arguments). */
 size_t svdq_gemm_w8a8_workspace_bytes(const svdq_int8_layer* layer, int64_t M);
-size_t svdq_int8_workspace_bytes(const svdq_int8_layer* layer, int64_t M);
+size_t svdq_int8_workspace_bytes(const svdq_int8_layer* layer, int64_t M, int32_t xdtype);
 
 /* The product alone on codes as svdq_quantize_act_int8 writes them (qX 16-byte aligned; the bytes
  * past K may hold anything: the weights' are zero).  Y device [M][ldy], svdq_dtype ydtype,
@@ -490,8 +497,9 @@ svdq_status svdq_gemm_w8a8(const svdq_int8_layer* layer, int64_t M, const int8_t
                            int64_t ldy, int32_t ydtype, void* workspace, size_t ws_bytes, void* stream);
 
 /* The layer: quantizer, then product, on `stream`, the codes in `workspace` (>=
- * svdq_int8_workspace_bytes, 256-byte aligned, contents on entry irrelevant).  The same result,
- * bit for bit, as the two calls above. */
+ * svdq_int8_workspace_bytes, 256-byte aligned, contents on entry irrelevant); for few tokens one
+ * launch that quantizes inside and needs no workspace.  The same result, bit for bit, as the
+ * two calls above. */
 svdq_status svdq_linear_forward_int8(const svdq_int8_layer* layer, int64_t M, const void* X, int32_t xdtype,
                                      int64_t ldx, void* Y, int64_t ldy, int32_t ydtype, void* workspace,
                                      size_t ws_bytes, void* stream);

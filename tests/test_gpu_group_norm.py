@@ -178,11 +178,12 @@ def test_norm_linear():
         W = (rng.standard_normal((C, N)) / np.sqrt(C)).astype(np.float32)
         Wb = ((W.view(np.uint32) + 0x8000) >> 16).astype(np.uint16)
         amax = (1 + rng.random(C)).astype(np.float32)
-        lin = svdq.Int8Linear.from_weights(Wb, amax, 0.5, bias=rng.standard_normal(N).astype(np.float32))
+        _, inv, qW, sW = svdq.pack_weights_int8(Wb, amax, 0.5)
+        lin = svdq.Int8Linear(qW, sW, C, inv, rng.standard_normal(N).astype(np.float32))
         Y = gn.forward_linear(X, lin, svdq.F32)
         q, s = gn.quantize(X, lin.inv_s)
         assert torch.equal(Y, lin.gemm(q, s))
-        p = o8.product(q.cpu().numpy()[:, :C], s.cpu().numpy(), lin.qW.cpu().numpy()[:, :C], lin.sW.cpu().numpy())
+        p = o8.product(q.cpu().numpy()[:, :C], s.cpu().numpy(), qW[:, :C], sW)
         b = lin.bias.cpu().numpy().astype(np.float64)
         assert (np.abs(host(Y) - p - b) <= 5 * U * (np.abs(p) + np.abs(b)) + 1e-37).all()
 

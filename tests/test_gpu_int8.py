@@ -235,7 +235,7 @@ def test_refusals():
     with pytest.raises(svdq.SvdqError):
         lin.forward(X, out=torch.empty((4, 17), device="cuda:0"))
     with pytest.raises(svdq.SvdqError):
-        lin.forward(X, workspace=torch.empty(256, dtype=torch.uint8, device="cuda:0"))
+        lin.forward(make_x(40, 256, torch.bfloat16, 1), workspace=torch.empty(256, dtype=torch.uint8, device="cuda:0"))
     with pytest.raises(svdq.SvdqError):
         svdq.Int8Linear(qW[:, :200].copy(), sW, 256)
     with pytest.raises(svdq.SvdqError):
