@@ -85,7 +85,8 @@ svdq_status check_norm(const svdq_group_norm_desc* n, int64_t B, int64_t S) {
   if (!n) return fail(SVDQ_EINVAL, "norm is NULL");
   if (n->C < 1 || n->groups < 1 || n->C % n->groups != 0)
     return fail(SVDQ_EINVAL, "C must be a positive multiple of groups (got %lld, %d)", (long long)n->C, (int)n->groups);
-  if (n->C > kMaxNormC) return fail(SVDQ_EUNSUPPORTED, "C must be <= %lld", (long long)kMaxNormC);
+  if (n->C > kMaxNormC || n->groups > kMaxNormG)
+    return fail(SVDQ_EUNSUPPORTED, "C must be <= %lld and groups <= %d", (long long)kMaxNormC, kMaxNormG);
   if (n->act != SVDQ_GN_NONE && n->act != SVDQ_GN_SILU && n->act != SVDQ_GN_GELU)
     return fail(SVDQ_EUNSUPPORTED, "unknown activation %d", (int)n->act);
   if (!(n->eps > 0.0f && n->eps < 3.0e38f)) return fail(SVDQ_EINVAL, "eps must be positive and finite");

@@ -9,8 +9,9 @@ constexpr int64_t kI8Stage = 128;
 constexpr int64_t i8_ld(int64_t K) { return (K + kI8Stage - 1) / kI8Stage * kI8Stage; }
 // 127^2 K < 2^31
 constexpr int64_t kMaxInt8K = 131072;
-// the norm keeps per-channel values of a row in LDS
+// the norm keeps per-channel and per-group values in LDS
 constexpr int64_t kMaxNormC = 4096;
+constexpr int kMaxNormG = 1024;
 
 // Whether every row (from p, ld values apart; xdtype 0 fp32, 1 bf16) is 4-byte aligned.
 inline bool rows_aligned4(const void* p, int64_t ld, int xdtype) {

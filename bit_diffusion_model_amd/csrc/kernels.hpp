@@ -114,10 +114,13 @@ struct NormArgs {
   int xdtype;  // 0 fp32, 1 bf16
   int64_t bsx, ldx;
 };
-// The statistics' split: blocks of `chunk` positions, `parts` of them per image, `bytes` of workspace.
+// How the norm runs: one: a block per image and group, one launch; otherwise statistics in
+// `parts` blocks of `chunk` positions per image (join: a launch of their own joins them), and an output
+// pass of `blocks` blocks of `rows` positions per image.  bytes: workspace of the statistics.
 struct NormPlan {
-  int64_t chunk;
-  uint32_t parts;
+  bool one, join;
+  int64_t chunk, rows;
+  uint32_t parts, blocks;
   size_t bytes;
 };
 NormPlan plan_norm(int64_t B, int64_t S, int C, int G);
