@@ -40,6 +40,12 @@ svdq_status check_dims_int8(const svdq_int8_layer* L) {
   return SVDQ_OK;
 }
 
+// the product's tiles are counted in 31 bits
+svdq_status check_tiles(int64_t M, int64_t N) {
+  if (((M + 63) / 64) * ((N + 63) / 64) > kMaxRows) return fail(SVDQ_EUNSUPPORTED, "M * N must be < 2^43");
+  return SVDQ_OK;
+}
+
 svdq_status check_layer_int8(const svdq_int8_layer* L) {
   svdq_status st = check_dims_int8(L);
   if (st != SVDQ_OK) return st;
@@ -65,6 +71,7 @@ svdq_status check_in(const void* X, int32_t xdtype, int64_t ldx, int64_t K) {
   if (!X) return fail(SVDQ_EINVAL, "X must be non-NULL");
   if (!aligned(X, xdtype == SVDQ_F32 ? 4 : 2)) return fail(SVDQ_EINVAL, "X must be aligned to its element size");
   if (ldx < K) return fail(SVDQ_EINVAL, "ldx must be >= the row's length");
+  if (ldx > kMaxRows) return fail(SVDQ_EUNSUPPORTED, "ldx must be < 2^31");
   return SVDQ_OK;
 }
 
@@ -101,6 +108,7 @@ svdq_status norm_args(const svdq_group_norm_desc* n, int64_t B, int64_t S, const
   svdq_status st = check_in(X, xdtype, ldx, n->C);
   if (st != SVDQ_OK) return st;
   // images must not overlap (with one image the stride is not used)
+  if (B > 1 && bsx >= (int64_t(1) << 46)) return fail(SVDQ_EUNSUPPORTED, "bsx must be < 2^46");
   if (B > 1 && (bsx < n->C || (bsx < (S - 1) * ldx + n->C && ldx < (B - 1) * bsx + n->C)))
     return fail(SVDQ_EINVAL, "bsx must be >= (S - 1) * ldx + C");
   a = NormArgs{B, S, (int)n->C, n->groups, n->act, n->eps, n->gamma, n->beta, X, xdtype, B > 1 ? bsx : 0, ldx};
@@ -113,6 +121,7 @@ svdq_status run_gemm(const svdq_int8_layer* L, int64_t M, const int8_t* qX, cons
                      int32_t ydtype, void* ws, size_t ws_bytes, void* stream) {
   svdq_status st = check_codes(qX, sX);
   if (st != SVDQ_OK || (st = check_out(Y, ldy, L->N, ydtype)) != SVDQ_OK) return st;
+  if ((st = check_tiles(M, L->N)) != SVDQ_OK) return st;
   hipError_t e = launch_w8a8(M, L->K, L->N, qX, sX, L->qW, L->sW, L->bias, Y, ldy, ydtype, ws, (hipStream_t)stream);
   if (e != hipSuccess) return fail(SVDQ_EHIP, "W8A8 product launch: %s", hipGetErrorString(e));
   return ok();
@@ -163,7 +172,9 @@ svdq_status svdq_linear_forward_int8(const svdq_int8_layer* layer, int64_t M, co
   svdq_status st = check_layer_int8(layer);
   if (st != SVDQ_OK || (st = check_rows(M)) != SVDQ_OK) return st;
   if (M == 0) return ok();
-  if ((st = check_in(X, xdtype, ldx, layer->K)) != SVDQ_OK || (st = check_out(Y, ldy, layer->N, ydtype)) != SVDQ_OK) return st;
+  if ((st = check_in(X, xdtype, ldx, layer->K)) != SVDQ_OK || (st = check_out(Y, ldy, layer->N, ydtype)) != SVDQ_OK ||
+      (st = check_tiles(M, layer->N)) != SVDQ_OK)
+    return st;
   if ((st = check_ws(workspace, ws_bytes, svdq_int8_workspace_bytes(layer, M, xdtype))) != SVDQ_OK) return st;
   hipError_t e;
   if (few_layer(M, layer->K)) {
@@ -196,6 +207,7 @@ svdq_status svdq_group_norm(const svdq_group_norm_desc* norm, int64_t B, int64_t
   if ((st = norm_args(norm, B, S, X, xdtype, bsx, ldx, a)) != SVDQ_OK) return st;
   if (ydtype != SVDQ_F32 && ydtype != SVDQ_BF16) return fail(SVDQ_EUNSUPPORTED, "unsupported output dtype %d", (int)ydtype);
   if ((st = check_out(Y, ldy, norm->C, ydtype)) != SVDQ_OK) return st;
+  if (B > 1 && bsy >= (int64_t(1) << 46)) return fail(SVDQ_EUNSUPPORTED, "bsy must be < 2^46");
   if (B > 1 && (bsy < norm->C || (bsy < (S - 1) * ldy + norm->C && ldy < (B - 1) * bsy + norm->C)))
     return fail(SVDQ_EINVAL, "bsy must be >= (S - 1) * ldy + C");
   if ((st = check_ws(workspace, ws_bytes, svdq_group_norm_workspace_bytes(norm, B, S))) != SVDQ_OK) return st;
@@ -238,7 +250,7 @@ svdq_status svdq_norm_linear_forward_int8(const svdq_group_norm_desc* norm, cons
   const int64_t M = B * S;
   NormArgs a;
   if ((st = norm_args(norm, B, S, X, xdtype, bsx, ldx, a)) != SVDQ_OK ||
-      (st = check_out(Y, ldy, layer->N, ydtype)) != SVDQ_OK ||
+      (st = check_out(Y, ldy, layer->N, ydtype)) != SVDQ_OK || (st = check_tiles(M, layer->N)) != SVDQ_OK ||
       (st = check_ws(workspace, ws_bytes, svdq_norm_linear_int8_workspace_bytes(norm, layer, B, S))) != SVDQ_OK)
     return st;
   uint8_t* base = static_cast<uint8_t*>(workspace);

@@ -72,10 +72,33 @@ struct Row<uint16_t, false> {
 // and a NaN or an infinity (0x7F800000 and above) is larger than every finite value.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = umax(v, (uint32_t)__shfl_xor((int)v, m, 64));
+
+// A reduction over groups of L lanes (16, 32 or 64) by lane moves in the vector unit (no LDS
+// round trips): two quad permutations, two rotations of a row of 16, then the row and half
+// swaps.  Every lane gets its group's result.
+template <int L, typename F>
+__device__ __forceinline__ uint32_t lane_reduce(uint32_t v, F f) {
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));   // quad [1 0 3 2]
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));   // quad [2 3 0 1]
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, true));  // row rotated by 4
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true));  // row rotated by 8
+  if constexpr (L >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = f(r[0], r[1]);
+  }
+  if constexpr (L >= 64) {
+    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = f(h[0], h[1]);
+  }
   return v;
+}
+template <int L = 64>
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  return lane_reduce<L>(v, [](uint32_t a, uint32_t b) { return umax(a, b); });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  return __uint_as_float(lane_reduce<64>(
+      __float_as_uint(v), [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); }));
 }
 
 // A row's scale s = a / 127 and the factor r = 127 / a of its codes (both IEEE quotients), from

@@ -437,11 +437,8 @@ __global__ __launch_bounds__(64 * FEW_NW) __attribute__((amdgpu_waves_per_eu(6, 
       }
     }
   }
-  // the rows' reductions side by side: one shuffle's latency per step, not one per row
 #pragma unroll
-  for (int step = 32; step >= 1; step >>= 1)
-#pragma unroll
-    for (int m = 0; m < RM; ++m) top[m] = umax(top[m], (uint32_t)__shfl_xor((int)top[m], step, 64));
+  for (int m = 0; m < RM; ++m) top[m] = wave_umax(top[m]);
   if (lane == 0) {
 #pragma unroll
     for (int m = 0; m < RM; ++m) tops[m][wave] = top[m];

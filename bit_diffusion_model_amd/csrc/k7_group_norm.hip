@@ -11,14 +11,14 @@
 //    thread of 1024);
 //  * k7_stats, then k7_apply (or k7_apply_quant): statistics per block of positions, and the
 //    output pass, which first joins the blocks' statistics (by itself where there are few,
-//    after k7_join where there are many).  A thread keeps the same V consecutive channels over
+//    after k7_join where there are many: an output block would read them all).  A thread keeps the same V consecutive channels over
 //    all its positions, so group boundaries may fall anywhere: sums are kept per channel and
 //    meet per group in LDS.
-// Statistics in fp32 without cancellation: a block's pivot p is the mean of the first rows that
-// it holds in registers; it sums d = x - p and d^2, so (mean, M2) = (p + sum d / n, sum d^2 -
-// (sum d)^2 / n); blocks are joined in fp64 around the first block's mean m_0: mean = m_0 +
-// sum n_i (m_i - m_0) / n, M2 = sum (M2_i + n_i (m_i - m_0)^2) - n (mean - m_0)^2 (the pairwise
-// formula of Chan, Golub and LeVeque, summed).
+// Statistics in fp32: a thread sums d = x - p and d^2 per channel, p its first value, so that
+// (mean, M2) = (p + sum d / n, sum d^2 - (sum d)^2 / n): since p is one of the n values, M2 >=
+// (p - mean)^2 and the subtraction loses at most a factor n (the thread's positions, 32 or so).
+// Threads, then blocks, are joined by mean = sum n_i mean_i / n, M2 = sum (M2_i + n_i (mean_i -
+// mean)^2) (the pairwise formula of Chan, Golub and LeVeque, summed).
 #include <type_traits>
 
 #include "../../include/svdq.h"
@@ -28,7 +28,7 @@
 namespace svdq {
 namespace {
 
-constexpr int GN_NT = 256;
+constexpr int ST_NT = 256, AP_NT = 256;  // threads of the statistics and output passes (1024: 16-27 us for 10)
 
 // ---- vectors of V channels; rows are 4-byte aligned for V > 1
 
@@ -81,7 +81,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-template <typename TY, int V>
+template <bool NT, typename P, typename W>
+__device__ __forceinline__ void put(P* p, W w) {
+  if constexpr (NT) __builtin_nontemporal_store(w, p);
+  else *p = w;
+}
+
+// NT: past the caches, for outputs that nothing reads before they are evicted
+template <typename TY, int V, bool NT = false>
 __device__ __forceinline__ void storev(TY* p, const float v[V]) {
   constexpr int W = V * (int)sizeof(TY) / 4;
   uint32_t w[W < 1 ? 1 : W];
@@ -95,7 +102,7 @@ __device__ __forceinline__ void storev(TY* p, const float v[V]) {
   if constexpr (W >= 4) {
 #pragma unroll
     for (int i = 0; i < W / 4; ++i)
-      reinterpret_cast<u32x4a*>(p)[i] = u32x4a{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+      put<NT>(reinterpret_cast<u32x4a*>(p) + i, u32x4a{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]});
   } else if constexpr (W == 2) {
     *reinterpret_cast<u32x2a*>(p) = u32x2a{w[0], w[1]};
   } else if constexpr (W == 1) {
@@ -113,12 +120,6 @@ __device__ __forceinline__ float norm_act(float y, int act) {
 }
 
 // ---- one launch: a block per (group, image)
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
-}
 
 // Sum over the block (at most 16 waves), in the same order on every call
 __device__ __forceinline__ float block_sum(float v, float* scratch) {
@@ -208,133 +209,95 @@ struct Place {
   int ct, rp, col, row;
   bool on;
 };
-__host__ __device__ __forceinline__ int place_ct(int cv) { return cv < GN_NT ? cv : GN_NT; }
+__host__ __device__ __forceinline__ int place_ct(int cv, int nt) { return cv < nt ? cv : nt; }
+template <int NT>
 __device__ __forceinline__ Place place(int cv) {
   Place p;
-  p.ct = place_ct(cv);
-  p.rp = GN_NT / p.ct;
-  p.col = threadIdx.x % p.ct;
+  p.ct = place_ct(cv, NT);
+  p.rp = NT / p.ct;
   p.row = threadIdx.x / p.ct;
+  p.col = threadIdx.x - p.row * p.ct;
   p.on = p.row < p.rp;
   return p;
 }
 
-// Sums per group of the block's per-channel values red[r][c] (r < rp, C channels): out[g].
-// 2^k threads per group (as many as there are), joined by shuffles inside a wave.
-__device__ __forceinline__ void group_sums(const float2* red, int rp, int C, int G, float2* out) {
+// Joins the threads' statistics red[r][c] = (mean, M2) (r < rp: positions r, r + rp, .. of `rows`)
+// per group: out[g] = (mean, M2).  2^k threads per group (as many as there are), shuffles in a wave.
+__device__ __forceinline__ void group_stats(const float2* red, int rp, int rows, int C, int G, float2* __restrict__ out) {
   const int cpg = C / G;
   int tpg = 1;
-  while (tpg < 64 && tpg * 2 * G <= GN_NT) tpg *= 2;
-  const int per = GN_NT / tpg, dr = tpg / cpg, dc = tpg - dr * cpg;
+  while (tpg < 64 && tpg * 2 * G <= ST_NT) tpg *= 2;
+  const int per = ST_NT / tpg, dr = tpg / cpg, dc = tpg - dr * cpg, t = threadIdx.x % tpg;
+  const int full = rows / rp, more = rows - full * rp;  // rows of threads r < more have one position more
+  const int top = rows < rp ? rows : rp;
   for (int g0 = 0; g0 < G; g0 += per) {
-    const int g = g0 + threadIdx.x / tpg, t = threadIdx.x % tpg;
-    float2 s = make_float2(0.0f, 0.0f);
-    if (g < G) {
+    const int g = g0 + threadIdx.x / tpg;
+    const float2* at = red + (g < G ? g : 0) * cpg;
+    const float m0 = at[0].x;
+    auto each = [&](auto f) {
+      float s = 0.0f;
       int r = t / cpg, c = t - r * cpg;
-      while (r < rp) {
-        const float2 v = red[r * C + g * cpg + c];
-        s.x += v.x, s.y += v.y;
+      while (r < top) {
+        s += f((float)(full + (r < more)), at[r * C + c]);
         c += dc, r += dr;
         if (c >= cpg) c -= cpg, ++r;
       }
-    }
-    for (int m = tpg / 2; m >= 1; m >>= 1) s.x += __shfl_xor(s.x, m, 64), s.y += __shfl_xor(s.y, m, 64);
-    if (g < G && t == 0) out[g] = s;
+      for (int m = tpg / 2; m >= 1; m >>= 1) s += __shfl_xor(s, m, 64);
+      return s;
+    };
+    const float mean = m0 + each([&](float n, float2 v) { return n * (v.x - m0); }) / ((float)rows * (float)cpg);
+    const float m2 = each([&](float n, float2 v) { return v.y + n * (v.x - mean) * (v.x - mean); });
+    if (g < G && t == 0) out[g] = make_float2(mean, m2);
   }
 }
 
 // Statistics of positions [blockIdx.x * chunk, + chunk) of image blockIdx.y: part[b][i][g] =
-// (mean, M2).  LDS: red [rp C], gsum [G] (float2), piv [G].  HELD rows per thread stay in
-// registers while the pivot is found; with more than GN_NT columns they are read again.
+// (mean, M2).  LDS: red [rp C].
 template <typename T, int V>
-__global__ __launch_bounds__(GN_NT) void k7_stats(const T* __restrict__ X, int64_t bsx, int64_t ldx, int64_t S, int C,
+__global__ __launch_bounds__(ST_NT) void k7_stats(const T* __restrict__ X, int64_t bsx, int64_t ldx, int64_t S, int C,
                                                   int G, int64_t chunk, float2* __restrict__ part) {
   extern __shared__ float lds[];
-  constexpr int HELD = 8;
-  const int cv = C / V, cpg = C / G;
-  const Place pl = place(cv);
+  constexpr int U = 8;  // loads in flight
+  const int cv = C / V;
+  const Place pl = place<ST_NT>(cv);
   float2* red = reinterpret_cast<float2*>(lds);
-  float2* gsum = red + pl.rp * C;
-  float* piv = reinterpret_cast<float*>(gsum + G);
   const int64_t r0 = (int64_t)blockIdx.x * chunk;
   const int rows = (int)(r0 + chunk < S ? chunk : S - r0);
   const T* x = X + blockIdx.y * bsx + r0 * ldx;
-  const int first = rows < HELD * pl.rp ? rows : HELD * pl.rp;
-
-  Vec<T, V> raw[HELD];
-  for (int c = pl.col; c < cv && pl.on; c += pl.ct) {
+  if (pl.on && pl.row < rows)
+    for (int c = pl.col; c < cv; c += pl.ct) {
+      float p[V], s[V] = {}, q[V] = {};
+      for (int i = pl.row; i < rows; i += U * pl.rp) {
+        Vec<T, V> raw[U];
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) {
-      const int r = pl.row + i * pl.rp;
-      raw[i] = loadv<T, V>(x + (r < rows ? r : 0) * ldx + c * V);
-    }
-    float s[V] = {};
+        for (int j = 0; j < U; ++j) {
+          const int r = i + j * pl.rp;
+          raw[j] = loadv<T, V>(x + (r < rows ? r : i) * ldx + c * V);
+        }
+        if (i == pl.row) valuev<T, V>(raw[0], p);
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) {
-      float v[V];
-      valuev<T, V>(raw[i], v);
+        for (int j = 0; j < U; ++j) {
+          float v[V];
+          valuev<T, V>(raw[j], v);
+          const bool in = i + j * pl.rp < rows;
 #pragma unroll
-      for (int e = 0; e < V; ++e) s[e] += pl.row + i * pl.rp < rows ? v[e] : 0.0f;
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) red[pl.row * C + c * V + e] = make_float2(s[e], 0.0f);
-  }
-  __syncthreads();
-  group_sums(red, pl.rp, C, G, gsum);
-  __syncthreads();
-  for (int g = threadIdx.x; g < G; g += GN_NT) piv[g] = gsum[g].x / (float)(first * cpg);
-  __syncthreads();
-
-  for (int c = pl.col; c < cv && pl.on; c += pl.ct) {
-    float p[V], s[V] = {}, q[V] = {};
-    {
-      int g = c * V / cpg, in = c * V - g * cpg;
+          for (int e = 0; e < V; ++e) {
+            const float d = in ? v[e] - p[e] : 0.0f;
+            s[e] += d;
+            q[e] += d * d;
+          }
+        }
+      }
+      const float n = (float)((rows - pl.row + pl.rp - 1) / pl.rp);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        p[e] = piv[g];
-        if (++in == cpg) in = 0, ++g;
+        // (a NaN passes: only a negative remainder of rounding is cut off)
+        const float m2 = q[e] - s[e] * (s[e] / n);
+        red[pl.row * C + c * V + e] = make_float2(p[e] + s[e] / n, m2 < 0.0f ? 0.0f : m2);
       }
     }
-    auto add = [&](const Vec<T, V>& w, bool on) {
-      float v[V];
-      valuev<T, V>(w, v);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float d = on ? v[e] - p[e] : 0.0f;
-        s[e] += d;
-        q[e] += d * d;
-      }
-    };
-    if (cv > GN_NT) {  // several columns per thread: the registers hold the last one's rows
-#pragma unroll
-      for (int i = 0; i < HELD; ++i) {
-        const int r = pl.row + i * pl.rp;
-        raw[i] = loadv<T, V>(x + (r < rows ? r : 0) * ldx + c * V);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < HELD; ++i) add(raw[i], pl.row + i * pl.rp < rows);
-    // the rest, HELD rows' loads in flight at once
-    for (int i = pl.row + HELD * pl.rp; i < rows; i += HELD * pl.rp) {
-#pragma unroll
-      for (int j = 0; j < HELD; ++j) {
-        const int r = i + j * pl.rp;
-        raw[j] = loadv<T, V>(x + (r < rows ? r : 0) * ldx + c * V);
-      }
-#pragma unroll
-      for (int j = 0; j < HELD; ++j) add(raw[j], i + j * pl.rp < rows);
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) red[pl.row * C + c * V + e] = make_float2(s[e], q[e]);
-  }
   __syncthreads();
-  group_sums(red, pl.rp, C, G, gsum);
-  __syncthreads();
-  for (int g = threadIdx.x; g < G; g += GN_NT) {
-    const double n = (double)rows * cpg, d = gsum[g].x;
-    part[((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * G + g] =
-        make_float2((float)(piv[g] + d / n), (float)fmax(gsum[g].y - d * d / n, 0.0));
-  }
+  group_stats(red, pl.rp, rows, C, G, part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * G);
 }
 
 // ---- joining the blocks' statistics
@@ -347,88 +310,118 @@ struct Stats {
   float eps;
 };
 
-struct Join {
-  double n, d, q;
-};
-// One block's (mean, M2) around m0
-__device__ __forceinline__ void join_add(Join& j, const Stats& st, int i, float2 v, float m0) {
-  const double n = (double)((i + 1) * st.chunk < st.S ? st.chunk : st.S - i * st.chunk) * (st.C / st.G);
-  const double d = (double)v.x - (double)m0;
-  j.n += n;
-  j.d += n * d;
-  j.q += (double)v.y + n * d * d;
-}
-// A NaN or an infinity leaves NaN statistics, as the formula does (the maximum would drop it)
-__device__ __forceinline__ float2 join_end(const Join& j, float m0, float eps) {
-  const double d = j.d / j.n;
-  double var = j.q / j.n - d * d;
-  if (var < 0.0) var = 0.0;
-  return make_float2((float)((double)m0 + d), 1.0f / sqrtf((float)var + eps));
+// Positions that block i covered, times channels of a group
+__device__ __forceinline__ float part_count(const Stats& st, int i) {
+  const int64_t rows = i + 1 < st.parts ? st.chunk : st.S - (st.parts - 1) * st.chunk;
+  return (float)rows * (float)(st.C / st.G);
 }
 
-// (mean, rstd) of all groups of image b into out[G] (LDS); 256 threads, scratch [256]
-__device__ __forceinline__ void join_groups(const Stats& st, int64_t b, float2* out, Join* scratch) {
+// (mean, rstd) of all groups of image b into out[G] (LDS); AP_NT threads, scratch [AP_NT].  Threads
+// side by side take groups side by side; rows of threads share a group's parts.  One round
+// of loads where a thread has at most 16 parts (the usual case), two for the rest.
+__device__ __forceinline__ void join_groups(const Stats& st, int64_t b, float2* out, double* scratch) {
   if (st.parts == 0) {
-    for (int g = threadIdx.x; g < st.G; g += GN_NT) out[g] = st.at[b * st.G + g];
+    for (int g = threadIdx.x; g < st.G; g += AP_NT) out[g] = st.at[b * st.G + g];
     __syncthreads();
     return;
   }
+  constexpr int U = 16;
   const float2* p = st.at + b * st.parts * (int64_t)st.G;
-  const int width = st.G < GN_NT ? st.G : GN_NT, rows = GN_NT / width;
+  const int width = st.G < AP_NT ? st.G : AP_NT, rows = AP_NT / width;
+  const int col = (int)threadIdx.x % width, r = (int)threadIdx.x / width;
+  const float full = part_count(st, 0), last = part_count(st, st.parts - 1), n = (float)st.S * (float)(st.C / st.G);
+  auto across = [&](double v) {  // over the rows of threads, in their order
+    scratch[threadIdx.x] = v;
+    __syncthreads();
+    double s = 0.0;
+    for (int i = 0; i < rows; ++i) s += scratch[i * width + col];
+    __syncthreads();
+    return s;
+  };
   for (int g0 = 0; g0 < st.G; g0 += width) {
-    const int g = g0 + (int)threadIdx.x % width, r = (int)threadIdx.x / width;
-    Join j = {0.0, 0.0, 0.0};
+    const int g = g0 + col;
     const bool on = r < rows && g < st.G;
-    const float m0 = on ? p[g].x : 0.0f;
-    if (on)
-      for (int i = r; i < st.parts; i += rows) join_add(j, st, i, p[(int64_t)i * st.G + g], m0);
-    scratch[threadIdx.x] = j;
-    __syncthreads();
-    if (on && r == 0) {
-      for (int i = 1; i < rows; ++i) {
-        const Join o = scratch[i * width + (int)threadIdx.x];
-        j.n += o.n, j.d += o.d, j.q += o.q;
-      }
-      out[g] = join_end(j, m0, st.eps);
+    const float2* q = p + (on ? g : 0);
+    const int parts = on ? st.parts : 0;
+    float2 v[U];
+    auto load = [&](int i) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = q[(i + u * rows < parts ? i + u * rows : 0) * st.G];
+    };
+    auto count = [&](int i) { return i < parts ? (i + 1 < parts ? full : last) : 0.0f; };
+    load(r);
+    double s = 0.0;
+    for (int i = r; i < parts; i += U * rows) {
+      if (i != r) load(i);
+#pragma unroll
+      for (int u = 0; u < U; ++u) s += (double)count(i + u * rows) * (double)v[u].x;
     }
-    __syncthreads();
+    const float mean = (float)(across(s) / (double)n);
+    float m2 = 0.0f;
+    for (int i = r; i < parts; i += U * rows) {
+      if (parts > r + U * rows) load(i);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float d = v[u].x - mean;
+        m2 += i + u * rows < parts ? v[u].y + count(i + u * rows) * d * d : 0.0f;
+      }
+    }
+    const float var = (float)across(m2) / n;
+    if (on && r == 0) out[g] = make_float2(mean, 1.0f / sqrtf(var + st.eps));
   }
+  __syncthreads();
 }
 
 // Many blocks: group blockIdx.x of image blockIdx.y by a block of its own
-__global__ __launch_bounds__(GN_NT) void k7_join(Stats st, float2* __restrict__ out) {
-  __shared__ Join scratch[GN_NT];
+constexpr int JN_NT = 256;
+__global__ __launch_bounds__(JN_NT) void k7_join(Stats st, float2* __restrict__ out) {
+  __shared__ float scratch[16];
+  constexpr int U = 4;
   const float2* p = st.at + (int64_t)blockIdx.y * st.parts * st.G + blockIdx.x;
+  const float full = part_count(st, 0), last = part_count(st, st.parts - 1), n = (float)st.S * (float)(st.C / st.G);
+  auto count = [&](int i) { return i < st.parts ? (i + 1 < st.parts ? full : last) : 0.0f; };
+  float2 v[U];
+  auto load = [&](int i) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = p[(int64_t)(i + u * JN_NT < st.parts ? i + u * JN_NT : 0) * st.G];
+  };
+  load(threadIdx.x);
   const float m0 = p[0].x;
-  Join j = {0.0, 0.0, 0.0};
-  for (int i = threadIdx.x; i < st.parts; i += GN_NT) join_add(j, st, i, p[(int64_t)i * st.G], m0);
-  scratch[threadIdx.x] = j;
-  for (int m = GN_NT / 2; m >= 1; m >>= 1) {
-    __syncthreads();
-    if ((int)threadIdx.x < m) {
-      const Join o = scratch[threadIdx.x + m];
-      j.n += o.n, j.d += o.d, j.q += o.q;
-      scratch[threadIdx.x] = j;
+  float s = 0.0f;
+  for (int i = threadIdx.x; i < st.parts; i += U * JN_NT) {
+    if (i != (int)threadIdx.x) load(i);
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += count(i + u * JN_NT) * (v[u].x - m0);
+  }
+  const float mean = m0 + block_sum(s, scratch) / n;
+  float m2 = 0.0f;
+  for (int i = threadIdx.x; i < st.parts; i += U * JN_NT) {
+    if (st.parts > U * JN_NT) load(i);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float d = v[u].x - mean;
+      m2 += i + u * JN_NT < st.parts ? v[u].y + count(i + u * JN_NT) * d * d : 0.0f;
     }
   }
-  if (threadIdx.x == 0) out[(int64_t)blockIdx.y * st.G + blockIdx.x] = join_end(j, m0, st.eps);
+  m2 = block_sum(m2, scratch);
+  if (threadIdx.x == 0) out[(int64_t)blockIdx.y * st.G + blockIdx.x] = make_float2(mean, 1.0f / sqrtf(m2 / n + st.eps));
 }
 
 // ---- the output pass
 
 // Positions [i * chunk, + chunk) of image blockIdx.y, i counted from the end: the statistics pass
 // ended there, so that part of x is the likeliest to be in cache still.
-template <typename T, typename TY, int V>
-__global__ __launch_bounds__(GN_NT) void k7_apply(const T* __restrict__ X, int64_t bsx, int64_t ldx, int64_t chunk,
+template <typename T, typename TY, int V, bool NT>
+__global__ __launch_bounds__(AP_NT) void k7_apply(const T* __restrict__ X, int64_t bsx, int64_t ldx, int64_t chunk,
                                                   Stats st, const float* __restrict__ gamma,
                                                   const float* __restrict__ beta, int act, TY* __restrict__ Y,
                                                   int64_t bsy, int64_t ldy) {
   extern __shared__ float lds[];
-  __shared__ Join scratch[GN_NT];
+  __shared__ double scratch[AP_NT];
   float2* stat = reinterpret_cast<float2*>(lds);
-  constexpr int U = 4;
+  constexpr int U = 8;
   const int C = st.C, cv = C / V, cpg = C / st.G;
-  const Place pl = place(cv);
+  const Place pl = place<AP_NT>(cv);
   const int64_t r0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * chunk;
   const int rows = (int)(r0 + chunk < st.S ? chunk : st.S - r0);
   const T* x = X + blockIdx.y * bsx + r0 * ldx;
@@ -441,20 +434,30 @@ __global__ __launch_bounds__(GN_NT) void k7_apply(const T* __restrict__ X, int64
       raw[u] = loadv<T, V>(x + (r < rows ? r : 0) * ldx + c * V);
     }
   };
-  if (pl.on) load(pl.col, pl.row);  // under way while the statistics are joined
+  float a[V], b[V];
+  auto affine = [&](int c) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      a[e] = gamma ? gamma[c * V + e] : 1.0f;
+      b[e] = beta ? beta[c * V + e] : 0.0f;
+    }
+  };
+  if (pl.on) {  // under way while the statistics are joined
+    load(pl.col, pl.row);
+    affine(pl.col);
+  }
   join_groups(st, blockIdx.y, stat, scratch);
   if (!pl.on) return;
   for (int c = pl.col; c < cv; c += pl.ct) {
-    float mean[V], a[V], b[V];
+    if (c != pl.col) load(c, pl.row), affine(c);
+    float mean[V];
     int g = c * V / cpg, in = c * V - g * cpg;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       mean[e] = stat[g].x;
-      a[e] = stat[g].y * (gamma ? gamma[c * V + e] : 1.0f);
-      b[e] = beta ? beta[c * V + e] : 0.0f;
+      a[e] *= stat[g].y;
       if (++in == cpg) in = 0, ++g;
     }
-    if (c != pl.col) load(c, pl.row);
     for (int i = pl.row; i < rows; i += U * pl.rp) {
       if (i != pl.row) load(c, i);
 #pragma unroll
@@ -465,7 +468,7 @@ __global__ __launch_bounds__(GN_NT) void k7_apply(const T* __restrict__ X, int64
         valuev<T, V>(raw[u], v);
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = norm_act((v[e] - mean[e]) * a[e] + b[e], act);
-        storev<TY, V>(y + r * ldy + c * V, v);
+        storev<TY, V, NT>(y + r * ldy + c * V, v);
       }
     }
   }
@@ -475,13 +478,13 @@ __global__ __launch_bounds__(GN_NT) void k7_apply(const T* __restrict__ X, int64
 // 512 channels in registers.  Per channel (mean, rstd gamma, beta, inv_s) wait in LDS, eight planes
 // of C / 8 so that neighbouring lanes read neighbouring 16 bytes.
 template <typename T, bool VEC, int NC>
-__global__ __launch_bounds__(GN_NT) void k7_apply_quant(const T* __restrict__ X, int64_t bsx, int64_t ldx,
+__global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X, int64_t bsx, int64_t ldx,
                                                         int64_t chunk, Stats st, const float* __restrict__ gamma,
                                                         const float* __restrict__ beta, int act,
                                                         const float* __restrict__ inv_s, int8_t* __restrict__ qX,
                                                         int64_t ldq, float* __restrict__ sX) {
   extern __shared__ __attribute__((aligned(16))) float lds[];
-  __shared__ Join scratch[GN_NT];
+  __shared__ double scratch[AP_NT];
   const int C = st.C, cpg = C / st.G, c8 = (C + 7) / 8;
   float4* coef = reinterpret_cast<float4*>(lds);
   float2* stat = reinterpret_cast<float2*>(coef + 8 * c8);
@@ -496,17 +499,19 @@ __global__ __launch_bounds__(GN_NT) void k7_apply_quant(const T* __restrict__ X,
 #pragma unroll
     for (int j = 0; j < NC; ++j) raw[j] = x.load(8 * lane + 512 * j);
   }
+  // gamma, beta and inv_s while the statistics are joined; channels past C: value act(0) * 0
+  for (int c = threadIdx.x; c < 8 * c8; c += AP_NT)
+    coef[(c & 7) * c8 + (c >> 3)] = c < C ? make_float4(0.0f, gamma ? gamma[c] : 1.0f, beta ? beta[c] : 0.0f,
+                                                        inv_s ? inv_s[c] : 1.0f)
+                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   join_groups(st, blockIdx.y, stat, scratch);
-  for (int c = threadIdx.x; c < 8 * c8; c += GN_NT) {
-    float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // channels past C: value act(0) * 0
-    if (c < C) {
-      const float2 s = stat[c / cpg];
-      f = make_float4(s.x, s.y * (gamma ? gamma[c] : 1.0f), beta ? beta[c] : 0.0f, inv_s ? inv_s[c] : 1.0f);
-    }
-    coef[(c & 7) * c8 + (c >> 3)] = f;
+  for (int c = threadIdx.x; c < C; c += AP_NT) {
+    const float2 s = stat[c / cpg];
+    float4& f = coef[(c & 7) * c8 + (c >> 3)];
+    f.x = s.x, f.y *= s.y;
   }
   __syncthreads();
-  for (int i = wave; i < rows; i += 4) {
+  for (int i = wave; i < rows; i += AP_NT / 64) {
     const RowX x = row_at(i);
     float v[NC][8];
     uint32_t a = 0;
@@ -522,7 +527,7 @@ __global__ __launch_bounds__(GN_NT) void k7_apply_quant(const T* __restrict__ X,
         a = umax(a, abs_bits(v[j][e]));
       }
     }
-    const RowX next = row_at(i + 4);  // the next row's loads under this row's reduction
+    const RowX next = row_at(i + AP_NT / 64);  // the next row's loads under this row's reduction
 #pragma unroll
     for (int j = 0; j < NC; ++j) raw[j] = next.load(8 * lane + 512 * j);
     float s, r;
@@ -536,6 +541,71 @@ __global__ __launch_bounds__(GN_NT) void k7_apply_quant(const T* __restrict__ X,
                                                                    codes4(v[j][4], v[j][5], v[j][6], v[j][7], r));
     }
     if (lane == 0) sX[row] = s;
+  }
+}
+
+// The same for narrow rows (C <= 8 LPR, a multiple of 8; rows 4-byte aligned): LPR lanes per row, 64 /
+// LPR rows per wave at once; a lane keeps its 8 channels' coefficients in registers.
+template <typename T, int LPR>
+__global__ __launch_bounds__(AP_NT) void k7_apply_quant_narrow(const T* __restrict__ X, int64_t bsx, int64_t ldx,
+                                                               int64_t chunk, Stats st, const float* __restrict__ gamma,
+                                                               const float* __restrict__ beta, int act,
+                                                               const float* __restrict__ inv_s,
+                                                               int8_t* __restrict__ qX, int64_t ldq,
+                                                               float* __restrict__ sX) {
+  extern __shared__ __attribute__((aligned(16))) float lds[];
+  __shared__ double scratch[AP_NT];
+  float2* stat = reinterpret_cast<float2*>(lds);
+  constexpr int U = 4, STEP = AP_NT / LPR;
+  const int C = st.C, cpg = C / st.G;
+  const int li = threadIdx.x % LPR, first = threadIdx.x / LPR, c = 8 * li;
+  const bool on = c < C;
+  const int64_t r0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * chunk;
+  const int rows = (int)(r0 + chunk < st.S ? chunk : st.S - r0);
+  const T* x = X + blockIdx.y * bsx + r0 * ldx + (on ? c : 0);
+  Vec<T, 8> raw[U];
+  auto load = [&](int i) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u] = loadv<T, 8>(x + (i + u * STEP < rows ? i + u * STEP : 0) * ldx);
+  };
+  load(first);
+  float a[8], b[8], f[8], mean[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    a[e] = on ? (gamma ? gamma[c + e] : 1.0f) : 0.0f;
+    b[e] = on && beta ? beta[c + e] : 0.0f;
+    f[e] = on ? (inv_s ? inv_s[c + e] : 1.0f) : 0.0f;
+  }
+  join_groups(st, blockIdx.y, stat, scratch);
+  int g = (on ? c : 0) / cpg, in = (on ? c : 0) - g * cpg;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    mean[e] = stat[g].x;
+    a[e] *= stat[g].y;
+    if (++in == cpg) in = 0, g = g + 1 < st.G ? g + 1 : g;
+  }
+  for (int i = first; i < rows + first; i += U * STEP) {  // whole rows of lanes stay together
+    if (i != first) load(i);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = i + u * STEP;
+      float v[8];
+      valuev<T, 8>(raw[u], v);
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = on ? norm_act((v[e] - mean[e]) * a[e] + b[e], act) * f[e] : 0.0f;
+        top = umax(top, abs_bits(v[e]));
+      }
+      float s, q;
+      row_scale(wave_umax<LPR>(top), s, q);
+      if (r >= rows) continue;
+      const int64_t row = blockIdx.y * st.S + r0 + r;
+      if (c < ldq)
+        *reinterpret_cast<uint2*>(qX + row * ldq + c) =
+            make_uint2(codes4(v[0], v[1], v[2], v[3], q), codes4(v[4], v[5], v[6], v[7], q));
+      if (li == 0) sX[row] = s;
+    }
   }
 }
 
@@ -578,18 +648,24 @@ void launch_one(const NormArgs& a, int width, void* Y, int64_t bsy, int64_t ldy,
 
 template <typename T, int V>
 void launch_stats(const NormArgs& a, const NormPlan& p, float2* part, hipStream_t st) {
-  const int rp = GN_NT / place_ct(a.C / V);
-  const size_t bytes = (size_t)rp * a.C * 8 + (size_t)a.G * 12;
-  hipLaunchKernelGGL((k7_stats<T, V>), dim3(p.parts, (uint32_t)a.B), dim3(GN_NT), bytes, st,
+  const int rp = ST_NT / place_ct(a.C / V, ST_NT);
+  const size_t bytes = (size_t)rp * a.C * 8;
+  hipLaunchKernelGGL((k7_stats<T, V>), dim3(p.parts, (uint32_t)a.B), dim3(ST_NT), bytes, st,
                      static_cast<const T*>(a.X), a.bsx, a.ldx, a.S, a.C, a.G, p.chunk, part);
 }
 
 template <typename T, typename TY, int V>
 void launch_apply(const NormArgs& a, const NormPlan& p, const Stats& s, void* Y, int64_t bsy, int64_t ldy,
                   hipStream_t st) {
-  hipLaunchKernelGGL((k7_apply<T, TY, V>), dim3(p.blocks, (uint32_t)a.B), dim3(GN_NT), (size_t)a.G * 8, st,
-                     static_cast<const T*>(a.X), a.bsx, a.ldx, p.rows, s, a.gamma, a.beta, a.act,
-                     static_cast<TY*>(Y), bsy, ldy);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(p.blocks, (uint32_t)a.B), dim3(AP_NT), (size_t)a.G * 8, st,
+                       static_cast<const T*>(a.X), a.bsx, a.ldx, p.rows, s, a.gamma, a.beta, a.act,
+                       static_cast<TY*>(Y), bsy, ldy);
+  };
+  if constexpr (V == 8) {  // x and y past the 256 MB cache: y would only push x out
+    if ((double)a.B * (double)a.S * a.C * (sizeof(T) + sizeof(TY)) > 268435456.0) return go(k7_apply<T, TY, V, true>);
+  }
+  go(k7_apply<T, TY, V, false>);
 }
 
 // Statistics for an output pass: by k7_one where a group fits a block, else by blocks of positions
@@ -609,7 +685,7 @@ Stats run_stats(const NormArgs& a, const NormPlan& p, void* ws, hipStream_t st) 
   s.parts = (int)p.parts;
   if (p.join) {
     float2* out = part + (size_t)a.B * p.parts * a.G;
-    hipLaunchKernelGGL(k7_join, dim3((uint32_t)a.G, (uint32_t)a.B), dim3(GN_NT), 0, st, s, out);
+    hipLaunchKernelGGL(k7_join, dim3((uint32_t)a.G, (uint32_t)a.B), dim3(JN_NT), 0, st, s, out);
     s.at = out;
     s.parts = 0;
   }
@@ -622,22 +698,25 @@ NormPlan plan_norm(int64_t B, int64_t S, int C, int G) {
   NormPlan p{};
   const int64_t cpg = C / G;
   p.one = S * cpg <= 32 * 1024;
-  // statistics: blocks of at least 8 rows per thread; up to 256 blocks joined by every output
-  // block itself, more (up to 1024) by a launch of their own
-  const int ct = place_ct(C % 8 == 0 ? C / 8 : C), rp = GN_NT / ct;
-  const int64_t least = 8 * rp;
-  auto split = [&](int64_t blocks) {
-    int64_t chunk = (S * B + blocks - 1) / blocks;
-    return chunk < least ? least : chunk;
-  };
-  p.chunk = split(256);
-  p.join = p.chunk * C > 131072;
-  if (p.join) p.chunk = split(1024);
+  // Measured (us, both launches or all three; statistics blocks / output blocks):
+  //   2x4096x320 bf16 256 / 256 14.9, 256 / 512 15.9, 256 joined apart / 256 16.5, 256 / 1024 20.8
+  //   1x16384x128 bf16 128 / 256 13.9, 256 / 256 16.5, 256 joined apart / 256 15.8
+  //   1x65536x256 bf16 512 joined apart / 768 31.1, 512 / 2048 38.2, 256 / 512 joined inside 35.2
+  //   1x262144x128 bf16 512 joined apart / 768 45.6, 256 / 512 joined inside 50.8
+  // so up to 2^23 values one block of each kind per CU, the output blocks joining at most 128 parts
+  // per image; above, a join of its own.
+  const int64_t n = B * S * C;
+  p.join = n > (int64_t(1) << 23);
+  int64_t parts = p.join ? (512 + B - 1) / B : (256 + B - 1) / B;
+  if (!p.join && parts > 128) parts = 128;
+  const int cv = C % 8 == 0 ? C / 8 : C, rp = 256 / place_ct(cv, 256);
+  p.chunk = (S + parts - 1) / parts;
+  if (p.chunk < 2 * rp) p.chunk = 2 * rp;
   p.parts = (uint32_t)((S + p.chunk - 1) / p.chunk);
   p.bytes = ((size_t)B * p.parts * G + (size_t)B * G) * sizeof(float2);
-  // the output pass: about 2048 blocks of at least 4 rows per thread
-  p.rows = (S * B + 2047) / 2048;
-  if (p.rows < 4 * rp) p.rows = 4 * rp;
+  const int64_t blocks = !p.join ? 256 : n <= (int64_t(1) << 25) ? 768 : 2048;
+  p.rows = (S * B + blocks - 1) / blocks;
+  if (p.rows < 2 * rp) p.rows = 2 * rp;
   p.blocks = (uint32_t)((S + p.rows - 1) / p.rows);
   return p;
 }
@@ -672,21 +751,27 @@ hipError_t launch_norm_quant(const NormArgs& a, const float* inv_s, int8_t* qX, 
   const bool vec = vec_ok(a.X, a.bsx, a.ldx, a.xdtype);
   const size_t bytes = (size_t)((a.C + 7) / 8) * 8 * 16 + (size_t)a.G * 8;
   const int64_t ldq = i8_ld(a.C);
-  // about 2048 blocks of at least 8 rows (two per wave)
-  int64_t rows = (a.S * a.B + 2047) / 2048;
-  if (rows < 8) rows = 8;
-  const dim3 g((uint32_t)((a.S + rows - 1) / rows), (uint32_t)a.B), b(GN_NT);
-  auto go = [&](auto kernel, auto x) {
-    hipLaunchKernelGGL(kernel, g, b, bytes, st, x, a.bsx, a.ldx, rows, s, a.gamma, a.beta, a.act, inv_s, qX, ldq, sX);
+  // as many blocks as the norm's output pass, of at least two rows per wave
+  const int64_t rows = p.rows < 8 ? 8 : p.rows;
+  const dim3 g((uint32_t)((a.S + rows - 1) / rows), (uint32_t)a.B), b(AP_NT);
+  auto go = [&](auto kernel, auto x, size_t lds) {
+    hipLaunchKernelGGL(kernel, g, b, lds, st, x, a.bsx, a.ldx, rows, s, a.gamma, a.beta, a.act, inv_s, qX, ldq, sX);
   };
   const float* x32 = static_cast<const float*>(a.X);
   const uint16_t* x16 = static_cast<const uint16_t*>(a.X);
   auto by_type = [&](auto nc) {
     constexpr int NC = decltype(nc)::value;
-    if (a.xdtype == 0) go(k7_apply_quant<float, true, NC>, x32);
-    else vec ? go(k7_apply_quant<uint16_t, true, NC>, x16) : go(k7_apply_quant<uint16_t, false, NC>, x16);
+    if (a.xdtype == 0) go(k7_apply_quant<float, true, NC>, x32, bytes);
+    else vec ? go(k7_apply_quant<uint16_t, true, NC>, x16, bytes) : go(k7_apply_quant<uint16_t, false, NC>, x16, bytes);
   };
-  if (ldq <= 512) by_type(std::integral_constant<int, 1>{});
+  const bool even = a.C % 8 == 0 && vec;
+  if (even && a.C <= 128) {
+    a.xdtype == 0 ? go(k7_apply_quant_narrow<float, 16>, x32, (size_t)a.G * 8)
+                  : go(k7_apply_quant_narrow<uint16_t, 16>, x16, (size_t)a.G * 8);
+  } else if (even && a.C <= 256) {
+    a.xdtype == 0 ? go(k7_apply_quant_narrow<float, 32>, x32, (size_t)a.G * 8)
+                  : go(k7_apply_quant_narrow<uint16_t, 32>, x16, (size_t)a.G * 8);
+  } else if (ldq <= 512) by_type(std::integral_constant<int, 1>{});
   else if (ldq <= 1024) by_type(std::integral_constant<int, 2>{});
   else if (ldq <= 2048) by_type(std::integral_constant<int, 4>{});
   else by_type(std::integral_constant<int, 8>{});
