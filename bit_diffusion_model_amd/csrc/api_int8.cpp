@@ -192,9 +192,15 @@ svdq_status svdq_linear_forward_int8(const svdq_int8_layer* layer, int64_t M, co
   return run_gemm(layer, M, qX, sX, Y, ldy, ydtype, base + used, ws_bytes - used, stream);
 }
 
-size_t svdq_group_norm_workspace_bytes(const svdq_group_norm_desc* norm, int64_t B, int64_t S) {
+size_t svdq_group_norm_quantize_workspace_bytes(const svdq_group_norm_desc* norm, int64_t B, int64_t S) {
   if (check_norm(norm, B, S) != SVDQ_OK || B == 0 || S == 0) return 0;
   return rup(plan_norm(B, S, (int)norm->C, norm->groups).bytes);
+}
+
+size_t svdq_group_norm_workspace_bytes(const svdq_group_norm_desc* norm, int64_t B, int64_t S) {
+  if (check_norm(norm, B, S) != SVDQ_OK || B == 0 || S == 0) return 0;
+  const NormPlan p = plan_norm(B, S, (int)norm->C, norm->groups);
+  return p.one ? 0 : rup(p.bytes);  // one launch needs none
 }
 
 svdq_status svdq_group_norm(const svdq_group_norm_desc* norm, int64_t B, int64_t S, const void* X, int32_t xdtype,
@@ -225,7 +231,7 @@ svdq_status svdq_group_norm_quantize_int8(const svdq_group_norm_desc* norm, int6
   NormArgs a;
   if ((st = norm_args(norm, B, S, X, xdtype, bsx, ldx, a)) != SVDQ_OK || (st = check_codes(qX, sX)) != SVDQ_OK) return st;
   if (!aligned(inv_s, 16)) return fail(SVDQ_EINVAL, "inv_s must be 16-byte aligned");
-  if ((st = check_ws(workspace, ws_bytes, svdq_group_norm_workspace_bytes(norm, B, S))) != SVDQ_OK) return st;
+  if ((st = check_ws(workspace, ws_bytes, svdq_group_norm_quantize_workspace_bytes(norm, B, S))) != SVDQ_OK) return st;
   hipError_t e = launch_norm_quant(a, inv_s, qX, sX, workspace, (hipStream_t)stream);
   if (e != hipSuccess) return fail(SVDQ_EHIP, "group norm launch: %s", hipGetErrorString(e));
   return ok();
@@ -233,7 +239,7 @@ svdq_status svdq_group_norm_quantize_int8(const svdq_group_norm_desc* norm, int6
 
 size_t svdq_norm_linear_int8_workspace_bytes(const svdq_group_norm_desc* norm, const svdq_int8_layer* layer,
                                              int64_t B, int64_t S) {
-  const size_t n = svdq_group_norm_workspace_bytes(norm, B, S);
+  const size_t n = svdq_group_norm_quantize_workspace_bytes(norm, B, S);
   if (n == 0 || check_dims_int8(layer) != SVDQ_OK || layer->K != norm->C) return 0;
   return n + act_bytes(B * S, layer->K) + svdq_gemm_w8a8_workspace_bytes(layer, B * S);
 }
@@ -254,7 +260,7 @@ svdq_status svdq_norm_linear_forward_int8(const svdq_group_norm_desc* norm, cons
       (st = check_ws(workspace, ws_bytes, svdq_norm_linear_int8_workspace_bytes(norm, layer, B, S))) != SVDQ_OK)
     return st;
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  const size_t q = svdq_group_norm_workspace_bytes(norm, B, S);
+  const size_t q = svdq_group_norm_quantize_workspace_bytes(norm, B, S);
   int8_t* qX = reinterpret_cast<int8_t*>(base + q);
   float* sX = reinterpret_cast<float*>(base + q + rup((size_t)M * (size_t)i8_ld(layer->K)));
   const size_t used = q + act_bytes(M, layer->K);

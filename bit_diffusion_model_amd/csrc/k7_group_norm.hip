@@ -474,10 +474,10 @@ __global__ __launch_bounds__(AP_NT) void k7_apply(const T* __restrict__ X, int64
   }
 }
 
-// The output pass into codes: a wave takes whole positions (rows of C channels), NC chunks of
-// 512 channels in registers.  Per channel (mean, rstd gamma, beta, inv_s) wait in LDS, eight planes
-// of C / 8 so that neighbouring lanes read neighbouring 16 bytes.
-template <typename T, bool VEC, int NC>
+// The output pass into codes: a wave takes U whole positions (rows of C channels) at once, NC chunks
+// of 512 channels each in registers.  Per channel (mean, rstd gamma, beta, inv_s) wait in LDS, eight
+// planes of C / 8 so that neighbouring lanes read neighbouring 16 bytes, read once for U rows.
+template <typename T, bool VEC, int NC, int U>
 __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X, int64_t bsx, int64_t ldx,
                                                         int64_t chunk, Stats st, const float* __restrict__ gamma,
                                                         const float* __restrict__ beta, int act,
@@ -485,6 +485,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
                                                         int64_t ldq, float* __restrict__ sX) {
   extern __shared__ __attribute__((aligned(16))) float lds[];
   __shared__ double scratch[AP_NT];
+  constexpr int NW = AP_NT / 64;
   const int C = st.C, cpg = C / st.G, c8 = (C + 7) / 8;
   float4* coef = reinterpret_cast<float4*>(lds);
   float2* stat = reinterpret_cast<float2*>(coef + 8 * c8);
@@ -493,12 +494,16 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
   const int rows = (int)(r0 + chunk < st.S ? chunk : st.S - r0);
   typedef Row<T, VEC> RowX;
   auto row_at = [&](int i) { return RowX(X + blockIdx.y * bsx + (r0 + (i < rows ? i : 0)) * ldx, C); };
-  typename RowX::Raw raw[NC];
-  {
-    const RowX x = row_at(wave);
+  typename RowX::Raw raw[U][NC];
+  auto load = [&](int i) {
 #pragma unroll
-    for (int j = 0; j < NC; ++j) raw[j] = x.load(8 * lane + 512 * j);
-  }
+    for (int u = 0; u < U; ++u) {
+      const RowX x = row_at(i + u);
+#pragma unroll
+      for (int j = 0; j < NC; ++j) raw[u][j] = x.load(8 * lane + 512 * j);
+    }
+  };
+  load(wave * U);
   // gamma, beta and inv_s while the statistics are joined; channels past C: value act(0) * 0
   for (int c = threadIdx.x; c < 8 * c8; c += AP_NT)
     coef[(c & 7) * c8 + (c >> 3)] = c < C ? make_float4(0.0f, gamma ? gamma[c] : 1.0f, beta ? beta[c] : 0.0f,
@@ -511,36 +516,44 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
     f.x = s.x, f.y *= s.y;
   }
   __syncthreads();
-  for (int i = wave; i < rows; i += AP_NT / 64) {
-    const RowX x = row_at(i);
-    float v[NC][8];
-    uint32_t a = 0;
+  for (int i = wave * U; i < rows; i += NW * U) {
+    const RowX any = row_at(0);
+    float v[U][NC][8];
+    uint32_t a[U] = {};
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int k8 = lane + 64 * j;
-      x.value(raw[j], 8 * k8, v[j]);
       const bool in = k8 < c8;
+#pragma unroll
+      for (int u = 0; u < U; ++u) any.value(raw[u][j], 8 * k8, v[u][j]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float4 f = coef[e * c8 + (in ? k8 : 0)];
-        v[j][e] = in ? norm_act((v[j][e] - f.x) * f.y + f.z, act) * f.w : 0.0f;
-        a = umax(a, abs_bits(v[j][e]));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float y = in ? norm_act((v[u][j][e] - f.x) * f.y + f.z, act) * f.w : 0.0f;
+          v[u][j][e] = y;
+          a[u] = umax(a[u], abs_bits(y));
+        }
       }
     }
-    const RowX next = row_at(i + AP_NT / 64);  // the next row's loads under this row's reduction
+    load(i + NW * U);  // the next rows' loads under these rows' reductions
 #pragma unroll
-    for (int j = 0; j < NC; ++j) raw[j] = next.load(8 * lane + 512 * j);
-    float s, r;
-    row_scale(wave_umax(a), s, r);
-    const int64_t row = blockIdx.y * st.S + r0 + i;
+    for (int u = 0; u < U; ++u) {
+      if (i + u >= rows) break;
+      float s, r;
+      row_scale(wave_umax(a[u]), s, r);
+      const int64_t row = blockIdx.y * st.S + r0 + i + u;
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const int64_t k = 8 * (lane + 64 * j);
-      if (k < ldq)
-        *reinterpret_cast<uint2*>(qX + row * ldq + k) = make_uint2(codes4(v[j][0], v[j][1], v[j][2], v[j][3], r),
-                                                                   codes4(v[j][4], v[j][5], v[j][6], v[j][7], r));
+      for (int j = 0; j < NC; ++j) {
+        const int64_t k = 8 * (lane + 64 * j);
+        if (k < ldq)
+          *reinterpret_cast<uint2*>(qX + row * ldq + k) =
+              make_uint2(codes4(v[u][j][0], v[u][j][1], v[u][j][2], v[u][j][3], r),
+                         codes4(v[u][j][4], v[u][j][5], v[u][j][6], v[u][j][7], r));
+      }
+      if (lane == 0) sX[row] = s;
     }
-    if (lane == 0) sX[row] = s;
   }
 }
 
@@ -751,8 +764,9 @@ hipError_t launch_norm_quant(const NormArgs& a, const float* inv_s, int8_t* qX, 
   const bool vec = vec_ok(a.X, a.bsx, a.ldx, a.xdtype);
   const size_t bytes = (size_t)((a.C + 7) / 8) * 8 * 16 + (size_t)a.G * 8;
   const int64_t ldq = i8_ld(a.C);
-  // as many blocks as the norm's output pass, of at least two rows per wave
-  const int64_t rows = p.rows < 8 ? 8 : p.rows;
+  // about 768 blocks of at least two rows per wave
+  int64_t rows = (a.S * a.B + 767) / 768;
+  if (rows < 8) rows = 8;
   const dim3 g((uint32_t)((a.S + rows - 1) / rows), (uint32_t)a.B), b(AP_NT);
   auto go = [&](auto kernel, auto x, size_t lds) {
     hipLaunchKernelGGL(kernel, g, b, lds, st, x, a.bsx, a.ldx, rows, s, a.gamma, a.beta, a.act, inv_s, qX, ldq, sX);
@@ -760,9 +774,9 @@ hipError_t launch_norm_quant(const NormArgs& a, const float* inv_s, int8_t* qX, 
   const float* x32 = static_cast<const float*>(a.X);
   const uint16_t* x16 = static_cast<const uint16_t*>(a.X);
   auto by_type = [&](auto nc) {
-    constexpr int NC = decltype(nc)::value;
-    if (a.xdtype == 0) go(k7_apply_quant<float, true, NC>, x32, bytes);
-    else vec ? go(k7_apply_quant<uint16_t, true, NC>, x16, bytes) : go(k7_apply_quant<uint16_t, false, NC>, x16, bytes);
+    constexpr int NC = decltype(nc)::value, U = NC == 1 ? 4 : NC == 2 ? 2 : 1;
+    if (a.xdtype == 0) go(k7_apply_quant<float, true, NC, U>, x32, bytes);
+    else vec ? go(k7_apply_quant<uint16_t, true, NC, U>, x16, bytes) : go(k7_apply_quant<uint16_t, false, NC, U>, x16, bytes);
   };
   const bool even = a.C % 8 == 0 && vec;
   if (even && a.C <= 128) {

@@ -62,7 +62,7 @@ EXPORTS = [
     "svdq_int8_ld", "svdq_pack_weights_int8", "svdq_int8_weight_bytes", "svdq_prepare_weights_int8",
     "svdq_quantize_act_int8", "svdq_gemm_w8a8_workspace_bytes",
     "svdq_int8_workspace_bytes", "svdq_gemm_w8a8", "svdq_linear_forward_int8", "svdq_group_norm_workspace_bytes",
-    "svdq_group_norm", "svdq_group_norm_quantize_int8", "svdq_norm_linear_int8_workspace_bytes",
+    "svdq_group_norm_quantize_workspace_bytes", "svdq_group_norm", "svdq_group_norm_quantize_int8", "svdq_norm_linear_int8_workspace_bytes",
     "svdq_norm_linear_forward_int8",
 ]
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -115,6 +115,7 @@ def lib():
         "svdq_gemm_w8a8": (I32, [P, I64, P, P, P, I64, I32, P, SZ, P]),
         "svdq_linear_forward_int8": (I32, [P, I64, P, I32, I64, P, I64, I32, P, SZ, P]),
         "svdq_group_norm_workspace_bytes": (SZ, [P, I64, I64]),
+        "svdq_group_norm_quantize_workspace_bytes": (SZ, [P, I64, I64]),
         "svdq_group_norm": (I32, [P, I64, I64, P, I32, I64, I64, P, I32, I64, I64, P, SZ, P]),
         "svdq_group_norm_quantize_int8": (I32, [P, I64, I64, P, I32, I64, I64, P, P, P, P, SZ, P]),
         "svdq_norm_linear_int8_workspace_bytes": (SZ, [P, P, I64, I64]),
@@ -742,10 +743,12 @@ class GroupNorm:
             return B, H * W, X.stride(0), _ld(H * W, X.stride(2) if W > 1 else X.stride(1), self.C)
         return X.shape[0], X.shape[1], X.stride(0), _ld(X.shape[1], X.stride(1), self.C)
 
-    def workspace(self, B: int, S: int, device):
+    def workspace(self, B: int, S: int, device, quantize: bool = False):
+        """Device scratch of forward() (None when unused), or of quantize()."""
         torch, _, _, L = _rt()
-        n = L.svdq_group_norm_workspace_bytes(self._ref, B, S)
-        return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+        fn = L.svdq_group_norm_quantize_workspace_bytes if quantize else L.svdq_group_norm_workspace_bytes
+        n = fn(self._ref, B, S)
+        return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
     def forward(self, X, ydtype: int = BF16, out=None, workspace=None):
         """svdq_group_norm: act(norm(X)) in X's shape, fp32 or bf16."""
@@ -756,12 +759,15 @@ class GroupNorm:
             raise SvdqError("the norm's output is F32 or BF16")
         if out is None:
             out = torch.empty(X.shape, dtype=ty[ydtype], device=X.device)
+            bsy, ldy = S * self.C, self.C
         elif out.shape != X.shape or out.dtype != ty[ydtype] or not out.is_cuda:
             raise SvdqError(f"out must be a {tuple(X.shape)} {ty[ydtype]} device tensor")
-        _, _, bsy, ldy = self._geometry(out, "out")
+        else:
+            _, _, bsy, ldy = self._geometry(out, "out")
         ws = workspace if workspace is not None else self.workspace(B, S, X.device)
         _check(L.svdq_group_norm(self._ref, B, S, X.data_ptr(), xt[X.dtype], bs, ld, out.data_ptr(),
-                                 ydtype, bsy, ldy, ws.data_ptr(), ws.numel(), _raw_stream(X)))
+                                 ydtype, bsy, ldy, None if ws is None else ws.data_ptr(),
+                                 0 if ws is None else ws.numel(), _raw_stream(X)))
         return out
 
     def quantize(self, X, inv_s=None, out=None, workspace=None):
@@ -773,10 +779,11 @@ class GroupNorm:
         if out is None:
             out = (torch.empty((B * S, int8_ld(self.C)), dtype=torch.int8, device=X.device),
                    torch.empty(B * S, dtype=torch.float32, device=X.device))
-        ws = workspace if workspace is not None else self.workspace(B, S, X.device)
+        ws = workspace if workspace is not None else self.workspace(B, S, X.device, True)
         _check(L.svdq_group_norm_quantize_int8(self._ref, B, S, X.data_ptr(), xt[X.dtype], bs, ld,
                                                None if inv_s is None else inv_s.data_ptr(), out[0].data_ptr(),
-                                               out[1].data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(X)))
+                                               out[1].data_ptr(), None if ws is None else ws.data_ptr(),
+                                               0 if ws is None else ws.numel(), _raw_stream(X)))
         return out
 
     def forward_linear(self, X, layer: Int8Linear, ydtype: int = BF16, out=None, workspace=None):

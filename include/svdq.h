@@ -521,8 +521,10 @@ typedef struct svdq_group_norm_desc {
   const float* beta;  /* device [C] fp32, or NULL for 0 */
 } svdq_group_norm_desc;
 
-/* Bytes of device workspace of the calls below for B images of S positions (0 on bad arguments). */
+/* Bytes of device workspace of svdq_group_norm (0: none, where a group fits one block) and of
+ * svdq_group_norm_quantize_int8 for B images of S positions (0 on bad arguments). */
 size_t svdq_group_norm_workspace_bytes(const svdq_group_norm_desc* norm, int64_t B, int64_t S);
+size_t svdq_group_norm_quantize_workspace_bytes(const svdq_group_norm_desc* norm, int64_t B, int64_t S);
 
 /* Y [B][S][C] (position stride ldy, image stride bsy), SVDQ_F32 or SVDQ_BF16; X fp32 or bf16.
  * Y may be X itself (same type and strides).  workspace >= svdq_group_norm_workspace_bytes,

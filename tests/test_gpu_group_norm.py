@@ -233,7 +233,7 @@ def test_refusals():
     with pytest.raises(svdq.SvdqError):
         gn.forward(X, out=torch.empty((2, 10, 63), device="cuda:0"))
     with pytest.raises(svdq.SvdqError):
-        gn.forward(X, workspace=torch.empty(8, dtype=torch.uint8, device="cuda:0"))
+        gn.forward(make_x(2, 6000, 64, torch.float32, 1), workspace=torch.empty(8, dtype=torch.uint8, device="cuda:0"))
     with pytest.raises(svdq.SvdqError):
         svdq.GroupNorm(7, 64).forward(X)
     with pytest.raises(svdq.SvdqError):

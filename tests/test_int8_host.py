@@ -126,21 +126,23 @@ def test_norm_entry_points_validate_on_host():
     nrm = svdq._GroupNorm(64, 8, 1, 1e-5, 16, 16)
     ref = ctypes.byref(nrm)
     ws = (256, 1 << 30)
-    ok = lambda n=ref, B=2, S=10, X=16, xd=1, bsx=640, ldx=64, Y=16, yd=1, bsy=640, ldy=64, w=ws: L.svdq_group_norm(  # noqa: E731
+    ok = lambda n=ref, B=2, S=8000, X=16, xd=1, bsx=512000, ldx=64, Y=16, yd=1, bsy=512000, ldy=64, w=ws: L.svdq_group_norm(  # noqa: E731
         n, B, S, X, xd, bsx, ldx, Y, yd, bsy, ldy, *w, None)
     assert ok(B=0, X=None, Y=None) == 0 and ok(S=0, X=None, Y=None) == 0
     assert ok(n=None) == 1 and ok(B=-1) == 1 and ok(S=-1) == 1
     assert ok(X=None) == 1 and ok(Y=None) == 1 and ok(X=17) == 1 and ok(Y=18, yd=0) == 1
     assert ok(xd=2) == 2 and ok(yd=2) == 2 and ok(xd=7) == 2
-    assert ok(ldx=63) == 1 and ok(ldy=63) == 1 and ok(bsx=639) == 1 and "bsx" in _err()
-    assert ok(bsy=600) == 1 and "bsy" in _err()
+    assert ok(ldx=63) == 1 and ok(ldy=63) == 1 and ok(bsx=511999) == 1 and "bsx" in _err()
+    assert ok(bsy=511000) == 1 and "bsy" in _err()
     assert ok(B=70000, S=1) == 2 and ok(ldx=1 << 31, bsx=1 << 40) == 2
     assert ok(w=(256, 8)) == 1 and "workspace" in _err() and ok(w=(128, 1 << 30)) == 1 and ok(w=(None, 0)) == 1
+    # a group that fits one block needs no workspace, its codes' statistics do
+    assert L.svdq_group_norm_workspace_bytes(ref, 2, 10) == 0 < L.svdq_group_norm_quantize_workspace_bytes(ref, 2, 10)
     for bad, st in (((0, 8, 1, 1e-5, 16, 16), 1), ((64, 0, 1, 1e-5, 16, 16), 1), ((64, 7, 1, 1e-5, 16, 16), 1),
                     ((8192, 8, 1, 1e-5, 16, 16), 2), ((4096, 2048, 1, 1e-5, 16, 16), 2), ((64, 8, 3, 1e-5, 16, 16), 2),
                     ((64, 8, 1, 0.0, 16, 16), 1), ((64, 8, 1, float("nan"), 16, 16), 1), ((64, 8, 1, 1e-5, 8, 16), 1),
                     ((64, 8, 1, 1e-5, 16, 8), 1)):
-        assert ok(n=ctypes.byref(svdq._GroupNorm(*bad)), ldx=8192, bsx=81920, ldy=8192, bsy=81920) == st, bad
+        assert ok(n=ctypes.byref(svdq._GroupNorm(*bad)), ldx=8192, bsx=8192 * 8000, ldy=8192, bsy=8192 * 8000) == st, bad
         assert L.svdq_group_norm_workspace_bytes(ctypes.byref(svdq._GroupNorm(*bad)), 2, 10) == 0
     q = lambda inv=16, qX=16, sX=16, w=ws: L.svdq_group_norm_quantize_int8(ref, 2, 10, 16, 1, 640, 64, inv, qX, sX, *w, None)  # noqa: E731
     assert q(inv=8) == 1 and q(qX=None) == 1 and q(qX=8) == 1 and q(sX=None) == 1 and q(w=(256, 8)) == 1
