@@ -106,31 +106,22 @@ __device__ __forceinline__ void load_channels(const Out& o, int64_t n, float sw[
 // P > 1 parts: blockIdx.y takes a range of the stages and stores raw sums to part[y].
 // Outputs leave through a wave-private LDS strip of 32 rows, so that stores are whole
 // 16-byte pieces of consecutive columns.
-template <int WM, int WN, int TI, int TJ, int KG>
-__global__ __launch_bounds__(64 * WM * WN * KG) void k6_tiles(const int8_t* __restrict__ qX, int64_t ld,
-                                                         const int8_t* __restrict__ qW, Out o, uint32_t tiles_m,
-                                                         uint32_t tiles_n, int* __restrict__ part, int64_t ldp) {
+//
+// The LDS arrays come from the kernel (ROOM bytes at least each), so that two tile shapes can
+// share them; separate arrays, addressed statically: the compiler then knows that
+// operand reads do not touch the buffer whose loads are in flight, and does not wait for them.
+template <int WM, int WN, int TI, int TJ, int KG, int ROOM>
+__device__ __forceinline__ void tile(const int8_t* __restrict__ qX, int64_t ld, const int8_t* __restrict__ qW,
+                                     const Out& o, int64_t m0, int64_t n0, int* __restrict__ part, int64_t ldp,
+                                     uint8_t* la0, uint8_t* la1, uint8_t* lb0, uint8_t* lb1, float* lsx, float* lsw,
+                                     float* lbb) {
   constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN, NW = WM * WN;  // NW waves per K group
   constexpr int AB = BM * 128, BB = BN * 128, NA = AB / 1024 / NW, NB = BB / 1024 / NW, NL = NA + NB;
   static_assert(AB % (1024 * NW) == 0 && BB % (1024 * NW) == 0, "whole 1 KB loads per wave");
-  // separate arrays, addressed statically: the compiler then knows that operand reads do not
-  // touch the buffer whose loads are in flight, and does not wait for them
-  __shared__ __attribute__((aligned(1024))) uint8_t la0[KG * AB];
-  __shared__ __attribute__((aligned(1024))) uint8_t la1[KG * AB];
-  __shared__ __attribute__((aligned(1024))) uint8_t lb0[KG * BB];
-  __shared__ __attribute__((aligned(1024))) uint8_t lb1[KG * BB];
-  __shared__ float lsx[BM], lsw[BN], lbb[BN];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6), wave = wid % NW, g = wid / NW;
   const int l32 = lane & 31, kh = lane >> 5;
   const int wr = (wave / WN) * 32 * TI, wc = (wave % WN) * 32 * TJ;
-
-  const uint32_t T = tiles_m * tiles_n, xcd = blockIdx.x & 7, t8 = T >> 3, r8 = T & 7;
-  const uint32_t t = xcd * t8 + (xcd < r8 ? xcd : r8) + (blockIdx.x >> 3);
-  constexpr uint32_t GM = 8;
-  const uint32_t grp = t / (GM * tiles_n), fm = grp * GM, gs = tiles_m - fm < GM ? tiles_m - fm : GM;
-  const uint32_t in = t - grp * GM * tiles_n;
-  const int64_t m0 = (int64_t)(fm + in % gs) * BM, n0 = (int64_t)(in / gs) * BN;
 
   const uint32_t rows = (uint32_t)(o.M - m0 < BM ? o.M - m0 : BM), cols = (uint32_t)(o.N - n0 < BN ? o.N - n0 : BN);
   const uint32_t blocks = (cols + 15) / 16;  // channel blocks of 16 (the last one zero past N)
@@ -246,7 +237,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k6_tiles(const int8_t* __re
 
   constexpr int CW = 32 * TJ, LS = CW + 4, CL = CW / 8, RP = 64 / CL;  // CL lanes of 8 columns, RP rows at once
   constexpr int PW = NW * KG / 4, NP = 32 / RP;                       // waves per array; passes per strip
-  static_assert(32 * LS * 4 * PW <= KG * (AB < BB ? AB : BB) && PW * 4 == NW * KG, "a strip per wave");
+  static_assert(32 * LS * 4 * PW <= ROOM && PW * 4 == NW * KG, "a strip per wave");
   auto strip_of = [&](int w) {
     uint8_t* base = w / PW == 0 ? la0 : w / PW == 1 ? la1 : w / PW == 2 ? lb0 : lb1;
     return reinterpret_cast<int*>(base) + (w % PW) * 32 * LS;
@@ -297,6 +288,41 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k6_tiles(const int8_t* __re
         store8(o, m, n, I[p], sx[p], sw, bb);
       }
     }
+  }
+}
+
+// Tile t of tiles_m x tiles_n in strips of 8 tile rows
+__device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, uint32_t& m, uint32_t& n) {
+  constexpr uint32_t GM = 8;
+  const uint32_t grp = t / (GM * tiles_n), fm = grp * GM, gs = tiles_m - fm < GM ? tiles_m - fm : GM;
+  const uint32_t in = t - grp * GM * tiles_n;
+  m = fm + in % gs;
+  n = in / gs;
+}
+
+// HALVES: the tiles from `whole` on are cut into two of half as many rows, one block each
+template <int WM, int WN, int TI, int TJ, int KG, bool HALVES>
+__global__ __launch_bounds__(64 * WM * WN * KG) void k6_tiles(const int8_t* __restrict__ qX, int64_t ld,
+                                                              const int8_t* __restrict__ qW, Out o, uint32_t tiles_m,
+                                                              uint32_t tiles_n, uint32_t whole, int* __restrict__ part,
+                                                              int64_t ldp) {
+  constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN, ROOM = KG * (BM < BN ? BM : BN) * 128;
+  __shared__ __attribute__((aligned(1024))) uint8_t la0[KG * BM * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t la1[KG * BM * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t lb0[KG * BN * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t lb1[KG * BN * 128];
+  __shared__ float lsx[BM], lsw[BN], lbb[BN];
+  uint32_t m, n;
+  if (!HALVES || blockIdx.x < whole) {
+    const uint32_t xcd = blockIdx.x & 7, t8 = whole >> 3, r8 = whole & 7;
+    tile_at(xcd * t8 + (xcd < r8 ? xcd : r8) + (blockIdx.x >> 3), tiles_m, tiles_n, m, n);
+    tile<WM, WN, TI, TJ, KG, ROOM>(qX, ld, qW, o, (int64_t)m * BM, (int64_t)n * BN, part, ldp, la0, la1, lb0, lb1, lsx, lsw, lbb);
+  } else if constexpr (HALVES) {
+    const uint32_t h = blockIdx.x - whole;
+    tile_at(whole + (h >> 1), tiles_m, tiles_n, m, n);
+    const int64_t m0 = (int64_t)m * BM + (h & 1) * (BM / 2);
+    if (m0 < o.M)
+      tile<WM, WN, TI / 2, TJ, KG, ROOM>(qX, ld, qW, o, m0, (int64_t)n * BN, part, ldp, la0, la1, lb0, lb1, lsx, lsw, lbb);
   }
 }
 
@@ -492,13 +518,15 @@ int device_cus() {
   return cus;
 }
 
-template <int WM, int WN, int TI, int TJ, int KG>
+template <int WM, int WN, int TI, int TJ, int KG, bool HALVES = false>
 void launch_tiles(const W8A8Plan& p, int64_t ld, const int8_t* qX, const int8_t* qW, const Out& o, int* part,
                   hipStream_t st) {
   constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN;
   const uint32_t tm = (uint32_t)((o.M + BM - 1) / BM), tn = (uint32_t)((o.N + BN - 1) / BN);
-  hipLaunchKernelGGL((k6_tiles<WM, WN, TI, TJ, KG>), dim3(tm * tn, (uint32_t)p.parts), dim3(64 * WM * WN * KG), 0, st, qX, ld, qW,
-                     o, tm, tn, part, p.ldp);
+  const uint32_t whole = HALVES ? tm * tn - (uint32_t)p.halved : tm * tn;
+  const uint32_t blocks = whole + 2 * (tm * tn - whole);
+  hipLaunchKernelGGL((k6_tiles<WM, WN, TI, TJ, KG, HALVES>), dim3(blocks, (uint32_t)p.parts), dim3(64 * WM * WN * KG), 0,
+                     st, qX, ld, qW, o, tm, tn, whole, part, p.ldp);
 }
 
 // ---- the choice of kernel
@@ -516,9 +544,17 @@ void launch_tiles(const W8A8Plan& p, int64_t ld, const int8_t* qX, const int8_t*
 //   128     0.62 S + 2.5 alone, 1.04 S for two: 512x3072x9216 24.3, 2048x12288x3072 80.5
 //   128 x 2 two K groups (tiles <= CUs): 0.53 S + 2: 1024x12288x3072 53.1 (one group 67.2)
 //   256     1.38 S + 9 (1.15 S where at most 5/8 of the CUs have a tile): 4608x12288x3072 143 (128: 176),
-//           1024x3072x9216 38.8 (46.8), 2048x3072x9216 81.7 (71.6)
+//           1024x3072x9216 38.8 (46.8), 2048x3072x9216 81.7 (71.6); a last round for at most half of
+//           the CUs runs as tiles of 128 x 256, 0.9 S: 9216x3072x9216 269 (whole tiles 278),
+//           2304x3072x9216 79 (84), with GELU 88 (101), 8192x4096x8448 279 (297)
 // K parts (tiles of 64 with four groups, S / parts >= 24, all parts on the CUs at once) add the
 // partial sums' traffic and a launch, 4 + 12 bytes x M N parts / 6 TB/s: 64x12288x3072 15.7 in 4 parts, 26.6 in one.
+// Tiles of 256 that a last round leaves for at most half of the CUs, after at least one whole round
+int64_t halved_tiles(int64_t M, int64_t N, int cus) {
+  const int64_t T = ((M + 255) / 256) * ((N + 255) / 256), rest = T % cus;
+  return T > cus && 2 * rest <= cus ? rest : 0;
+}
+
 struct Cost {
   double us;
   int tile, groups, parts;
@@ -539,7 +575,8 @@ Cost tiles_cost(int64_t M, int64_t N, int S, int cus, int tile, int groups) {
   else if (tile == 128) groups == 1 ? by_line(a128, 2, 2.5) : by_line(a1282, 1, 2.0);
   else {
     const double full = (double)(int64_t)rounds, rest = rounds - full;
-    us = full * (1.38 * S + 9.0) + (rest > 0.625 ? 1.38 * S + 9.0 : rest > 0 ? 1.15 * S + 9.0 : 0.0);
+    const bool halved = full > 0 && rest <= 0.5;
+    us = full * (1.38 * S + 9.0) + (rest == 0 ? 0.0 : halved ? 0.9 * S + 9.0 : rest <= 0.625 ? 1.15 * S + 9.0 : 1.38 * S + 9.0);
   }
   return Cost{us, tile, groups, 1};
 }
@@ -570,7 +607,8 @@ W8A8Plan plan_w8a8(int64_t M, int64_t K, int64_t N) {
     }
   }
   if (M <= 32) take(Cost{2.3 + (double)(N * ld) * 1e-6 * (0.075 + 0.006 * (double)M), 0, 1, 1});
-  W8A8Plan p{best.tile, best.groups, best.parts, ldp, 0};
+  W8A8Plan p{best.tile, best.groups, best.parts, ldp, 0, 0};
+  if (p.tile == 256) p.halved = halved_tiles(M, N, cus);
   if (p.parts > 1) p.bytes = (size_t)p.parts * (size_t)M * (size_t)ldp * 4;
   return p;
 }
@@ -618,7 +656,8 @@ hipError_t launch_w8a8(int64_t M, int64_t K, int64_t N, const int8_t* qX, const 
     return hipGetLastError();
   }
   int* part = p.parts > 1 ? static_cast<int*>(ws) : nullptr;
-  if (p.tile == 256) launch_tiles<2, 4, 4, 2, 1>(p, ld, qX, qW, o, part, st);
+  if (p.tile == 256 && p.halved) launch_tiles<2, 4, 4, 2, 1, true>(p, ld, qX, qW, o, part, st);
+  else if (p.tile == 256) launch_tiles<2, 4, 4, 2, 1>(p, ld, qX, qW, o, part, st);
   else if (p.tile == 128 && p.groups == 1) launch_tiles<2, 2, 2, 2, 1>(p, ld, qX, qW, o, part, st);
   else if (p.tile == 128) launch_tiles<2, 2, 2, 2, 2>(p, ld, qX, qW, o, part, st);
   else if (p.groups == 1) launch_tiles<2, 2, 1, 1, 1>(p, ld, qX, qW, o, part, st);

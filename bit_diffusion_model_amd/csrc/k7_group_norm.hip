@@ -194,7 +194,7 @@ __global__ __launch_bounds__(1024) void k7_one(const T* __restrict__ X, int64_t 
       valuev<T, V>(raw[j], v);
 #pragma unroll
       for (int e = 0; e < V; ++e)
-        v[e] = norm_act((v[e] - mean) * (rstd * lds[q * V + e]) + lds[cpg + q * V + e], act);
+        v[e] = norm_act(fmaf(v[e] - mean, rstd * lds[q * V + e], lds[cpg + q * V + e]), act);
       storev<TY, V>(y + r * ldy + q * V, v);
     }
     q += dc, r += dr;
@@ -467,7 +467,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply(const T* __restrict__ X, int64
         float v[V];
         valuev<T, V>(raw[u], v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = norm_act((v[e] - mean[e]) * a[e] + b[e], act);
+        for (int e = 0; e < V; ++e) v[e] = norm_act(fmaf(v[e] - mean[e], a[e], b[e]), act);
         storev<TY, V, NT>(y + r * ldy + c * V, v);
       }
     }
@@ -531,7 +531,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
         const float4 f = coef[e * c8 + (in ? k8 : 0)];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const float y = in ? norm_act((v[u][j][e] - f.x) * f.y + f.z, act) * f.w : 0.0f;
+          const float y = in ? norm_act(fmaf(v[u][j][e] - f.x, f.y, f.z), act) * f.w : 0.0f;
           v[u][j][e] = y;
           a[u] = umax(a[u], abs_bits(y));
         }
@@ -607,7 +607,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant_narrow(const T* __restri
       uint32_t top = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[e] = on ? norm_act((v[e] - mean[e]) * a[e] + b[e], act) * f[e] : 0.0f;
+        v[e] = on ? norm_act(fmaf(v[e] - mean[e], a[e], b[e]), act) * f[e] : 0.0f;
         top = umax(top, abs_bits(v[e]));
       }
       float s, q;

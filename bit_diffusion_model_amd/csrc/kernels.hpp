@@ -92,6 +92,7 @@ struct W8A8Plan {
   int tile, groups, parts;
   int64_t ldp;
   size_t bytes;
+  int64_t halved;  // tiles of 256 at the end that run as two blocks of half the rows
 };
 W8A8Plan plan_w8a8(int64_t M, int64_t K, int64_t N);
 // Whether the layer runs as one launch for few tokens (which quantizes inside), and that launch.
