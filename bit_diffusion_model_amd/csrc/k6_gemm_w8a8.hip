@@ -536,11 +536,13 @@ void launch_tiles(const W8A8Plan& p, int64_t ld, const int8_t* qX, const int8_t*
 // through measured times (256 CUs, 20 launches back to back; M x K x N):
 //   few     2.3 + weight bytes x (0.075 + 0.006 M) / MB: 1x3072x9216 4.1 (64 x 2: 7.6), 16x3072x9216 7.1 (7.9),
 //           32x3072x9216 11.2 (8.1), 32x1280x1280 4.1 (5.3), 16x12288x3072 9.6 (64 x 4 in 4 parts: 14.6)
-//   64      one K group: 0.30 S + 1.6 alone on its CU, then 0.38, 0.58, 0.79 S for 2, 3, 4 blocks:
-//           512x3072x3072 10.6, 1024x3072x3072 16.4, 512x320x1280 4.1
-//   64 x 2  two K groups (blocks of 8 waves, tiles <= CUs): 0.24 S + 2: 64x3072x9216 8.2 (one group
-//           10.1, four 8.3), 128x1280x1280 5.4 (6.0, 6.3)
-//   64 x 4  four K groups: 0.20 S + 3: 128x12288x3072 26.1 (one group 48.3, two 32.0)
+//   64      one K group: 0.33 S + 1.6 alone on its CU, then 0.50, 0.62, 0.79 S for 2, 3, 4 blocks:
+//           2048x640x640 6.0, 1024x3072x3072 16.4, 512x320x1280 4.1
+//   64 x 2  two K groups (blocks of 8 waves, two to a CU): 0.25 S + 2 alone, 0.38 S + 3.8 for two:
+//           128x1280x1280 5.4 (one group 6.0, four 6.3), 512x3072x3072 13.1 (14.2), inputs out of
+//           cache 13.5 (17.0), 512x12288x3072 39 (56); 2048x640x640 7.2 (6.0)
+//   64 x 4  four K groups (tiles <= CUs): 0.20 S + 3: 128x12288x3072 26.1 (one group 48.3, two 32.0),
+//           64x3072x9216 out of cache 14.1 (20.8, 15.3)
 //   128     0.62 S + 2.5 alone, 1.04 S for two: 512x3072x9216 24.3, 2048x12288x3072 80.5
 //   128 x 2 two K groups (tiles <= CUs): 0.53 S + 2: 1024x12288x3072 53.1 (one group 67.2)
 //   256     1.38 S + 9 (1.15 S where at most 5/8 of the CUs have a tile): 4608x12288x3072 143 (128: 176),
@@ -569,9 +571,9 @@ Cost tiles_cost(int64_t M, int64_t N, int S, int cus, int tile, int groups) {
     us = full * (a[most - 1] * S + b);
     if (rest > 0) us += a[(int)(rest + 0.999999) - 1] * S + b;
   };
-  static const double a64[] = {0.30, 0.38, 0.58, 0.79}, a642[] = {0.24}, a644[] = {0.20}, a128[] = {0.62, 1.04},
+  static const double a64[] = {0.33, 0.50, 0.62, 0.79}, a642[] = {0.25, 0.38}, a644[] = {0.20}, a128[] = {0.62, 1.04},
                       a1282[] = {0.53};
-  if (tile == 64) groups == 1 ? by_line(a64, 4, 1.6) : groups == 2 ? by_line(a642, 1, 2.0) : by_line(a644, 1, 3.0);
+  if (tile == 64) groups == 1 ? by_line(a64, 4, 1.6) : groups == 2 ? by_line(a642, 2, rounds > 1.0 ? 3.8 : 2.0) : by_line(a644, 1, 3.0);
   else if (tile == 128) groups == 1 ? by_line(a128, 2, 2.5) : by_line(a1282, 1, 2.0);
   else {
     const double full = (double)(int64_t)rounds, rest = rounds - full;
@@ -596,8 +598,8 @@ W8A8Plan plan_w8a8(int64_t M, int64_t K, int64_t N) {
   take(tiles_cost(M, N, S, cus, 256, 1));
   const int64_t T64 = ((M + 63) / 64) * ((N + 63) / 64), T128 = ((M + 127) / 128) * ((N + 127) / 128);
   if (T128 <= cus) take(tiles_cost(M, N, S, cus, 128, 2));
+  if (T64 <= 2 * cus) take(tiles_cost(M, N, S, cus, 64, 2));
   if (T64 <= cus) {
-    take(tiles_cost(M, N, S, cus, 64, 2));
     for (int parts = 1; parts <= 8 && parts * T64 <= cus && (parts == 1 || S / parts >= 24); parts *= 2) {
       const int per = (S + parts - 1) / parts;
       Cost c = tiles_cost(M, N, per, cus, 64, 4);

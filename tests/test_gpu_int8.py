@@ -243,3 +243,22 @@ def test_refusals():
     q, s = lin.quantize(X)
     with pytest.raises(svdq.SvdqError):
         lin.gemm(q[:, :128], s)
+
+
+def test_example_runs():
+    """examples/spatial_block_int8.py: norm, projection, MLP and modulation together; 8 bits' error of each step."""
+    import importlib.util
+    import os
+    import sys
+    from unittest import mock
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "spatial_block_int8.py")
+    spec = importlib.util.spec_from_file_location("spatial_block_int8", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    with mock.patch.object(sys, "argv", ["x", "--images", "2", "--side", "12", "--channels", "320"]):
+        errors = m.main()
+    # per layer two roundings of at most 4 / 127 / sqrt(12) of the values' norm (maxima near 4 standard deviations),
+    # doubled for smoothed outliers; the block adds three layers
+    one = 2 * np.sqrt(2) * 4 / 127 / np.sqrt(12)
+    assert errors["norm and projection"] < one and errors["modulation"] < one and errors["block"] < 3 * one
