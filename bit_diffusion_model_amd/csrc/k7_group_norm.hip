@@ -112,11 +112,18 @@ __device__ __forceinline__ void storev(TY* p, const float v[V]) {
   }
 }
 
-// SiLU y / (1 + exp(-y)): a large negative y gives y times 1 / inf = -0.  GELU in its exact form.
-__device__ __forceinline__ float norm_act(float y, int act) {
-  if (act == SVDQ_GN_SILU) return y * __builtin_amdgcn_rcpf(1.0f + __expf(-y));
-  if (act == SVDQ_GN_GELU) return gelu_erf(y);
-  return y;
+// The activation of N values (one branch for all): SiLU y / (1 + exp(-y)), exp as a power of 2 (a large
+// negative y gives y times 1 / inf = -0); GELU in its exact form.
+template <int N>
+__device__ __forceinline__ void norm_act(float (&y)[N], int act) {
+  if (act == SVDQ_GN_SILU) {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      y[e] *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y[e] * -1.44269504088896341f));
+  } else if (act == SVDQ_GN_GELU) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) y[e] = gelu_erf(y[e]);
+  }
 }
 
 // ---- one launch: a block per (group, image)
@@ -193,8 +200,8 @@ __global__ __launch_bounds__(1024) void k7_one(const T* __restrict__ X, int64_t 
       float v[V];
       valuev<T, V>(raw[j], v);
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        v[e] = norm_act(fmaf(v[e] - mean, rstd * lds[q * V + e], lds[cpg + q * V + e]), act);
+      for (int e = 0; e < V; ++e) v[e] = fmaf(v[e] - mean, rstd * lds[q * V + e], lds[cpg + q * V + e]);
+      norm_act(v, act);
       storev<TY, V>(y + r * ldy + q * V, v);
     }
     q += dc, r += dr;
@@ -264,30 +271,39 @@ __global__ __launch_bounds__(ST_NT) void k7_stats(const T* __restrict__ X, int64
   const int64_t r0 = (int64_t)blockIdx.x * chunk;
   const int rows = (int)(r0 + chunk < S ? chunk : S - r0);
   const T* x = X + blockIdx.y * bsx + r0 * ldx;
+  const int64_t step = pl.rp * ldx;
   if (pl.on && pl.row < rows)
     for (int c = pl.col; c < cv; c += pl.ct) {
       float p[V], s[V] = {}, q[V] = {};
-      for (int i = pl.row; i < rows; i += U * pl.rp) {
-        Vec<T, V> raw[U];
+      const T* at = x + pl.row * ldx + c * V;
+      valuev<T, V>(loadv<T, V>(at), p);
+      auto add = [&](const Vec<T, V>& w) {
+        float v[V];
+        valuev<T, V>(w, v);
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-          const int r = i + j * pl.rp;
-          raw[j] = loadv<T, V>(x + (r < rows ? r : i) * ldx + c * V);
+        for (int e = 0; e < V; ++e) {
+          const float d = v[e] - p[e];
+          s[e] += d;
+          q[e] = fmaf(d, d, q[e]);
         }
-        if (i == pl.row) valuev<T, V>(raw[0], p);
+      };
+      Vec<T, V> raw[U];
+      int i = pl.row;
+      for (; i + (U - 1) * pl.rp < rows; i += U * pl.rp) {
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-          float v[V];
-          valuev<T, V>(raw[j], v);
-          const bool in = i + j * pl.rp < rows;
+        for (int j = 0; j < U; ++j, at += step) raw[j] = loadv<T, V>(at);
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float d = in ? v[e] - p[e] : 0.0f;
-            s[e] += d;
-            q[e] += d * d;
-          }
-        }
+        for (int j = 0; j < U; ++j) add(raw[j]);
       }
+      const T* end = at;  // at most U - 1 more positions
+#pragma unroll
+      for (int j = 0; j < U - 1; ++j) {
+        raw[j] = loadv<T, V>(i + j * pl.rp < rows ? end : x + c * V);
+        end += step;
+      }
+#pragma unroll
+      for (int j = 0; j < U - 1; ++j)
+        if (i + j * pl.rp < rows) add(raw[j]);
       const float n = (float)((rows - pl.row + pl.rp - 1) / pl.rp);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -426,13 +442,12 @@ __global__ __launch_bounds__(AP_NT) void k7_apply(const T* __restrict__ X, int64
   const int rows = (int)(r0 + chunk < st.S ? chunk : st.S - r0);
   const T* x = X + blockIdx.y * bsx + r0 * ldx;
   TY* y = Y + blockIdx.y * bsy + r0 * ldy;
+  const int64_t step = pl.rp * ldx, ystep = pl.rp * ldy;
   Vec<T, V> raw[U];
   auto load = [&](int c, int i) {
+    const T* at = x + i * ldx + c * V;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = i + u * pl.rp;
-      raw[u] = loadv<T, V>(x + (r < rows ? r : 0) * ldx + c * V);
-    }
+    for (int u = 0; u < U; ++u, at += step) raw[u] = loadv<T, V>(i + u * pl.rp < rows ? at : x + c * V);
   };
   float a[V], b[V];
   auto affine = [&](int c) {
@@ -460,15 +475,16 @@ __global__ __launch_bounds__(AP_NT) void k7_apply(const T* __restrict__ X, int64
     }
     for (int i = pl.row; i < rows; i += U * pl.rp) {
       if (i != pl.row) load(c, i);
+      TY* to = y + i * ldy + c * V;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = i + u * pl.rp;
-        if (r >= rows) break;
+      for (int u = 0; u < U; ++u, to += ystep) {
+        if (i + u * pl.rp >= rows) break;
         float v[V];
         valuev<T, V>(raw[u], v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = norm_act(fmaf(v[e] - mean[e], a[e], b[e]), act);
-        storev<TY, V, NT>(y + r * ldy + c * V, v);
+        for (int e = 0; e < V; ++e) v[e] = fmaf(v[e] - mean[e], a[e], b[e]);
+        norm_act(v, act);
+        storev<TY, V, NT>(to, v);
       }
     }
   }
@@ -494,16 +510,16 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
   const int rows = (int)(r0 + chunk < st.S ? chunk : st.S - r0);
   typedef Row<T, VEC> RowX;
   auto row_at = [&](int i) { return RowX(X + blockIdx.y * bsx + (r0 + (i < rows ? i : 0)) * ldx, C); };
-  typename RowX::Raw raw[U][NC];
-  auto load = [&](int i) {
+  typename RowX::Raw raw[U][NC], next[U][NC];
+  auto load = [&](int i, typename RowX::Raw (&to)[U][NC]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const RowX x = row_at(i + u);
 #pragma unroll
-      for (int j = 0; j < NC; ++j) raw[u][j] = x.load(8 * lane + 512 * j);
+      for (int j = 0; j < NC; ++j) to[u][j] = x.load(8 * lane + 512 * j);
     }
   };
-  load(wave * U);
+  load(wave * U, raw);
   // gamma, beta and inv_s while the statistics are joined; channels past C: value act(0) * 0
   for (int c = threadIdx.x; c < 8 * c8; c += AP_NT)
     coef[(c & 7) * c8 + (c >> 3)] = c < C ? make_float4(0.0f, gamma ? gamma[c] : 1.0f, beta ? beta[c] : 0.0f,
@@ -518,6 +534,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
   __syncthreads();
   for (int i = wave * U; i < rows; i += NW * U) {
     const RowX any = row_at(0);
+    load(i + NW * U, next);  // under way while these rows are computed
     float v[U][NC][8];
     uint32_t a[U] = {};
 #pragma unroll
@@ -526,18 +543,28 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
       const bool in = k8 < c8;
 #pragma unroll
       for (int u = 0; u < U; ++u) any.value(raw[u][j], 8 * k8, v[u][j]);
+      float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float4 f = coef[e * c8 + (in ? k8 : 0)];
+        const float4 k = coef[e * c8 + (in ? k8 : 0)];
+        f[e] = in ? k.w : 0.0f;  // lanes past the row: 0 whatever the value
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float y = in ? norm_act(fmaf(v[u][j][e] - f.x, f.y, f.z), act) * f.w : 0.0f;
-          v[u][j][e] = y;
-          a[u] = umax(a[u], abs_bits(y));
+        for (int u = 0; u < U; ++u) v[u][j][e] = fmaf(in ? v[u][j][e] - k.x : 0.0f, k.y, k.z);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        norm_act(v[u][j], act);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[u][j][e] *= f[e];
+          a[u] = umax(a[u], abs_bits(v[u][j][e]));
         }
       }
     }
-    load(i + NW * U);  // the next rows' loads under these rows' reductions
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NC; ++j) raw[u][j] = next[u][j];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i + u >= rows) break;
@@ -606,8 +633,11 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant_narrow(const T* __restri
       valuev<T, 8>(raw[u], v);
       uint32_t top = 0;
 #pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = fmaf(on ? v[e] - mean[e] : 0.0f, a[e], b[e]);  // off: a = b = f = 0
+      norm_act(v, act);
+#pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[e] = on ? norm_act(fmaf(v[e] - mean[e], a[e], b[e]), act) * f[e] : 0.0f;
+        v[e] *= f[e];
         top = umax(top, abs_bits(v[e]));
       }
       float s, q;
@@ -764,9 +794,9 @@ hipError_t launch_norm_quant(const NormArgs& a, const float* inv_s, int8_t* qX, 
   const bool vec = vec_ok(a.X, a.bsx, a.ldx, a.xdtype);
   const size_t bytes = (size_t)((a.C + 7) / 8) * 8 * 16 + (size_t)a.G * 8;
   const int64_t ldq = i8_ld(a.C);
-  // about 768 blocks of at least two rows per wave
-  int64_t rows = (a.S * a.B + 767) / 768;
-  if (rows < 8) rows = 8;
+  // about 768 blocks; whole turns of the four waves where a wave takes several rows at once
+  const int turn = ldq <= 512 ? 16 : 8;
+  const int64_t rows = ((a.S * a.B + 767) / 768 + turn - 1) / turn * turn;
   const dim3 g((uint32_t)((a.S + rows - 1) / rows), (uint32_t)a.B), b(AP_NT);
   auto go = [&](auto kernel, auto x, size_t lds) {
     hipLaunchKernelGGL(kernel, g, b, lds, st, x, a.bsx, a.ldx, rows, s, a.gamma, a.beta, a.act, inv_s, qX, ldq, sX);
