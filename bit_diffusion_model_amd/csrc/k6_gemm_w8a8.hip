@@ -43,34 +43,35 @@ struct Out {
   bool wide;  // Y's rows are 16-byte aligned
 };
 
+constexpr float kNoBias = -0.0f;  // y + -0 is y, whatever y's sign
+
 __device__ __forceinline__ void store1(const Out& o, int64_t m, int64_t n, float y) {
   if (o.ydtype == 0) static_cast<float*>(o.Y)[m * o.ldy + n] = y;
   else static_cast<__bf16*>(o.Y)[m * o.ldy + n] = (__bf16)(o.ydtype == 2 ? gelu_erf(y) : y);
 }
 
-// Eight outputs n .. n+7 (n a multiple of 8) of row m from their integer sums; sw, bb: those
-// channels' scales and biases, sx the row's scale.
-__device__ __forceinline__ void store8(const Out& o, int64_t m, int64_t n, const int I[8], float sx, const float sw[8],
-                                       const float bb[8]) {
-  float y[8];
+// Eight outputs n .. n + 7 (n a multiple of 8) of row m: all within Y, whose rows are 16-byte
+// aligned.  OUT: 0 fp32, 1 bf16, 2 bf16 of GELU.
+template <int OUT>
+__device__ __forceinline__ void store8_whole(const Out& o, int64_t m, int64_t n, const float y[8]) {
+  if (OUT == 0) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(o.Y) + m * o.ldy + n);
+    p[0] = make_float4(y[0], y[1], y[2], y[3]);
+    p[1] = make_float4(y[4], y[5], y[6], y[7]);
+  } else {
+    uint32_t w[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    y[e] = (float)I[e] * sx * sw[e];
-    if (o.bias) y[e] += bb[e];
+    for (int e = 0; e < 4; ++e) w[e] = OUT == 2 ? gelu_bf16x2(y[2 * e], y[2 * e + 1]) : bf16_pair(y[2 * e], y[2 * e + 1]);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.Y) + m * o.ldy + n) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+// The same with channels that may lie past N and rows of any alignment
+__device__ __forceinline__ void store8(const Out& o, int64_t m, int64_t n, const float y[8]) {
   if (o.wide && n + 8 <= o.N) {
-    if (o.ydtype == 0) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(o.Y) + m * o.ldy + n);
-      p[0] = make_float4(y[0], y[1], y[2], y[3]);
-      p[1] = make_float4(y[4], y[5], y[6], y[7]);
-    } else {
-      if (o.ydtype == 2) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = gelu_erf(y[e]);
-      }
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.Y) + m * o.ldy + n) =
-          make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]), bf16_pair(y[4], y[5]), bf16_pair(y[6], y[7]));
-    }
+    if (o.ydtype == 0) store8_whole<0>(o, m, n, y);
+    else if (o.ydtype == 1) store8_whole<1>(o, m, n, y);
+    else store8_whole<2>(o, m, n, y);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -82,7 +83,7 @@ __device__ __forceinline__ void load_channels(const Out& o, int64_t n, float sw[
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     sw[e] = n + e < o.N ? o.sW[n + e] : 0.0f;
-    bb[e] = o.bias && n + e < o.N ? o.bias[n + e] : 0.0f;
+    bb[e] = o.bias && n + e < o.N ? o.bias[n + e] : kNoBias;
   }
 }
 
@@ -121,6 +122,7 @@ __device__ __forceinline__ void tile(const int8_t* __restrict__ qX, int64_t ld, 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6), wave = wid % NW, g = wid / NW;
   const int l32 = lane & 31, kh = lane >> 5;
+  const int ch = (l32 & 19) | (l32 & 4) << 1 | (l32 & 8) >> 1;  // the channel that is row l32 of the A operand
   const int wr = (wave / WN) * 32 * TI, wc = (wave % WN) * 32 * TJ;
 
   const uint32_t rows = (uint32_t)(o.M - m0 < BM ? o.M - m0 : BM), cols = (uint32_t)(o.N - n0 < BN ? o.N - n0 : BN);
@@ -144,7 +146,7 @@ __device__ __forceinline__ void tile(const int8_t* __restrict__ qX, int64_t ld, 
     for (int i = tid; i < BM; i += 64 * NW * KG) lsx[i] = i < (int)rows ? o.sX[m0 + i] : 0.0f;
     for (int i = tid; i < BN; i += 64 * NW * KG) {
       lsw[i] = i < (int)cols ? o.sW[n0 + i] : 0.0f;
-      lbb[i] = o.bias && i < (int)cols ? o.bias[n0 + i] : 0.0f;
+      lbb[i] = o.bias && i < (int)cols ? o.bias[n0 + i] : kNoBias;
     }
   }
   // past the end the buffers have no range: nothing is read and the LDS gets zeros
@@ -176,7 +178,7 @@ __device__ __forceinline__ void tile(const int8_t* __restrict__ qX, int64_t ld, 
     ra(0);
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      const int c = wc + 32 * j + l32, k16 = 2 * s + kh;  // lane (c % 16) + 16 (k16 % 4) of a fragment
+      const int c = wc + 32 * j + ch, k16 = 2 * s + kh;  // lane (c % 16) + 16 (k16 % 4) of a fragment
       fb[j] = *reinterpret_cast<const v4i*>(b + (c >> 4) * 2048 + (k16 >> 2) * 1024 + (k16 & 3) * 256 + (c & 15) * 16);
     }
 #pragma unroll
@@ -186,7 +188,7 @@ __device__ __forceinline__ void tile(const int8_t* __restrict__ qX, int64_t ld, 
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
   };
   // a step's order: one MFMA, the next step's reads, the other MFMAs (each ahead of one load)
   auto order = [&](bool loads) {
@@ -232,62 +234,92 @@ __device__ __forceinline__ void tile(const int8_t* __restrict__ qX, int64_t ld, 
     stage(k + 1, la1, lb1, la0, lb0);
   }
   if (k < turns) stage(k, la0, lb0, la1, lb1);
-  wait_vm_lgkm0<0>();
-  __builtin_amdgcn_s_barrier();  // the buffers are free
-
-  constexpr int CW = 32 * TJ, LS = CW + 4, CL = CW / 8, RP = 64 / CL;  // CL lanes of 8 columns, RP rows at once
-  constexpr int PW = NW * KG / 4, NP = 32 / RP;                       // waves per array; passes per strip
-  static_assert(32 * LS * 4 * PW <= ROOM && PW * 4 == NW * KG, "a strip per wave");
-  auto strip_of = [&](int w) {
-    uint8_t* base = w / PW == 0 ? la0 : w / PW == 1 ? la1 : w / PW == 2 ? lb0 : lb1;
-    return reinterpret_cast<int*>(base) + (w % PW) * 32 * LS;
-  };
-  int* strip = strip_of(wid);
-  const int rl = lane / CL, cl = lane % CL;
-  const int64_t n = n0 + wc + cl * 8;
-  float sw[8], bb[8];
+  // Lane (l32, kh) holds token l32 and, in registers 8 h .. 8 h + 7, channels 16 h + 8 kh .. + 7.
+  if constexpr (KG > 1) {
+    // the K groups' sums meet in LDS: unit u of 8 registers is finished by group u % KG
+    wait_vm_lgkm0<0>();
+    __builtin_amdgcn_s_barrier();  // the buffers are free
+    constexpr int UNITS = TI * TJ * 2;
+    static_assert(KG * NW * UNITS * 2048 <= 4 * ROOM && ROOM % 2048 == 0, "room for the sums");
+    auto slot = [&](int grp, int u, int half) {
+      const int at = ((grp * NW + wave) * UNITS + u) * 2048 + half * 1024;
+      uint8_t* base = at / ROOM == 0 ? la0 : at / ROOM == 1 ? la1 : at / ROOM == 2 ? lb0 : lb1;
+      return reinterpret_cast<v4i*>(base + at % ROOM + lane * 16);
+    };
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sw[e] = lsw[wc + cl * 8 + e], bb[e] = lbb[wc + cl * 8 + e];
+    for (int u = 0; u < UNITS; ++u) {
+      if (u % KG == g) continue;
+      const v16i& c = acc[u / 2 / TJ][u / 2 % TJ];
 #pragma unroll
-  for (int i = 0; i < TI; ++i) {
-#pragma unroll
-    for (int j = 0; j < TJ; ++j)
-#pragma unroll
-      for (int a = 0; a < 16; ++a) strip[(8 * (a >> 2) + 4 * kh + (a & 3)) * LS + 32 * j + l32] = acc[i][j][a];
-    if (KG > 1) __syncthreads();
-    // the K groups share the strip's passes; each adds all groups' sums
-    int I[NP][8];
-    float sx[NP];
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      if (KG > 1 && p % KG != g) continue;
-      const int at = (p * RP + rl) * LS + cl * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) I[p][e] = 0;
-#pragma unroll
-      for (int h = 0; h < KG; ++h) {
-        const int4* q = reinterpret_cast<const int4*>((KG > 1 ? strip_of(h * NW + wave) : strip) + at);
-        const int4 u = q[0], v = q[1];
-        I[p][0] += u.x, I[p][1] += u.y, I[p][2] += u.z, I[p][3] += u.w;
-        I[p][4] += v.x, I[p][5] += v.y, I[p][6] += v.z, I[p][7] += v.w;
+      for (int q = 0; q < 2; ++q) {
+        const int r = 8 * (u & 1) + 4 * q;
+        *slot(g, u, q) = v4i{c[r], c[r + 1], c[r + 2], c[r + 3]};
       }
-      sx[p] = lsx[wr + 32 * i + p * RP + rl];
     }
-    if (KG > 1 && i + 1 < TI) __syncthreads();
+    __syncthreads();
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      if (KG > 1 && p % KG != g) continue;
-      const int64_t m = m0 + wr + 32 * i + p * RP + rl;
-      if (part) {
+    for (int u = 0; u < UNITS; ++u) {
+      if (u % KG != g) continue;
+      v16i& c = acc[u / 2 / TJ][u / 2 % TJ];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int r = 8 * (u & 1) + 4 * q;
+#pragma unroll
+        for (int o = 1; o < KG; ++o) {
+          const v4i d = *slot((g + o) % KG, u, q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[r + e] += d[e];
+        }
+      }
+    }
+  }
+  const int64_t m1 = m0 + wr + l32, n1 = n0 + wc + 8 * kh;
+  if (part) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int u = 0; u < 2 * TJ; ++u) {
+        if (KG > 1 && (i * 2 * TJ + u) % KG != g) continue;
+        const int64_t m = m1 + 32 * i, n = n1 + 16 * u;
+        const v16i& c = acc[i][u / 2];
+        const int r = 8 * (u & 1);
         if (m < o.M && n < ldp) {
           int4* q = reinterpret_cast<int4*>(part + ((int64_t)blockIdx.y * o.M + m) * ldp + n);
-          q[0] = make_int4(I[p][0], I[p][1], I[p][2], I[p][3]);
-          q[1] = make_int4(I[p][4], I[p][5], I[p][6], I[p][7]);
+          q[0] = make_int4(c[r], c[r + 1], c[r + 2], c[r + 3]);
+          q[1] = make_int4(c[r + 4], c[r + 5], c[r + 6], c[r + 7]);
         }
-      } else if (m < o.M) {
-        store8(o, m, n, I[p], sx[p], sw, bb);
+      }
+    return;
+  }
+  float sw[2 * TJ][8], bb[2 * TJ][8];
+#pragma unroll
+  for (int u = 0; u < 2 * TJ; ++u)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sw[u][e] = lsw[wc + 16 * u + 8 * kh + e], bb[u][e] = lbb[wc + 16 * u + 8 * kh + e];
+  // whole: no bounds to check, and the output's type known outside the loops
+  auto finish = [&](auto whole) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const float sx = lsx[wr + 32 * i + l32];
+#pragma unroll
+      for (int u = 0; u < 2 * TJ; ++u) {
+        if (KG > 1 && (i * 2 * TJ + u) % KG != g) continue;
+        const int64_t m = m1 + 32 * i, n = n1 + 16 * u;
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = (float)acc[i][u / 2][8 * (u & 1) + e] * sx * sw[u][e] + bb[u][e];
+        constexpr int OUT = decltype(whole)::value;
+        if (OUT >= 0) store8_whole<OUT>(o, m, n, y);
+        else if (m < o.M) store8(o, m, n, y);
       }
     }
+  };
+  if (o.wide && o.M - m0 >= BM && o.N - n0 >= BN) {
+    if (o.ydtype == 0) finish(std::integral_constant<int, 0>{});
+    else if (o.ydtype == 1) finish(std::integral_constant<int, 1>{});
+    else finish(std::integral_constant<int, 2>{});
+  } else {
+    finish(std::integral_constant<int, -1>{});
   }
 }
 
@@ -339,7 +371,11 @@ __global__ __launch_bounds__(256) void k6_join(const int* __restrict__ part, int
   }
   float sw[8], bb[8];
   load_channels(o, n, sw, bb);
-  store8(o, m, n, I, o.sX[m], sw, bb);
+  const float sx = o.sX[m];
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = (float)I[e] * sx * sw[e] + bb[e];
+  store8(o, m, n, y);
 }
 
 // ---- few tokens: v_mfma_i32_16x16x64_i8, weights straight from memory
