@@ -4,8 +4,9 @@
 // 127^2 K < 2^31); y = ((float)I s_X[m]) s_W[n] + bias[n], in fp32, then optionally GELU,
 // rounded once to the output type.  qX comes as rows of ld bytes; qW in the fragment order of
 // svdq_prepare_weights_int8: [N / 16][ld / 64] fragments of 1 KB, lane l of a fragment holding
-// channel l & 15 and the 16 codes k = 16 (l >> 4) .., N padded to 16 with zeros.  Integer sums do not depend on their order, so tiles,
-// K ranges and kernels may be chosen freely: every choice gives the same bits.
+// channel l & 15 and the 16 codes k = 16 (l >> 4) .., N padded to 16 with zeros.  Integer sums
+// do not depend on their order, so tiles, K ranges and kernels may be chosen freely: every
+// choice gives the same bits.
 #include <type_traits>
 
 #include "int8.hpp"
@@ -110,26 +111,38 @@ __device__ __forceinline__ void load_channels(const Out& o, int64_t n, float sw[
 //
 // A block owns BM x BN outputs, WM x WN waves with TI x TJ accumulators of 32 x 32 each, and
 // walks K in stages of 128 bytes.  KG K groups of such waves (where there are fewer tiles than
-// compute units) take the stages in turn, each with its own buffers, and meet in the epilogue.  Both operands go global -> LDS by LDS-destination
-// buffer loads into two buffers: the weights in their fragment order, whose reads are
-// contiguous; a token row's eight 16-byte slots XOR-swizzled by the row so that the operand
-// reads of 16 consecutive rows fall in distinct bank groups.  A stage has
-// four steps of 32 bytes of K; a step's operands are read into registers during the step
-// before it.  The one barrier of a stage lies before its last step: by then every wave
-// has read the whole buffer (its last step waits in registers), so the loads of stage k+2
-// can go into it, a whole stage ahead of their use, and the next stage's first
-// operands are read under the last step's MFMAs.
+// compute units) take the stages in turn, each with its own buffers, and meet in the epilogue.
+// Both operands go global -> LDS by LDS-destination buffer loads into two buffers: the weights
+// in their fragment order, whose reads are contiguous; a token row's eight 16-byte slots
+// XOR-swizzled by the row so that the operand reads of 16 consecutive rows fall in distinct
+// bank groups (no bank conflicts counted).  A stage has four steps of 32 bytes of K; a step's
+// operands are read into registers during the step before it.  The one barrier of a stage
+// lies before its last step: by then every wave has read the whole buffer (its last step
+// waits in registers), so the loads of stage k+2 can go into it, a whole stage ahead of their
+// use, and the next stage's first operands are read under the last step's MFMAs.
+// The weights are the MFMA's A operand: a lane then holds one token, its registers channels,
+// and the channels stand in the A operand's rows in such an order that eight registers are
+// eight consecutive channels.  They go from registers to memory in 16-byte pieces, two lanes'
+// pieces adjacent: 128 us for 4608x3072x9216, against 136 by whole 128-byte rows put together
+// in LDS; 64 bytes put together by lane swaps gained nothing over the 32.
 // Rows past M and channel blocks past N lie beyond the buffers' ranges: they read as zeros
-// and are not stored.  Blocks are numbered so that each XCD (own L2; blocks go to the eight XCDs in
-// turn) gets a contiguous run of tiles in strips of 8 tile rows, whose operand panels it
-// then shares.
+// and are not stored.  Blocks are numbered so that each XCD (own L2; blocks go to the eight
+// XCDs in turn) gets a contiguous run of tiles in strips of 8 tile rows, whose operand panels
+// it then shares.
 // P > 1 parts: blockIdx.y takes a range of the stages and stores raw sums to part[y].
-// Outputs leave through a wave-private LDS strip of 32 rows, so that stores are whole
-// 16-byte pieces of consecutive columns.
+//
+// What bounds it: tiles of 256 the card's power (the MFMA units are busy 80% of the time at a
+// clock of 1.9 GHz: 4608x12288x3072 in 140 us, 2.5 POP/s on one set of operands; 97 us with
+// the loads left out); products with few stages the epilogue and the outputs' way to memory
+// (16384x320x1280: 20.7 us, of which 42 MB of stores 5).  Blocks that stay and take tile after
+// tile, with loads running ahead over the tiles' ends, were no faster there (23.5 us against
+// 23.3) and slower in long products (144 against 128): the registers they need crowd the loop.
 //
 // The LDS arrays come from the kernel (ROOM bytes at least each), so that two tile shapes can
 // share them; separate arrays, addressed statically: the compiler then knows that
 // operand reads do not touch the buffer whose loads are in flight, and does not wait for them.
+
+// One of the four arrays, by values: chosen by reference they would be fetched from scratch memory
 __device__ __forceinline__ uint8_t* one_of(int i, uint8_t* a, uint8_t* b, uint8_t* c, uint8_t* d) {
   return i == 0 ? a : i == 1 ? b : i == 2 ? c : d;
 }
@@ -590,25 +603,23 @@ void launch_tiles(const W8A8Plan& p, int64_t ld, const int8_t* qX, const int8_t*
 // ---- the choice of kernel
 //
 // Every choice gives the same bits, so it is made by estimated time alone (us; S = stages of
-// 128 along K, c = blocks that share a compute unit).  The estimates are straight lines
-// through measured times (256 CUs, 20 launches back to back; M x K x N):
-//   few     2.3 + weight bytes x (0.075 + 0.006 M) / MB: 1x3072x9216 4.1 (64 x 2: 7.6), 16x3072x9216 7.1 (7.9),
-//           32x3072x9216 11.2 (8.1), 32x1280x1280 4.1 (5.3), 16x12288x3072 9.6 (64 x 4 in 4 parts: 14.6)
-//   64      one K group: 0.33 S + 1.6 alone on its CU, then 0.50, 0.62, 0.79 S for 2, 3, 4 blocks:
-//           2048x640x640 6.0, 1024x3072x3072 16.4, 512x320x1280 4.1
-//   64 x 2  two K groups (blocks of 8 waves, two to a CU): 0.25 S + 2 alone, 0.38 S + 3.8 for two:
-//           128x1280x1280 5.4 (one group 6.0, four 6.3), 512x3072x3072 13.1 (14.2), inputs out of
-//           cache 13.5 (17.0), 512x12288x3072 39 (56); 2048x640x640 7.2 (6.0)
-//   64 x 4  four K groups (tiles <= CUs): 0.20 S + 3: 128x12288x3072 26.1 (one group 48.3, two 32.0),
-//           64x3072x9216 out of cache 14.1 (20.8, 15.3)
-//   128     0.62 S + 2.5 alone, 1.04 S for two: 512x3072x9216 24.3, 2048x12288x3072 80.5
-//   128 x 2 two K groups (tiles <= CUs): 0.53 S + 2: 1024x12288x3072 53.1 (one group 67.2)
-//   256     1.38 S + 9 (1.15 S where at most 5/8 of the CUs have a tile): 4608x12288x3072 143 (128: 176),
-//           1024x3072x9216 38.8 (46.8), 2048x3072x9216 81.7 (71.6); a last round for at most half of
-//           the CUs runs as tiles of 128 x 256, 0.9 S: 9216x3072x9216 269 (whole tiles 278),
-//           2304x3072x9216 79 (84), with GELU 88 (101), 8192x4096x8448 279 (297)
+// 128 along K, c = blocks that share a compute unit; a round of c blocks takes a[c] S + b[c]).
+// The estimates are fitted to 480 measured times (256 CUs, 20 launches back to back; M x K x N;
+// over those the choice costs 2% more than the best of the six):
+//   few     2.3 + weight bytes x (0.075 + 0.006 M) / MB: 1x3072x9216 4.5 (64 x 2: 8.2), 16x3072x9216 7.2 (8.1),
+//           32x3072x9216 11.2 (8.2), 32x1280x1280 4.2 (5.4), 16x12288x3072 9.7 (64 x 4 in 4 parts: 15)
+//   64      one K group, up to four blocks to a CU: 2048x640x640 5.3 (128: 6.1), 1024x3072x3072 14.8 (128 x 2: 18.2),
+//           512x320x1280 3.7 (128: 5.1)
+//   64 x 2  two K groups (blocks of 8 waves, two to a CU): 512x3072x3072 10.9 (64 x 4: 15.6), 512x12288x3072 36 (64: 50)
+//   64 x 4  four K groups (tiles <= CUs): 256x12288x3072 26.9 (one group 48.5, two 32.5)
+//   128     two blocks to a CU: 512x3072x9216 22.5 (64 x 2: 29), 2048x12288x3072 74.7 (64 x 2: 110), 8192x640x640 9.8 (64: 10.5)
+//   128 x 2 two K groups (tiles <= CUs): 1024x12288x3072 55.3 (one group 69.5), 256x3072x9216 17.5 (one group 19.6)
+//   256     1024x3072x9216 35.3 (128: 42), 4608x12288x3072 121-140 (128: 151), 8192x3072x9216 181 (210); 2048x3072x9216 70.6
+//           (63.2); a last round for at most half of the CUs runs as tiles of 128 x 256: 9216x3072x9216 269 (whole tiles
+//           278), 2304x3072x9216 79 (84), with GELU 88 (101), 16384x320x2560 35 (39)
 // K parts (tiles of 64 with four groups, S / parts >= 24, all parts on the CUs at once) add the
-// partial sums' traffic and a launch, 4 + 12 bytes x M N parts / 6 TB/s: 64x12288x3072 15.7 in 4 parts, 26.6 in one.
+// partial sums' traffic and a launch, 4 + 12 bytes x M N parts / 6 TB/s: 64x12288x3072 15.6 in 4 parts, 26.3 in one.
+
 // Tiles of 256 that a last round leaves for at most half of the CUs, after at least one whole round
 int64_t halved_tiles(int64_t M, int64_t N, int cus) {
   const int64_t T = ((M + 255) / 256) * ((N + 255) / 256), rest = T % cus;
@@ -624,19 +635,23 @@ Cost tiles_cost(int64_t M, int64_t N, int S, int cus, int tile, int groups) {
   const double T = (double)((M + tile - 1) / tile) * (double)((N + tile - 1) / tile);
   const double rounds = T / cus;
   double us = 0.0;
-  auto by_line = [&](const double* a, int most, double b) {  // a[c - 1] per stage with c blocks on a CU
+  auto by_line = [&](const double* a, const double* b, int most) {  // a[c - 1], b[c - 1]: c blocks on a CU
     const double full = (double)(int64_t)(rounds / most), rest = rounds - full * most;
-    us = full * (a[most - 1] * S + b);
-    if (rest > 0) us += a[(int)(rest + 0.999999) - 1] * S + b;
+    us = full * (a[most - 1] * S + b[most - 1]);
+    if (rest > 0) us += a[(int)(rest + 0.999999) - 1] * S + b[(int)(rest + 0.999999) - 1];
   };
-  static const double a64[] = {0.33, 0.50, 0.62, 0.79}, a642[] = {0.25, 0.38}, a644[] = {0.20}, a128[] = {0.62, 1.04},
-                      a1282[] = {0.53};
-  if (tile == 64) groups == 1 ? by_line(a64, 4, 1.6) : groups == 2 ? by_line(a642, 2, rounds > 1.0 ? 3.8 : 2.0) : by_line(a644, 1, 3.0);
-  else if (tile == 128) groups == 1 ? by_line(a128, 2, 2.5) : by_line(a1282, 1, 2.0);
+  static const double a64[] = {0.315, 0.42, 0.42, 0.64}, b64[] = {0.0, 0.8, 0.8, 0.8}, a642[] = {0.26, 0.335},
+                      b642[] = {2.5, 3.6}, a644[] = {0.19}, b644[] = {3.6}, a128[] = {0.575, 0.725}, b128[] = {2.6, 5.6},
+                      a1282[] = {0.46}, b1282[] = {5.7};
+  if (tile == 64 && groups == 1) by_line(a64, b64, 4), us += 2.6;
+  else if (tile == 64 && groups == 2) by_line(a642, b642, 2), us += 1.0;
+  else if (tile == 64) by_line(a644, b644, 1), us += 0.9;
+  else if (tile == 128 && groups == 1) by_line(a128, b128, 2), us += 1.1;
+  else if (tile == 128) by_line(a1282, b1282, 1), us += 0.2;
   else {
     const double full = (double)(int64_t)rounds, rest = rounds - full;
     const bool halved = full > 0 && rest <= 0.5;
-    us = full * (1.38 * S + 9.0) + (rest == 0 ? 0.0 : halved ? 0.9 * S + 9.0 : rest <= 0.625 ? 1.15 * S + 9.0 : 1.38 * S + 9.0);
+    us = full * (1.245 * S + 8.3) + (rest == 0 ? 0.0 : (halved ? 0.9 : rest <= 0.625 ? 1.08 : 1.245) * S + 8.3);
   }
   return Cost{us, tile, groups, 1};
 }
