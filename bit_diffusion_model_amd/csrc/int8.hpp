@@ -12,9 +12,10 @@ namespace svdq {
 // Row reads without branches, so that all of a row's loads can be issued before the first is
 // waited for.  A Row covers K values from p; load(k) starts the read of values k .. k+7 and
 // value() turns it into fp32; what lies at or past K reads as 0 (the buffer's range).
-// VEC: p is 4-byte aligned (16-byte loads need no more); otherwise bf16 values are loaded one by one.
-// The range of an odd number of bf16 values ends in the middle of a word whose first half
-// is the row's, and value() drops the second half.
+// VEC: p is 4-byte aligned (16-byte loads need no more).  A bf16 row that may begin in the middle
+// of a word is read from the word's start, 20 bytes for 8 values, and shifted.  Only whole aligned
+// words are read: the first and the last may hold a neighbour's value, never an unmapped byte, and
+// value() drops the last one's second half where that is not the row's.
 template <typename T, bool VEC>
 struct Row;
 
@@ -53,18 +54,28 @@ struct Row<uint16_t, true> {
 
 template <>
 struct Row<uint16_t, false> {
-  typedef struct { uint32_t h[8]; } Raw;
+  typedef struct { uint4 a; uint32_t b; } Raw;
   __amdgpu_buffer_rsrc_t r;
-  __device__ __forceinline__ Row(const uint16_t* p, int K) : r(make_rsrc(p, (uint32_t)K * 2)) {}
-  __device__ __forceinline__ Raw load(int k) const {
-    Raw w;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w.h[e] = buf_load2(r, (uint32_t)(k + e) * 2);
-    return w;
+  uint32_t shift;  // 16 where the row begins in the middle of a word, else 0
+  int end;         // K where a neighbour's value follows the last one in its word, else past every k
+  __device__ __forceinline__ Row(const uint16_t* p, int K) : shift((uint32_t)(reinterpret_cast<uintptr_t>(p) & 2) * 8) {
+    const uint32_t halves = (uint32_t)K + shift / 16;
+    r = make_rsrc(p - shift / 16, K > 0 ? (halves + 1) / 2 * 4 : 0);
+    end = halves & 1 ? K : 0x7FFFFFFF;
   }
-  __device__ __forceinline__ void value(const Raw& w, int, float v[8]) const {
+  __device__ __forceinline__ Raw load(int k) const {
+    return Raw{buf_load16(r, (uint32_t)k * 2), buf_load4(r, (uint32_t)k * 2 + 16)};
+  }
+  __device__ __forceinline__ void value(const Raw& w, int k, float v[8]) const {
+    const uint32_t x[5] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w.h[e] << 16);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t d = __builtin_amdgcn_alignbit(x[i + 1], x[i], shift);
+      v[2 * i] = bf16_lo_to_f32(d), v[2 * i + 1] = bf16_hi_to_f32(d);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k + e == end) v[e] = 0.0f;
   }
 };
 

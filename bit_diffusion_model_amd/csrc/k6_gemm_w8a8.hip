@@ -57,7 +57,6 @@ struct Out {
   void* Y;
   int64_t ldy, M, N;
   int ydtype;
-  bool wide;  // Y's rows are 16-byte aligned
 };
 
 constexpr float kNoBias = -0.0f;  // y + -0 is y, whatever y's sign
@@ -68,17 +67,24 @@ __device__ __forceinline__ void store1(const Out& o, int64_t m, int64_t n, float
   else static_cast<__bf16*>(o.Y)[m * o.ldy + n] = (__bf16)(o.ydtype == 2 ? gelu5(y) : y);
 }
 
-// Eight outputs n .. n + 7 (n a multiple of 8) of row m.  WHOLE: all of them lie within Y and its
-// rows are 16-byte aligned; else channels may lie past N and the rows may have any alignment.
-// OUT: 0 fp32, 1 bf16, 2 bf16 of GELU.
+// Sixteen bytes at any output's address: the memory takes them at every alignment (rows of an odd
+// length included: 4141x1408x4274 fp32 95 us by single outputs, 50 so)
+typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
+
+// Eight outputs n .. n + 7 (n a multiple of 8) of row m.  WHOLE: all of them lie within Y; else
+// channels may lie past N.  OUT: 0 fp32, 1 bf16, 2 bf16 of GELU.
 template <int OUT, bool WHOLE>
 __device__ __forceinline__ void store8(const Out& o, int64_t m, int64_t n, const float y[8]) {
-  const bool whole = WHOLE || (o.wide && n + 8 <= o.N);
+  const bool whole = WHOLE || n + 8 <= o.N;
   if constexpr (OUT == 0) {
     float* p = static_cast<float*>(o.Y) + m * o.ldy + n;
     if (whole) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4_2 w = {__float_as_uint(y[4 * h]), __float_as_uint(y[4 * h + 1]), __float_as_uint(y[4 * h + 2]),
+                           __float_as_uint(y[4 * h + 3])};
+        reinterpret_cast<u32x4_2*>(p)[h] = w;
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -86,11 +92,12 @@ __device__ __forceinline__ void store8(const Out& o, int64_t m, int64_t n, const
     }
   } else {
     uint16_t* p = static_cast<uint16_t*>(o.Y) + m * o.ldy + n;
-    uint32_t w[4];
+    u32x4_2 w;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = OUT == 2 ? bf16_pair(gelu5(y[2 * e]), gelu5(y[2 * e + 1])) : bf16_pair(y[2 * e], y[2 * e + 1]);
+    for (int e = 0; e < 4; ++e)
+      w[e] = OUT == 2 ? bf16_pair(gelu5(y[2 * e]), gelu5(y[2 * e + 1])) : bf16_pair(y[2 * e], y[2 * e + 1]);
     if (whole) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<u32x4_2*>(p) = w;
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -349,7 +356,7 @@ __device__ __forceinline__ void tile(const int8_t* __restrict__ qX, int64_t ld, 
         }
     }
   };
-  if (o.wide && rows == BM && cols == BN) finish(std::true_type{});
+  if (rows == BM && cols == BN) finish(std::true_type{});
   else finish(std::false_type{});
 }
 
@@ -617,8 +624,8 @@ void launch_tiles(const W8A8Plan& p, int64_t ld, const int8_t* qX, const int8_t*
 //   256     1024x3072x9216 35.3 (128: 42), 4608x12288x3072 121-140 (128: 151), 8192x3072x9216 181 (210); 2048x3072x9216 70.6
 //           (63.2); a last round for at most half of the CUs runs as tiles of 128 x 256: 9216x3072x9216 269 (whole tiles
 //           278), 2304x3072x9216 79 (84), with GELU 88 (101), 16384x320x2560 35 (39)
-// K parts (tiles of 64 with four groups, S / parts >= 24, all parts on the CUs at once) add the
-// partial sums' traffic and a launch, 4 + 12 bytes x M N parts / 6 TB/s: 64x12288x3072 15.6 in 4 parts, 26.3 in one.
+// K parts (tiles of 64 with four groups, S / parts >= 8, all parts on the CUs at once) add the
+// partial sums' traffic and a launch, 6 + 12 bytes x M N parts / 6 TB/s: 64x12288x3072 15.6 in 4 parts, 26.3 in one.
 
 // Tiles of 256 that a last round leaves for at most half of the CUs, after at least one whole round
 int64_t halved_tiles(int64_t M, int64_t N, int cus) {
@@ -673,11 +680,11 @@ W8A8Plan plan_w8a8(int64_t M, int64_t K, int64_t N) {
   if (T128 <= cus) take(tiles_cost(M, N, S, cus, 128, 2));
   if (T64 <= 2 * cus) take(tiles_cost(M, N, S, cus, 64, 2));
   if (T64 <= cus) {
-    for (int parts = 1; parts <= 8 && parts * T64 <= cus && (parts == 1 || S / parts >= 24); parts *= 2) {
+    for (int parts = 1; parts <= 8 && parts * T64 <= cus && (parts == 1 || S / parts >= 8); parts *= 2) {
       const int per = (S + parts - 1) / parts;
       Cost c = tiles_cost(M, N, per, cus, 64, 4);
       c.parts = (S + per - 1) / per;  // no empty part
-      if (c.parts > 1) c.us += 4.0 + 12.0 * (double)(M * ldp) * c.parts / 6e6;
+      if (c.parts > 1) c.us += 6.0 + 12.0 * (double)(M * ldp) * c.parts / 6e6;
       take(c);
     }
   }
@@ -698,7 +705,7 @@ bool few_layer(int64_t M, int64_t K) {
 hipError_t launch_few_layer(int64_t M, int64_t K, int64_t N, const void* X, int xdtype, int64_t ldx, const float* inv_s,
                             const int8_t* qW, const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype,
                             hipStream_t st) {
-  const Out o{nullptr, sW, bias, Y, ldy, M, N, ydtype, false};
+  const Out o{nullptr, sW, bias, Y, ldy, M, N, ydtype};
   const int64_t ld = i8_ld(K);
   const dim3 g((uint32_t)((N + 15) / 16)), b(64 * FEW_NW);
   const size_t lds = (size_t)M * (size_t)(ld + 16);
@@ -721,8 +728,7 @@ hipError_t launch_few_layer(int64_t M, int64_t K, int64_t N, const void* X, int 
 hipError_t launch_w8a8(int64_t M, int64_t K, int64_t N, const int8_t* qX, const float* sX, const int8_t* qW,
                        const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype, void* ws, hipStream_t st) {
   const int64_t ld = i8_ld(K);
-  const bool wide = reinterpret_cast<uintptr_t>(Y) % 16 == 0 && ldy % (ydtype == 0 ? 4 : 8) == 0;
-  const Out o{sX, sW, bias, Y, ldy, M, N, ydtype, wide};
+  const Out o{sX, sW, bias, Y, ldy, M, N, ydtype};
   const W8A8Plan p = plan_w8a8(M, K, N);
   if (p.tile == 0) {
     const dim3 g((uint32_t)((N + 15) / 16)), b(64 * FEW_NW);

@@ -30,10 +30,11 @@ namespace {
 
 constexpr int ST_NT = 256, AP_NT = 256;  // threads of the statistics and output passes (1024: 16-27 us for 10)
 
-// ---- vectors of V channels; rows are 4-byte aligned for V > 1
+// ---- vectors of V channels, at any value's address: the memory takes wide loads and stores at every alignment
 
-typedef uint32_t u32x4a __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint32_t u32x2a __attribute__((ext_vector_type(2), aligned(4)));
+typedef uint32_t u32x4a __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2a __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32a __attribute__((aligned(2)));
 
 template <typename T, int V>
 struct Vec {  // V values as loaded
@@ -55,7 +56,7 @@ __device__ __forceinline__ Vec<T, V> loadv(const T* p) {
     const u32x2a q = *reinterpret_cast<const u32x2a*>(p);
     r.w[0] = q.x, r.w[1] = q.y;
   } else if constexpr (W == 1) {
-    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+    r.w[0] = *reinterpret_cast<const u32a*>(p);
   } else {
     r.w[0] = *p;
   }
@@ -106,7 +107,7 @@ __device__ __forceinline__ void storev(TY* p, const float v[V]) {
   } else if constexpr (W == 2) {
     *reinterpret_cast<u32x2a*>(p) = u32x2a{w[0], w[1]};
   } else if constexpr (W == 1) {
-    *reinterpret_cast<uint32_t*>(p) = w[0];
+    *reinterpret_cast<u32a*>(p) = w[0];
   } else {
     *reinterpret_cast<__bf16*>(p) = (__bf16)v[0];
   }
@@ -533,7 +534,6 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
   }
   __syncthreads();
   for (int i = wave * U; i < rows; i += NW * U) {
-    const RowX any = row_at(0);
     load(i + NW * U, next);  // under way while these rows are computed
     float v[U][NC][8];
     uint32_t a[U] = {};
@@ -542,7 +542,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
       const int k8 = lane + 64 * j;
       const bool in = k8 < c8;
 #pragma unroll
-      for (int u = 0; u < U; ++u) any.value(raw[u][j], 8 * k8, v[u][j]);
+      for (int u = 0; u < U; ++u) row_at(i + u).value(raw[u][j], 8 * k8, v[u][j]);
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -584,7 +584,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
   }
 }
 
-// The same for narrow rows (C <= 8 LPR, a multiple of 8; rows 4-byte aligned): LPR lanes per row, 64 /
+// The same for narrow rows (C <= 8 LPR, a multiple of 8): LPR lanes per row, 64 /
 // LPR rows per wave at once; a lane keeps its 8 channels' coefficients in registers.
 template <typename T, int LPR>
 __global__ __launch_bounds__(AP_NT) void k7_apply_quant_narrow(const T* __restrict__ X, int64_t bsx, int64_t ldx,
@@ -654,14 +654,10 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant_narrow(const T* __restri
 
 // ---- launches
 
-bool vec_ok(const void* p, int64_t bs, int64_t ld, int dtype) {
-  return rows_aligned4(p, ld, dtype) && (dtype == 0 || bs % 2 == 0);
-}
-
-// Vector width of k7_one: the widest of 8, 4, 2 that divides a group and keeps 4-byte alignment
-int one_width(int cpg, bool vec, int dtype) {
+// Vector width of k7_one: the widest of 8, 4, 2 that divides a group
+int one_width(int cpg) {
   for (int v = 8; v > 1; v /= 2)
-    if (cpg % v == 0 && (vec || dtype == 0)) return v;
+    if (cpg % v == 0) return v;
   return 1;
 }
 
@@ -715,14 +711,13 @@ void launch_apply(const NormArgs& a, const NormPlan& p, const Stats& s, void* Y,
 Stats run_stats(const NormArgs& a, const NormPlan& p, void* ws, hipStream_t st) {
   float2* part = static_cast<float2*>(ws);
   Stats s{part, 0, a.S, p.chunk, a.C, a.G, a.eps};
-  const bool vec = vec_ok(a.X, a.bsx, a.ldx, a.xdtype);
   if (p.one) {
-    const int w = one_width(a.C / a.G, vec, a.xdtype);
+    const int w = one_width(a.C / a.G);
     a.xdtype == 0 ? launch_one<float, float>(a, w, nullptr, 0, 0, part, st)
                   : launch_one<uint16_t, uint16_t>(a, w, nullptr, 0, 0, part, st);
     return s;
   }
-  const bool v8 = a.C % 8 == 0 && vec;
+  const bool v8 = a.C % 8 == 0;
   if (a.xdtype == 0) v8 ? launch_stats<float, 8>(a, p, part, st) : launch_stats<float, 1>(a, p, part, st);
   else v8 ? launch_stats<uint16_t, 8>(a, p, part, st) : launch_stats<uint16_t, 1>(a, p, part, st);
   s.parts = (int)p.parts;
@@ -766,9 +761,8 @@ NormPlan plan_norm(int64_t B, int64_t S, int C, int G) {
 
 hipError_t launch_norm(const NormArgs& a, void* Y, int ydtype, int64_t bsy, int64_t ldy, void* ws, hipStream_t st) {
   const NormPlan p = plan_norm(a.B, a.S, a.C, a.G);
-  const bool vec = vec_ok(a.X, a.bsx, a.ldx, a.xdtype) && vec_ok(Y, bsy, ldy, ydtype);
   if (p.one) {
-    const int w = one_width(a.C / a.G, vec, a.xdtype == 0 && ydtype == 0 ? 0 : 1);
+    const int w = one_width(a.C / a.G);
     if (a.xdtype == 0 && ydtype == 0) launch_one<float, float>(a, w, Y, bsy, ldy, nullptr, st);
     else if (a.xdtype == 0) launch_one<float, uint16_t>(a, w, Y, bsy, ldy, nullptr, st);
     else if (ydtype == 0) launch_one<uint16_t, float>(a, w, Y, bsy, ldy, nullptr, st);
@@ -776,7 +770,7 @@ hipError_t launch_norm(const NormArgs& a, void* Y, int ydtype, int64_t bsy, int6
     return hipGetLastError();
   }
   const Stats s = run_stats(a, p, ws, st);
-  const bool v8 = a.C % 8 == 0 && vec;
+  const bool v8 = a.C % 8 == 0;
   if (a.xdtype == 0 && ydtype == 0)
     v8 ? launch_apply<float, float, 8>(a, p, s, Y, bsy, ldy, st) : launch_apply<float, float, 1>(a, p, s, Y, bsy, ldy, st);
   else if (a.xdtype == 0)
@@ -791,7 +785,7 @@ hipError_t launch_norm(const NormArgs& a, void* Y, int ydtype, int64_t bsy, int6
 hipError_t launch_norm_quant(const NormArgs& a, const float* inv_s, int8_t* qX, float* sX, void* ws, hipStream_t st) {
   const NormPlan p = plan_norm(a.B, a.S, a.C, a.G);
   const Stats s = run_stats(a, p, ws, st);
-  const bool vec = vec_ok(a.X, a.bsx, a.ldx, a.xdtype);
+  const bool vec = rows_aligned4(a.X, a.ldx, a.xdtype) && (a.xdtype == 0 || a.bsx % 2 == 0);
   const size_t bytes = (size_t)((a.C + 7) / 8) * 8 * 16 + (size_t)a.G * 8;
   const int64_t ldq = i8_ld(a.C);
   // about 768 blocks; whole turns of the four waves where a wave takes several rows at once
@@ -808,7 +802,7 @@ hipError_t launch_norm_quant(const NormArgs& a, const float* inv_s, int8_t* qX, 
     if (a.xdtype == 0) go(k7_apply_quant<float, true, NC, U>, x32, bytes);
     else vec ? go(k7_apply_quant<uint16_t, true, NC, U>, x16, bytes) : go(k7_apply_quant<uint16_t, false, NC, U>, x16, bytes);
   };
-  const bool even = a.C % 8 == 0 && vec;
+  const bool even = a.C % 8 == 0;
   if (even && a.C <= 128) {
     a.xdtype == 0 ? go(k7_apply_quant_narrow<float, 16>, x32, (size_t)a.G * 8)
                   : go(k7_apply_quant_narrow<uint16_t, 16>, x16, (size_t)a.G * 8);

@@ -12,7 +12,7 @@ import pytest
 
 from bit_diffusion_model_amd import svdq
 from oracle import int8 as o8
-from test_gpu_int8 import host
+from test_gpu_int8 import at_any_value, host
 
 pytestmark = pytest.mark.gpu
 U, L = 2.0 ** -24, 400
@@ -94,6 +94,33 @@ def test_strides(pad, rows_pad, xd):
     own = X.clone() if pad == 0 and rows_pad == 0 else X
     gn.forward(own, svdq.F32 if xd == "f32" else svdq.BF16, out=own)
     assert (np.abs(host(own) - want) <= tol + (0 if xd == "f32" else 2.0 ** -8 * np.abs(want))).all()
+
+
+@pytest.mark.parametrize("B,S,G,C,pad", [(2, 37, 4, 24, 1), (3, 150, 8, 96, 3), (1, 40, 8, 77 * 8, 0), (2, 700, 32, 416, 1),
+                                         (1, 3000, 8, 40, 3), (2, 1500, 32, 1184, 5), (1, 900, 3, 129, 0), (2, 2, 2, 4, 1)])
+@pytest.mark.parametrize("xd,yd", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16")])
+def test_rows_at_any_value(B, S, G, C, pad, xd, yd):
+    """Positions that begin at any value, between NaNs that must not be taken in; the norm's values and the codes' differ
+    from the contiguous call's by no more than the bounds, and nothing is written beside the rows."""
+    torch = _torch()
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}
+    X = make_x(B, S, C, dt[xd], 11).contiguous()
+    gamma, beta = affine(C, 3)
+    gn = svdq.GroupNorm(G, C, gamma, beta, 1e-6, svdq.GN_SILU)
+    strides = (S * (C + pad) + 1, C + pad, 1)
+    _, x = at_any_value((B, S, C), strides, X.dtype, float("nan"))
+    x.copy_(X)
+    want, tol = reference(host(X), G, gamma, beta, 1e-6, "silu")
+    buf, y = at_any_value((B, S, C), strides, dt[yd], 9.0)
+    gn.forward(x, svdq.F32 if yd == "f32" else svdq.BF16, out=y)
+    assert (np.abs(host(y) - want) <= tol + (0 if yd == "f32" else 2.0 ** -8 * np.abs(want))).all()
+    y.fill_(9.0)
+    assert (buf == 9.0).all()
+    q, s = gn.quantize(x)
+    s = host(s)[:, None]
+    q = q.cpu().numpy()[:, :C].astype(np.float64)
+    # half a step of the row's scale (a 127th of its largest magnitude), and the norm's own error
+    assert (np.abs(q * s - want.reshape(B * S, C)) <= 0.501 * s + 2 * tol.reshape(B * S, C).max(1, keepdims=True)).all()
 
 
 def test_images_of_positions():

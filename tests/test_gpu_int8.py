@@ -169,6 +169,37 @@ def test_layer(M, K, N, pad, dt, yd):
     check_product(Y, q, s, qW[:, :K], sW, b, ydtype, f"layer {M}x{K}x{N}")
 
 
+def at_any_value(shape, stride, dtype, fill, device="cuda:0"):
+    """(buffer, view): a view of `shape` whose first value is the buffer's second, so that rows of an odd stride begin
+    at both halves of a word; everything else of the buffer holds `fill`."""
+    torch = _torch()
+    span = 1 + sum((n - 1) * s for n, s in zip(shape, stride)) + 1
+    buf = torch.full((span + 1,), fill, dtype=dtype, device=device)
+    return buf, torch.as_strided(buf, shape, stride, 1)
+
+
+@pytest.mark.parametrize("M,K,N,pad", [(1, 129, 131, 0), (4, 322, 64, 1), (70, 128, 131, 3), (300, 320, 77, 1), (90, 4609, 261, 2),
+                                       (33, 2057, 40, 0), (2, 16389, 24, 1), (4096, 301, 2051, 0), (2304, 64, 1030, 1)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("yd", ["f32", "bf16", "gelu"])
+def test_rows_at_any_value(M, K, N, pad, dt, yd):
+    """Rows that begin at any value, between NaNs that must not be taken in: the bits of the contiguous call, and nothing
+    written beside the rows."""
+    torch = _torch()
+    ydtype = {"f32": svdq.F32, "bf16": svdq.BF16, "gelu": svdq.BF16_GELU}[yd]
+    X = make_x(M, K, {"bf16": torch.bfloat16, "f32": torch.float32}[dt], M + K).contiguous()
+    qW, sW, b = weights(N, K, M + N, True)
+    lin = svdq.Int8Linear(qW, sW, K, inv_s=(0.2 + np.random.default_rng(N).random(K)).astype(np.float32), bias=b)
+    want = lin.forward(X, ydtype)
+    _, x = at_any_value((M, K), (K + pad, 1), X.dtype, float("nan"))
+    x.copy_(X)
+    buf, y = at_any_value((M, N), (N + pad, 1), want.dtype, 7.0)
+    lin.forward(x, ydtype, out=y)
+    assert torch.equal(y, want)
+    y.fill_(7.0)
+    assert (buf == 7.0).all()
+
+
 def test_layer_empty_and_other_stream():
     torch = _torch()
     qW, sW, b = weights(48, 256, 3, True)
