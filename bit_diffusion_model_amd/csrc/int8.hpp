@@ -91,8 +91,11 @@ template <int L, typename F>
 __device__ __forceinline__ uint32_t lane_reduce(uint32_t v, F f) {
   v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));   // quad [1 0 3 2]
   v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));   // quad [2 3 0 1]
-  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, true));  // row rotated by 4
-  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true));  // row rotated by 8
+  if constexpr (L == 8) v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));  // halves of a row mirrored
+  if constexpr (L >= 16) {
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, true));  // row rotated by 4
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true));  // row rotated by 8
+  }
   if constexpr (L >= 32) {
     const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
     v = f(r[0], r[1]);

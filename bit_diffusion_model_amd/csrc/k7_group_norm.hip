@@ -644,9 +644,10 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant_narrow(const T* __restri
       row_scale(wave_umax<LPR>(top), s, q);
       if (r >= rows) continue;
       const int64_t row = blockIdx.y * st.S + r0 + r;
-      if (c < ldq)
-        *reinterpret_cast<uint2*>(qX + row * ldq + c) =
-            make_uint2(codes4(v[0], v[1], v[2], v[3], q), codes4(v[4], v[5], v[6], v[7], q));
+      int8_t* to = qX + row * ldq + c;
+      *reinterpret_cast<uint2*>(to) = make_uint2(codes4(v[0], v[1], v[2], v[3], q), codes4(v[4], v[5], v[6], v[7], q));
+#pragma unroll
+      for (int z = 8 * LPR; z < 128; z += 8 * LPR) *reinterpret_cast<uint2*>(to + z) = make_uint2(0, 0);  // to the end of the row
       if (li == 0) sX[row] = s;
     }
   }
@@ -803,12 +804,16 @@ hipError_t launch_norm_quant(const NormArgs& a, const float* inv_s, int8_t* qX, 
     else vec ? go(k7_apply_quant<uint16_t, true, NC, U>, x16, bytes) : go(k7_apply_quant<uint16_t, false, NC, U>, x16, bytes);
   };
   const bool even = a.C % 8 == 0;
-  if (even && a.C <= 128) {
-    a.xdtype == 0 ? go(k7_apply_quant_narrow<float, 16>, x32, (size_t)a.G * 8)
-                  : go(k7_apply_quant_narrow<uint16_t, 16>, x16, (size_t)a.G * 8);
-  } else if (even && a.C <= 256) {
-    a.xdtype == 0 ? go(k7_apply_quant_narrow<float, 32>, x32, (size_t)a.G * 8)
-                  : go(k7_apply_quant_narrow<uint16_t, 32>, x16, (size_t)a.G * 8);
+  auto narrow = [&](auto lpr) {
+    constexpr int LPR = decltype(lpr)::value;
+    a.xdtype == 0 ? go(k7_apply_quant_narrow<float, LPR>, x32, (size_t)a.G * 8)
+                  : go(k7_apply_quant_narrow<uint16_t, LPR>, x16, (size_t)a.G * 8);
+  };
+  if (even && a.C <= 256) {
+    if (a.C <= 32) narrow(std::integral_constant<int, 4>{});
+    else if (a.C <= 64) narrow(std::integral_constant<int, 8>{});
+    else if (a.C <= 128) narrow(std::integral_constant<int, 16>{});
+    else narrow(std::integral_constant<int, 32>{});
   } else if (ldq <= 512) by_type(std::integral_constant<int, 1>{});
   else if (ldq <= 1024) by_type(std::integral_constant<int, 2>{});
   else if (ldq <= 2048) by_type(std::integral_constant<int, 4>{});
