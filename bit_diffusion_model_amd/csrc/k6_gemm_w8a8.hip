@@ -419,7 +419,8 @@ __global__ __launch_bounds__(256) void k6_join(const int* __restrict__ part, int
 
 // ---- few tokens: v_mfma_i32_16x16x64_i8, weights straight from memory
 //
-// Bound by the weights' read.  A block of 8 waves owns 16 channels (one channel block of the
+// Bound by the weights' read (1x3072x9216 4.5 us with the launch: 28 MB at 6.3 TB/s; more rows cost
+// their own reads: 16 7.2).  A block of 8 waves owns 16 channels (one channel block of the
 // weights' fragment order) and up to 16 NT tokens; its waves take the fragments of 64 along K in
 // turn, U loads of 1 KB in flight each, and add their integer sums in LDS.  The weights are
 // the A operand, the tokens the B operand: lane l holds token l & 15 and k = 16 (l >> 4) .. + 15.
@@ -695,9 +696,9 @@ W8A8Plan plan_w8a8(int64_t M, int64_t K, int64_t N) {
   return p;
 }
 
-// Measured against the quantizer's launch and k6_few (us): 4x3072x9216 6.6 against 2.6 + 4.9, 4x3072x12288
-// 8.1 against 3.1 + 6.3, 2x1280x1280 3.8 against 2.9 + 2.7; at 6 and 8 rows the values no longer fit 80
-// registers (8x3072x3072 10.7 against 2.8 + 3.2).
+// Measured against the quantizer's launch and k6_few (us): 4x3072x9216 6.3 against 2.6 + 5.0, 4x3072x12288
+// 7.6 against 3.2 + 6.0, 2x1280x1280 3.4 against 2.8 + 2.7; at 6 and 8 rows the values no longer fit 80
+// registers (8x3072x3072 10.7 against 2.9 + 3.2).
 bool few_layer(int64_t M, int64_t K) {
   return M <= 4 && i8_ld(K) <= 4096;
 }

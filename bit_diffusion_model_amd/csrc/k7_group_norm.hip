@@ -5,15 +5,19 @@
 // group's cpg channels: mean, var (biased); y = act((x - mean) / sqrt(var + eps) gamma_c +
 // beta_c), x - mean formed first so that a mean far from zero costs no digits.
 //
-// Bound by HBM: x read, y written, once each at best.  Three kernels:
+// Bound by HBM where x and y pass the 256 MB cache (262144x256 fp32, x read twice and y written:
+// 151 us, 5.3 TB/s), by the cache below that (65536x256 bf16 29.3 us), by launches and the
+// blocks' meeting in the smallest.  Three kernels:
 //  * k7_one: a block holds one image's group in registers: x read once, mean and variance by
-//    two exact passes over the registers, one launch.  Where the group fits (32 values per
-//    thread of 1024);
+//    two exact passes over the registers, one launch.  Taken where a group has at most 32768
+//    values, 32 per thread of 1024 (us, against the two launches below: 2x64x1280 in groups of
+//    40 3.8 against 10.5, 2x2048x512 of 16 8.5 against 13.0; 1x4096x320 of 10, 40960 values: 13.2
+//    against 12.3; with 64 values per thread 26);
 //  * k7_stats, then k7_apply (or k7_apply_quant): statistics per block of positions, and the
 //    output pass, which first joins the blocks' statistics (by itself where there are few,
-//    after k7_join where there are many: an output block would read them all).  A thread keeps the same V consecutive channels over
-//    all its positions, so group boundaries may fall anywhere: sums are kept per channel and
-//    meet per group in LDS.
+//    after k7_join where there are many: an output block would read them all).  A thread keeps
+//    the same V consecutive channels over all its positions, so group boundaries may fall
+//    anywhere: sums are kept per channel and meet per group in LDS.
 // Statistics in fp32: a thread sums d = x - p and d^2 per channel, p its first value, so that
 // (mean, M2) = (p + sum d / n, sum d^2 - (sum d)^2 / n): since p is one of the n values, M2 >=
 // (p - mean)^2 and the subtraction loses at most a factor n (the thread's positions, 32 or so).
@@ -88,7 +92,9 @@ __device__ __forceinline__ void put(P* p, W w) {
   else *p = w;
 }
 
-// NT: past the caches, for outputs that nothing reads before they are evicted
+// NT: past the caches, for outputs that nothing reads before they are evicted (where x and y together
+// pass the 256 MB cache: 262144x256 fp32 172 -> 156 us, 1048576x128 bf16 163 -> 135; below, the next
+// operator finds y in the cache)
 template <typename TY, int V, bool NT = false>
 __device__ __forceinline__ void storev(TY* p, const float v[V]) {
   constexpr int W = V * (int)sizeof(TY) / 4;
@@ -494,6 +500,8 @@ __global__ __launch_bounds__(AP_NT) void k7_apply(const T* __restrict__ X, int64
 // The output pass into codes: a wave takes U whole positions (rows of C channels) at once, NC chunks
 // of 512 channels each in registers.  Per channel (mean, rstd gamma, beta, inv_s) wait in LDS, eight
 // planes of C / 8 so that neighbouring lanes read neighbouring 16 bytes, read once for U rows.
+// The next rows' loads are under way while these are computed (4x4096x320 21.4 -> 18.7 us, both
+// launches; about 30 VALU instructions a value are what bounds it now).
 template <typename T, bool VEC, int NC, int U>
 __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X, int64_t bsx, int64_t ldx,
                                                         int64_t chunk, Stats st, const float* __restrict__ gamma,
@@ -584,8 +592,10 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
   }
 }
 
-// The same for narrow rows (C <= 8 LPR, a multiple of 8): LPR lanes per row, 64 /
-// LPR rows per wave at once; a lane keeps its 8 channels' coefficients in registers.
+// The same for narrow rows (C <= 8 LPR, a multiple of 8): LPR lanes per row, 64 / LPR rows per
+// wave at once; a lane keeps its 8 channels' coefficients in registers.  us, all launches, against
+// a wave per row: 65536x256 35.2 (40.6), x128 27.0 (38.7), x64 19.3 (36.8; 16 lanes a row 21.9), x32 16.7
+// (36.1; 16 lanes 19.9); a few thousand rows cost the same either way (2x4096x128 15.8, 14.3).
 template <typename T, int LPR>
 __global__ __launch_bounds__(AP_NT) void k7_apply_quant_narrow(const T* __restrict__ X, int64_t bsx, int64_t ldx,
                                                                int64_t chunk, Stats st, const float* __restrict__ gamma,
@@ -629,6 +639,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant_narrow(const T* __restri
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = i + u * STEP;
+      if (r - first >= rows) break;  // the same for the whole block
       float v[8];
       valuev<T, 8>(raw[u], v);
       uint32_t top = 0;
