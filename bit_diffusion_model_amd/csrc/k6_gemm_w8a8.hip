@@ -612,12 +612,12 @@ void launch_tiles(const W8A8Plan& p, int64_t ld, const int8_t* qX, const int8_t*
 //
 // Every choice gives the same bits, so it is made by estimated time alone (us; S = stages of
 // 128 along K, c = blocks that share a compute unit; a round of c blocks takes a[c] S + b[c]).
-// The estimates are fitted to 480 measured times (256 CUs, 20 launches back to back; M x K x N;
+// The estimates are fitted to 550 measured times (256 CUs, 20 launches back to back; M x K x N;
 // over those the choice costs 2% more than the best of the six):
 //   few     2.3 + weight bytes x (0.075 + 0.006 M) / MB: 1x3072x9216 4.5 (64 x 2: 8.2), 16x3072x9216 7.2 (8.1),
 //           32x3072x9216 11.2 (8.2), 32x1280x1280 4.2 (5.4), 16x12288x3072 9.7 (64 x 4 in 4 parts: 15)
 //   64      one K group, up to four blocks to a CU: 2048x640x640 5.3 (128: 6.1), 1024x3072x3072 14.8 (128 x 2: 18.2),
-//           512x320x1280 3.7 (128: 5.1)
+//           512x320x1280 3.7 (128: 5.1); 16384x320x1280 27 (128: 20.7)
 //   64 x 2  two K groups (blocks of 8 waves, two to a CU): 512x3072x3072 10.9 (64 x 4: 15.6), 512x12288x3072 36 (64: 50)
 //   64 x 4  four K groups (tiles <= CUs): 256x12288x3072 26.9 (one group 48.5, two 32.5)
 //   128     two blocks to a CU: 512x3072x9216 22.5 (64 x 2: 29), 2048x12288x3072 74.7 (64 x 2: 110), 8192x640x640 9.8 (64: 10.5)
@@ -648,7 +648,7 @@ Cost tiles_cost(int64_t M, int64_t N, int S, int cus, int tile, int groups) {
     us = full * (a[most - 1] * S + b[most - 1]);
     if (rest > 0) us += a[(int)(rest + 0.999999) - 1] * S + b[(int)(rest + 0.999999) - 1];
   };
-  static const double a64[] = {0.315, 0.42, 0.42, 0.64}, b64[] = {0.0, 0.8, 0.8, 0.8}, a642[] = {0.26, 0.335},
+  static const double a64[] = {0.315, 0.42, 0.42, 0.64}, b64[] = {0.0, 0.8, 0.8, 2.9}, a642[] = {0.26, 0.335},
                       b642[] = {2.5, 3.6}, a644[] = {0.19}, b644[] = {3.6}, a128[] = {0.575, 0.725}, b128[] = {2.6, 5.6},
                       a1282[] = {0.46}, b1282[] = {5.7};
   if (tile == 64 && groups == 1) by_line(a64, b64, 4), us += 2.6;
