@@ -36,22 +36,6 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// GELU x Phi(x) for outputs that are rounded to bf16: Phi(-|x|) = t 2^(P(t) - x^2 / (2 ln 2)), t = 1 /
-// (1 + |x| / 5), P the polynomial of degree 5 that fits log2(Phi(-a) / t) + a^2 / (2 ln 2) over 0 <= a <= 14
-// best in the largest error (8.5e-6 of Phi).  With fp32 rounding GELU's relative error stays below 2e-5 (a bf16
-// rounding: 2e-3), in the tail too.  Four terms fewer than gelu_erf: 4608x3072x9216 with GELU 145 -> 142 us.
-__device__ __forceinline__ float gelu5(float x) {
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.2f, fabsf(x), 1.0f));
-  float p = -0.843770526f;
-  p = fmaf(p, t, 1.98156184f);
-  p = fmaf(p, t, -1.07346919f);
-  p = fmaf(p, t, 1.25041619f);
-  p = fmaf(p, t, 1.32332888f);
-  p = fmaf(p, t, -3.63807946f);
-  const float h = t * __builtin_amdgcn_exp2f(fmaf(x * x, -0.721347520f, p));
-  return x * (x >= 0.0f ? 1.0f - h : h);
-}
-
 struct Out {
   const float *sX, *sW, *bias;
   void* Y;

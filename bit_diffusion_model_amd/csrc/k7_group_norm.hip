@@ -9,10 +9,9 @@
 // 151 us, 5.3 TB/s), by the cache below that (65536x256 bf16 29.3 us), by launches and the
 // blocks' meeting in the smallest.  Three kernels:
 //  * k7_one: a block holds one image's group in registers: x read once, mean and variance by
-//    two exact passes over the registers, one launch.  Taken where a group has at most 32768
-//    values, 32 per thread of 1024 (us, against the two launches below: 2x64x1280 in groups of
-//    40 3.8 against 10.5, 2x2048x512 of 16 8.5 against 13.0; 1x4096x320 of 10, 40960 values: 13.2
-//    against 12.3; with 64 values per thread 26);
+//    two exact passes over the registers, one launch.  Taken where a group's values fit the
+//    registers of 1024 threads in few loads (the plan below holds the figures: 2x64x1280 in
+//    groups of 40 3.8 us against the two launches' 10.5);
 //  * k7_stats, then k7_apply (or k7_apply_quant): statistics per block of positions, and the
 //    output pass, which first joins the blocks' statistics (by itself where there are few,
 //    after k7_join where there are many: an output block would read them all).  A thread keeps
@@ -120,8 +119,8 @@ __device__ __forceinline__ void storev(TY* p, const float v[V]) {
 }
 
 // The activation of N values (one branch for all): SiLU y / (1 + exp(-y)), exp as a power of 2 (a large
-// negative y gives y times 1 / inf = -0); GELU in its exact form.
-template <int N>
+// negative y gives y times 1 / inf = -0); GELU in its exact form, for FP32 outputs by the longer fit.
+template <bool FP32, int N>
 __device__ __forceinline__ void norm_act(float (&y)[N], int act) {
   if (act == SVDQ_GN_SILU) {
 #pragma unroll
@@ -129,7 +128,7 @@ __device__ __forceinline__ void norm_act(float (&y)[N], int act) {
       y[e] *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y[e] * -1.44269504088896341f));
   } else if (act == SVDQ_GN_GELU) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) y[e] = gelu_erf(y[e]);
+    for (int e = 0; e < N; ++e) y[e] = FP32 ? gelu_erf(y[e]) : gelu5(y[e]);
   }
 }
 
@@ -208,7 +207,7 @@ __global__ __launch_bounds__(1024) void k7_one(const T* __restrict__ X, int64_t 
       valuev<T, V>(raw[j], v);
 #pragma unroll
       for (int e = 0; e < V; ++e) v[e] = fmaf(v[e] - mean, rstd * lds[q * V + e], lds[cpg + q * V + e]);
-      norm_act(v, act);
+      norm_act<sizeof(TY) == 4>(v, act);
       storev<TY, V>(y + r * ldy + q * V, v);
     }
     q += dc, r += dr;
@@ -490,7 +489,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply(const T* __restrict__ X, int64
         valuev<T, V>(raw[u], v);
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = fmaf(v[e] - mean[e], a[e], b[e]);
-        norm_act(v, act);
+        norm_act<sizeof(TY) == 4>(v, act);
         storev<TY, V, NT>(to, v);
       }
     }
@@ -561,7 +560,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        norm_act(v[u][j], act);
+        norm_act<false>(v[u][j], act);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           v[u][j][e] *= f[e];
@@ -645,7 +644,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant_narrow(const T* __restri
       uint32_t top = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = fmaf(on ? v[e] - mean[e] : 0.0f, a[e], b[e]);  // off: a = b = f = 0
-      norm_act(v, act);
+      norm_act<false>(v, act);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         v[e] *= f[e];
@@ -686,8 +685,10 @@ void launch_one_nv(const NormArgs& a, void* Y, int64_t bsy, int64_t ldy, float2*
 template <typename T, typename TY, int V>
 void launch_one_v(const NormArgs& a, void* Y, int64_t bsy, int64_t ldy, float2* stat, hipStream_t st) {
   // 8 values per thread where 1024 threads then hold the group, otherwise 32
-  if (a.S * (a.C / a.G) <= 8 * 1024) launch_one_nv<T, TY, V, 8 / V>(a, Y, bsy, ldy, stat, st);
-  else launch_one_nv<T, TY, V, 32 / V>(a, Y, bsy, ldy, stat, st);
+  if constexpr (V > 1) {  // one value per load: never more than 8 loads
+    if (a.S * (a.C / a.G) > 8 * 1024) return launch_one_nv<T, TY, V, 32 / V>(a, Y, bsy, ldy, stat, st);
+  }
+  launch_one_nv<T, TY, V, 8 / V>(a, Y, bsy, ldy, stat, st);
 }
 template <typename T, typename TY>
 void launch_one(const NormArgs& a, int width, void* Y, int64_t bsy, int64_t ldy, float2* stat, hipStream_t st) {
@@ -747,7 +748,11 @@ Stats run_stats(const NormArgs& a, const NormPlan& p, void* ws, hipStream_t st) 
 NormPlan plan_norm(int64_t B, int64_t S, int C, int G) {
   NormPlan p{};
   const int64_t cpg = C / G;
-  p.one = S * cpg <= 32 * 1024;
+  // Measured (us, one launch / two): groups of 16 over 2048 positions 8.5 / 13.0, of 8 over 4096 10.1 / 12.2, of 10 over
+  // 1024 7.8 / 11.9, over 2000 14.1 / 13.4, of 3 over 2700 9.8 / 11.5, over 5000 16.8 / 12.1, of 4 over 8000 21.7 / 13.1, of
+  // 1 over 8000 10.6 / 11.2, of 35 over 300 10.1 / 10.7, over 794 16.6 / 14.6: what counts are the loads, at most 8 per
+  // thread of 1024, and the rows that they touch.
+  p.one = S * cpg <= 32 * 1024 && S * (cpg / one_width((int)cpg)) <= 8 * 1024 && S <= 4096;
   // Measured (us, both launches or all three; statistics blocks / output blocks):
   //   2x4096x320 bf16 256 / 256 14.9, 256 / 512 15.9, 256 joined apart / 256 16.5, 256 / 1024 20.8
   //   1x16384x128 bf16 128 / 256 13.9, 256 / 256 16.5, 256 joined apart / 256 15.8
