@@ -79,7 +79,7 @@ struct Row<uint16_t, false> {
   }
 };
 
-// GELU x Phi(x) for outputs that are rounded to bf16 or to codes: Phi(-|x|) = t 2^(P(t) - x^2 / (2 ln 2)), t = 1 /
+// GELU x Phi(x) for outputs that are rounded to bf16: Phi(-|x|) = t 2^(P(t) - x^2 / (2 ln 2)), t = 1 /
 // (1 + |x| / 5), P the polynomial of degree 5 that fits log2(Phi(-a) / t) + a^2 / (2 ln 2) over 0 <= a <= 14
 // best in the largest error (8.5e-6 of Phi).  With fp32 rounding GELU's relative error stays below 2e-5 (a bf16
 // rounding: 2e-3), in the tail too.  Four terms fewer than gelu_erf: the product 4608x3072x9216

@@ -122,9 +122,10 @@ __device__ __forceinline__ void load_channels(const Out& o, int64_t n, float sw[
 // it then shares.
 // P > 1 parts: blockIdx.y takes a range of the stages and stores raw sums to part[y].
 //
-// What bounds it: tiles of 256 the card's power (the MFMA units are busy 80% of the time at a
-// clock of 1.9 GHz: 4608x12288x3072 in 140 us, 2.5 POP/s on one set of operands; 97 us with
-// the loads left out); products with few stages the epilogue and the outputs' way to memory
+// What bounds it: tiles of 256 with the operands in cache the card's power (4608x12288x3072 in
+// 140 us, 2.5 POP/s; MFMAs alone 97); out of cache the operands' way: 173 us, the MFMA units of a
+// busy CU occupied 53% of the time, a stage being fetched one stage, about 1 us, ahead (LDS has
+// no room for a third buffer).  Products with few stages: fetch, epilogue and stores in turn
 // (16384x320x1280: 20.7 us, of which 42 MB of stores 5).  Blocks that stay and take tile after
 // tile, with loads running ahead over the tiles' ends, were no faster there (23.5 us against
 // 23.3) and slower in long products (144 against 128): the registers they need crowd the loop.
@@ -342,6 +343,7 @@ __device__ __forceinline__ void tile(const int8_t* __restrict__ qX, int64_t ld, 
   };
   if (rows == BM && cols == BN) finish(std::true_type{});
   else finish(std::false_type{});
+  wait_vm_lgkm0<0>();  // no load into LDS outlives the block, not the last ones without a range either
 }
 
 // Tile t of tiles_m x tiles_n in strips of 8 tile rows

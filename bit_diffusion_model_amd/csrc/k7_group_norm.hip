@@ -119,8 +119,9 @@ __device__ __forceinline__ void storev(TY* p, const float v[V]) {
 }
 
 // The activation of N values (one branch for all): SiLU y / (1 + exp(-y)), exp as a power of 2 (a large
-// negative y gives y times 1 / inf = -0); GELU in its exact form, for FP32 outputs by the longer fit.
-template <bool FP32, int N>
+// negative y gives y times 1 / inf = -0); GELU in its exact form, for FINE outputs by the longer fit: fp32, and codes,
+// where the shorter one's 8.5e-6 would move one rounding in a thousand.
+template <bool FINE, int N>
 __device__ __forceinline__ void norm_act(float (&y)[N], int act) {
   if (act == SVDQ_GN_SILU) {
 #pragma unroll
@@ -128,7 +129,7 @@ __device__ __forceinline__ void norm_act(float (&y)[N], int act) {
       y[e] *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y[e] * -1.44269504088896341f));
   } else if (act == SVDQ_GN_GELU) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) y[e] = FP32 ? gelu_erf(y[e]) : gelu5(y[e]);
+    for (int e = 0; e < N; ++e) y[e] = FINE ? gelu_erf(y[e]) : gelu5(y[e]);
   }
 }
 
@@ -560,7 +561,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X,
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        norm_act<false>(v[u][j], act);
+        norm_act<true>(v[u][j], act);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           v[u][j][e] *= f[e];
@@ -644,7 +645,7 @@ __global__ __launch_bounds__(AP_NT) void k7_apply_quant_narrow(const T* __restri
       uint32_t top = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = fmaf(on ? v[e] - mean[e] : 0.0f, a[e], b[e]);  // off: a = b = f = 0
-      norm_act<false>(v, act);
+      norm_act<true>(v, act);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         v[e] *= f[e];
