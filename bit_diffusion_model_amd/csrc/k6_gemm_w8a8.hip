@@ -609,8 +609,9 @@ void launch_tiles(const W8A8Plan& p, int64_t ld, const int8_t* qX, const int8_t*
 //   128     two blocks to a CU: 512x3072x9216 22.5 (64 x 2: 29), 2048x12288x3072 74.7 (64 x 2: 110), 8192x640x640 9.8 (64: 10.5)
 //   128 x 2 two K groups (tiles <= CUs): 1024x12288x3072 55.3 (one group 69.5), 256x3072x9216 17.5 (one group 19.6)
 //   256     1024x3072x9216 35.3 (128: 42), 4608x12288x3072 121-140 (128: 151), 8192x3072x9216 181 (210); 2048x3072x9216 70.6
-//           (63.2); a last round for at most half of the CUs runs as tiles of 128 x 256: 9216x3072x9216 269 (whole tiles
-//           278), 2304x3072x9216 79 (84), with GELU 88 (101), 16384x320x2560 35 (39)
+//           (63.2); a last round for at most half of the CUs runs as tiles of 128 x 256: 9216x3072x9216 275 (whole
+//           tiles 285), 2304x3072x9216 77 (82), with GELU 81 (90), 8192x4096x8448 280 (302), 16384x320x2560 35 (39),
+//           4608x3072x12288 with GELU 201 (203)
 // K parts (tiles of 64 with four groups, S / parts >= 8, all parts on the CUs at once) add the
 // partial sums' traffic and a launch, 6 + 12 bytes x M N parts / 6 TB/s: 64x12288x3072 15.6 in 4 parts, 26.3 in one.
 

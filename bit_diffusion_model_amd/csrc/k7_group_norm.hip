@@ -755,10 +755,10 @@ NormPlan plan_norm(int64_t B, int64_t S, int C, int G) {
   // thread of 1024, and the rows that they touch.
   p.one = S * cpg <= 32 * 1024 && S * (cpg / one_width((int)cpg)) <= 8 * 1024 && S <= 4096;
   // Measured (us, both launches or all three; statistics blocks / output blocks):
-  //   2x4096x320 bf16 256 / 256 14.9, 256 / 512 15.9, 256 joined apart / 256 16.5, 256 / 1024 20.8
-  //   1x16384x128 bf16 128 / 256 13.9, 256 / 256 16.5, 256 joined apart / 256 15.8
-  //   1x65536x256 bf16 512 joined apart / 768 31.1, 512 / 2048 38.2, 256 / 512 joined inside 35.2
-  //   1x262144x128 bf16 512 joined apart / 768 45.6, 256 / 512 joined inside 50.8
+  //   2x4096x320 bf16 256 / 256 13.4, 256 / 512 15.0, 256 joined apart / 256 14.9, 256 / 1024 17.2
+  //   1x16384x128 bf16 128 / 256 13.2, 256 / 256 15.3, 256 joined apart / 256 14.7
+  //   1x65536x256 bf16 512 joined apart / 768 28.6, 512 / 2048 35.7, 256 / 512 joined inside 30.9
+  //   1x262144x128 bf16 512 joined apart / 768 42.8, 256 / 512 joined inside 44.4
   // so up to 2^23 values one block of each kind per CU, the output blocks joining at most 128 parts
   // per image; above, a join of its own.
   const int64_t n = B * S * C;
