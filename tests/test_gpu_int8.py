@@ -179,7 +179,7 @@ def at_any_value(shape, stride, dtype, fill, device="cuda:0"):
 
 
 @pytest.mark.parametrize("M,K,N,pad", [(1, 129, 131, 0), (4, 322, 64, 1), (70, 128, 131, 3), (300, 320, 77, 1), (90, 4609, 261, 2),
-                                       (33, 2057, 40, 0), (2, 16389, 24, 1), (4096, 301, 2051, 0), (2304, 64, 1030, 1)])
+                                       (33, 2057, 40, 0), (40, 8192, 51, 2), (2, 16389, 24, 1), (4096, 301, 2051, 0), (2304, 64, 1030, 1)])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("yd", ["f32", "bf16", "gelu"])
 def test_rows_at_any_value(M, K, N, pad, dt, yd):
