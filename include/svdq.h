@@ -448,8 +448,8 @@ svdq_status svdq_mlp_chain_reduce(const svdq_layer* fc1, const svdq_layer* fc2, 
  *             integers, the rest in fp32, then GELU if asked, rounded once to Y's type.
  * Rows of codes, of activations and weights alike, are svdq_int8_ld(K) = K rounded up to 128
  * bytes long; the bytes past K are zero.  X is fp32 or bf16 (svdq_dtype SVDQ_F32 /
- * SVDQ_BF16) of any K >= 1 and any row stride ldx >= K; rows that are 16-byte aligned are
- * read by wide loads.  Limits: K <= 131072 (the integer sums stay below 2^31), M, N, ldx and
+ * SVDQ_BF16) of any K >= 1 and any row stride ldx >= K; rows of X and Y may begin at any
+ * element's address.  Limits: K <= 131072 (the integer sums stay below 2^31), M, N, ldx and
  * ldy below 2^31, M N below 2^43 (EUNSUPPORTED beyond). */
 typedef struct svdq_int8_layer {
   int64_t K, N;
