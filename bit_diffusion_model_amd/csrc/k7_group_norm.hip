@@ -9,7 +9,7 @@
 // 151 us, 5.3 TB/s), by the cache below that (65536x256 bf16 29.3 us), by launches and the
 // blocks' meeting in the smallest.  Three kernels:
 //  * k7_one: a block holds one image's group in registers: x read once, mean and variance by
-//    two exact passes over the registers, one launch.  Taken where a group's values fit the
+//    two passes over the registers, one launch.  Taken where a group's values fit the
 //    registers of 1024 threads in few loads (the plan below holds the figures: 2x64x1280 in
 //    groups of 40 3.8 us against the two launches' 10.5);
 //  * k7_stats, then k7_apply (or k7_apply_quant): statistics per block of positions, and the
@@ -146,7 +146,21 @@ __device__ __forceinline__ float block_sum(float v, float* scratch) {
   for (int i = 0; i < waves; ++i) s += scratch[i];
   return s;
 }
+__device__ __forceinline__ float2 block_sum(float2 v, float2* scratch) {
+  const int waves = (int)((blockDim.x + 63) >> 6);
+  v = make_float2(wave_sum(v.x), wave_sum(v.y));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float2 s = make_float2(0.0f, 0.0f);
+  for (int i = 0; i < waves; ++i) s.x += scratch[i].x, s.y += scratch[i].y;
+  return s;
+}
 
+// The sum of the values over n is a first mean p only, off by the roundings of a sum (a constant group: two bits of
+// 3000.7, which eps = 1e-5 would show as 0.15); the second pass takes d = x - p, which is small or exact, and gives
+// mean = p + sum d / n, M2 = sum d^2 - (sum d)^2 / n.
+//
 // NV vectors of V channels per thread.  stat != NULL: the statistics alone, (mean, rstd) to stat[b][g].
 template <typename T, typename TY, int V, int NV>
 __global__ __launch_bounds__(1024) void k7_one(const T* __restrict__ X, int64_t bsx, int64_t ldx, int S, int C, int G,
@@ -154,7 +168,7 @@ __global__ __launch_bounds__(1024) void k7_one(const T* __restrict__ X, int64_t 
                                                const float* __restrict__ beta, int act, TY* __restrict__ Y, int64_t bsy,
                                                int64_t ldy, float2* __restrict__ stat) {
   extern __shared__ float lds[];  // gamma, beta of the group
-  __shared__ float scratch[16];
+  __shared__ float2 scratch[16];
   const int cpg = C / G, c0 = (int)blockIdx.x * cpg, vpr = cpg / V, total = S * vpr;
   const T* x = X + blockIdx.y * bsx + c0;
   // the thread's vectors t, t + threads, ..: (row, col) advance by the quotient and the rest
@@ -184,17 +198,24 @@ __global__ __launch_bounds__(1024) void k7_one(const T* __restrict__ X, int64_t 
     s += (int)threadIdx.x + j * nt < total ? t : 0.0f;
   }
   const float n = (float)S * (float)cpg;
-  const float mean = block_sum(s, scratch) / n;
-  s = 0.0f;
+  const float p = block_sum(s, &scratch[0].x) / n;
+  float2 sums = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    float v[V], t = 0.0f;
+    float v[V];
+    float2 t = make_float2(0.0f, 0.0f);
     valuev<T, V>(raw[j], v);
 #pragma unroll
-    for (int e = 0; e < V; ++e) t += (v[e] - mean) * (v[e] - mean);
-    s += (int)threadIdx.x + j * nt < total ? t : 0.0f;
+    for (int e = 0; e < V; ++e) {
+      const float d = v[e] - p;
+      t.x += d;
+      t.y = fmaf(d, d, t.y);
+    }
+    if ((int)threadIdx.x + j * nt < total) sums.x += t.x, sums.y += t.y;
   }
-  const float rstd = 1.0f / sqrtf(block_sum(s, scratch) / n + eps);
+  sums = block_sum(sums, scratch);
+  const float mean = p + sums.x / n, m2 = sums.y - sums.x * (sums.x / n);
+  const float rstd = 1.0f / sqrtf((m2 < 0.0f ? 0.0f : m2) / n + eps);  // (a NaN passes)
   if (stat) {
     if (threadIdx.x == 0) stat[(int64_t)blockIdx.y * G + blockIdx.x] = make_float2(mean, rstd);
     return;

@@ -1,0 +1,51 @@
+"""GPU tests of the group norm on each of its paths: one launch (no workspace), statistics and output in two launches,
+and three launches (the blocks' statistics joined by a launch of their own, above 2^23 values)."""
+import numpy as np
+import pytest
+
+from bit_diffusion_model_amd import svdq
+from test_gpu_int8 import host
+
+pytestmark = pytest.mark.gpu
+
+
+def _torch():
+    import torch
+
+    return torch
+
+
+# (B, S, groups, C, whether one launch serves it): vectors of 8, 4, 2 and 1 channels, groups of 1 to 40 channels
+CONSTANT = [(2, 1024, 32, 640, True), (1, 2048, 4, 64, True), (2, 64, 32, 1280, True), (1, 1000, 5, 15, True), (1, 700, 7, 42, True),
+            (1, 1, 4, 64, True), (2, 6000, 8, 64, False), (1, 9001, 3, 9, False), (1, 70001, 4, 128, False)]
+
+
+@pytest.mark.parametrize("B,S,G,C,one", CONSTANT)
+@pytest.mark.parametrize("value", [0.1, 100.1, 1000.1, 3000.7, -33333.3])
+def test_constant_group_gives_beta(B, S, G, C, one, value):
+    """A group of one value: its mean is that value and x - mean is 0, whatever the value, so y is beta to the bit.
+    (Sums of such values are not exact in fp32: a mean that is off by one bit of 3000.7 moves y by 0.08 at eps = 1e-5.)
+    The other groups hold normals around the value."""
+    torch = _torch()
+    rng = np.random.default_rng(S + C)
+    x = (rng.standard_normal((B, S, C)) + value).astype(np.float32)
+    cpg = C // G
+    x[:, :, :cpg] = np.float32(value)
+    x[B - 1, :, C - cpg:] = np.float32(value)
+    X = torch.from_numpy(x).to("cuda:0")
+    beta = (0.3 * rng.standard_normal(C)).astype(np.float32)
+    gn = svdq.GroupNorm(G, C, (1 + 0.3 * rng.standard_normal(C)).astype(np.float32), beta)
+    assert (gn.workspace(B, S, X.device) is None) == one
+    Y = host(gn.forward(X, svdq.F32))
+    want = beta.astype(np.float64)
+    assert np.array_equal(Y[:, :, :cpg], np.broadcast_to(want[:cpg], (B, S, cpg)))
+    assert np.array_equal(Y[B - 1, :, C - cpg:], np.broadcast_to(want[C - cpg:], (S, cpg)))
+
+
+@pytest.mark.parametrize("B,S,C", [(2, 1024, 640), (2, 64, 1280), (1, 2000, 24), (1, 9001, 64)])
+def test_constant_image_gives_zero_codes(B, S, C):
+    """Without gamma and beta an image of one value is 0 everywhere: codes 0 and the smallest scale."""
+    torch = _torch()
+    X = torch.full((B, S, C), 3000.7, device="cuda:0")
+    q, s = svdq.GroupNorm(8, C).quantize(X)
+    assert not q.any() and torch.equal(s, torch.full_like(s, float(np.float32(2.0 ** -96) / np.float32(127))))
