@@ -604,9 +604,49 @@ def _dev_tensor(t, name: str, dtype, device, n=None):
     return t
 
 
-def _on_current_device(torch, t):
-    if t.get_device() != torch.cuda.current_device():
+def _on_current_device(torch, t) -> int:
+    """t's device, which has to be the current one (a tensor in host memory has none)."""
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
         raise SvdqError(f"the tensor is on {t.device}, the current HIP device is {torch.cuda.current_device()}")
+    return dev
+
+
+def _on(t, dev: int, name: str):
+    if t.get_device() != dev:
+        raise SvdqError(f"{name} is on {t.device}, the input on cuda:{dev}")
+
+
+def _one_device(tensors, what: str) -> int:
+    """The device that all of the tensors given are on; -1 where there is none."""
+    devs = {t.get_device() for t in tensors if t is not None}
+    if len(devs) > 1:
+        raise SvdqError(f"the {what}'s tensors must be on one device")
+    return devs.pop() if devs else -1
+
+
+def _scratch(ws, dev: int):
+    """(address, bytes) of a workspace tensor, or of none."""
+    if ws is None:
+        return None, 0
+    _on(ws, dev, "the workspace")
+    if not ws.is_contiguous():
+        raise SvdqError("the workspace must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _codes_out(torch, out, M: int, K: int, X, dev: int):
+    """The quantizers' two outputs, made, or the caller's checked: the library takes no sizes for them."""
+    ld = int8_ld(K)
+    if out is None:
+        return (torch.empty((M, ld), dtype=torch.int8, device=X.device), torch.empty(M, dtype=torch.float32, device=X.device))
+    q, s = out
+    if q.shape != (M, ld) or q.dtype != torch.int8 or not q.is_contiguous() or s.shape != (M,) or \
+            s.dtype != torch.float32 or not s.is_contiguous():
+        raise SvdqError(f"out must be contiguous int8 [{M}][{ld}] and contiguous fp32 [{M}]")
+    _on(q, dev, "out[0]")
+    _on(s, dev, "out[1]")
+    return out
 
 
 class Int8Linear:
@@ -629,6 +669,7 @@ class Int8Linear:
         self.inv_s = _dev_tensor(inv_s, "inv_s", torch.float32, device, self.K)
         self.bias = _dev_tensor(bias, "bias", torch.float32, device, self.N)
         self.device = self.qW.device
+        self._dev = _one_device((self.qW, self.sW, self.inv_s, self.bias), "layer")
         self._c = _Int8Layer(self.K, self.N, _dptr(self.inv_s), _dptr(self.qW), _dptr(self.sW), _dptr(self.bias))
         self._ref = ctypes.addressof(self._c)
 
@@ -645,26 +686,28 @@ class Int8Linear:
 
     def _out(self, M, ydtype, out, X):
         torch, _, ty, L = _rt()
-        _on_current_device(torch, X)
+        if _on_current_device(torch, X) != self._dev:
+            raise SvdqError(f"the layer is on cuda:{self._dev}, the input on {X.device}")
         if out is None:
             return torch.empty((M, self.N), dtype=ty[ydtype], device=X.device)
-        if out.shape != (M, self.N) or out.dtype != ty[ydtype] or out.stride(1) != 1 or not out.is_cuda:
+        if out.shape != (M, self.N) or out.dtype != ty[ydtype] or out.stride(1) != 1:
             raise SvdqError(f"out must be a [{M}][{self.N}] {ty[ydtype]} device tensor with unit column stride")
+        _on(out, self._dev, "out")
         return out
 
     def gemm(self, qX, sX, ydtype: int = F32, out=None, workspace=None):
         """svdq_gemm_w8a8: Y [M][N] from codes qX int8 [M][int8_ld(K)] and their scales sX fp32 [M]."""
         torch, _, _, L = _rt()
-        M = qX.shape[0]
-        if qX.dtype != torch.int8 or sX.dtype != torch.float32 or qX.shape[1] != int8_ld(self.K) or sX.numel() != M or \
-                not qX.is_contiguous() or not sX.is_contiguous():
+        if qX.dim() != 2 or qX.dtype != torch.int8 or sX.dtype != torch.float32 or qX.shape[1] != int8_ld(self.K) or \
+                sX.numel() != qX.shape[0] or not qX.is_contiguous() or not sX.is_contiguous():
             raise SvdqError(f"qX must be contiguous int8 [M][{int8_ld(self.K)}] and sX contiguous fp32 [M]")
+        M = qX.shape[0]
         out = self._out(M, ydtype, out, qX)
+        _on(sX, self._dev, "sX")
         n = L.svdq_gemm_w8a8_workspace_bytes(self._ref, M)
         ws = workspace if workspace is not None or n == 0 else torch.empty(n, dtype=torch.uint8, device=qX.device)
         _check(L.svdq_gemm_w8a8(self._ref, M, qX.data_ptr(), sX.data_ptr(), out.data_ptr(),
-                                _ld(M, out.stride(0), self.N), ydtype, None if ws is None else ws.data_ptr(),
-                                0 if ws is None else ws.numel(), _raw_stream(qX)))
+                                _ld(M, out.stride(0), self.N), ydtype, *_scratch(ws, self._dev), _raw_stream(qX)))
         return out
 
     def workspace(self, M: int, xdtype: int = BF16):
@@ -681,8 +724,8 @@ class Int8Linear:
         xd = xt[X.dtype]
         ws = workspace if workspace is not None else self.workspace(M, xd)
         _check(L.svdq_linear_forward_int8(self._ref, M, X.data_ptr(), xd, _ld(M, X.stride(0), self.K), out.data_ptr(),
-                                          _ld(M, out.stride(0), self.N), ydtype, None if ws is None else ws.data_ptr(),
-                                          0 if ws is None else ws.numel(), _raw_stream(X)))
+                                          _ld(M, out.stride(0), self.N), ydtype, *_scratch(ws, self._dev),
+                                          _raw_stream(X)))
         return out
 
 
@@ -704,13 +747,13 @@ def _raw_stream(t) -> int:
 def quantize_act_int8(X, inv_s=None, out=None):
     """svdq_quantize_act_int8: (qX int8 [M][int8_ld(K)], sX fp32 [M]) of X [M][K] times inv_s."""
     torch, xt, _, L = _rt()
-    K = X.shape[-1]
+    K = X.shape[-1] if X.dim() else 0
     M = _check_rows(X, K, xt)
-    _on_current_device(torch, X)
+    dev = _on_current_device(torch, X)
     inv_s = _dev_tensor(inv_s, "inv_s", torch.float32, X.device, K)
-    if out is None:
-        out = (torch.empty((M, int8_ld(K)), dtype=torch.int8, device=X.device),
-               torch.empty(M, dtype=torch.float32, device=X.device))
+    if inv_s is not None:
+        _on(inv_s, dev, "inv_s")
+    out = _codes_out(torch, out, M, K, X, dev)
     _check(L.svdq_quantize_act_int8(M, K, X.data_ptr(), xt[X.dtype], _ld(M, X.stride(0), K),
                                     None if inv_s is None else inv_s.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
                                     _raw_stream(X)))
@@ -727,8 +770,14 @@ class GroupNorm:
         self.C, self.groups, self.eps, self.act = int(C), int(groups), float(eps), int(act)
         self.gamma = _dev_tensor(gamma, "gamma", torch.float32, device, self.C)
         self.beta = _dev_tensor(beta, "beta", torch.float32, device, self.C)
+        self._dev = _one_device((self.gamma, self.beta), "norm")
         self._c = _GroupNorm(self.C, self.groups, self.act, self.eps, _dptr(self.gamma), _dptr(self.beta))
         self._ref = ctypes.addressof(self._c)
+
+    def _same(self, dev: int) -> int:
+        if self._dev not in (-1, dev):
+            raise SvdqError(f"the norm's gamma and beta are on cuda:{self._dev}, the input on cuda:{dev}")
+        return dev
 
     def _geometry(self, X, what="X"):
         """(B, S, bs, ld): images, positions, image and position stride of X."""
@@ -754,36 +803,35 @@ class GroupNorm:
         """svdq_group_norm: act(norm(X)) in X's shape, fp32 or bf16."""
         torch, xt, ty, L = _rt()
         B, S, bs, ld = self._geometry(X)
-        _on_current_device(torch, X)
+        dev = self._same(_on_current_device(torch, X))
         if ydtype not in (F32, BF16):
             raise SvdqError("the norm's output is F32 or BF16")
         if out is None:
             out = torch.empty(X.shape, dtype=ty[ydtype], device=X.device)
             bsy, ldy = S * self.C, self.C
-        elif out.shape != X.shape or out.dtype != ty[ydtype] or not out.is_cuda:
+        elif out.shape != X.shape or out.dtype != ty[ydtype]:
             raise SvdqError(f"out must be a {tuple(X.shape)} {ty[ydtype]} device tensor")
         else:
+            _on(out, dev, "out")
             _, _, bsy, ldy = self._geometry(out, "out")
         ws = workspace if workspace is not None else self.workspace(B, S, X.device)
         _check(L.svdq_group_norm(self._ref, B, S, X.data_ptr(), xt[X.dtype], bs, ld, out.data_ptr(),
-                                 ydtype, bsy, ldy, None if ws is None else ws.data_ptr(),
-                                 0 if ws is None else ws.numel(), _raw_stream(X)))
+                                 ydtype, bsy, ldy, *_scratch(ws, dev), _raw_stream(X)))
         return out
 
     def quantize(self, X, inv_s=None, out=None, workspace=None):
         """svdq_group_norm_quantize_int8: (qX int8 [B S][int8_ld(C)], sX fp32 [B S]) of act(norm(X)) inv_s."""
         torch, xt, _, L = _rt()
         B, S, bs, ld = self._geometry(X)
-        _on_current_device(torch, X)
+        dev = self._same(_on_current_device(torch, X))
         inv_s = _dev_tensor(inv_s, "inv_s", torch.float32, X.device, self.C)
-        if out is None:
-            out = (torch.empty((B * S, int8_ld(self.C)), dtype=torch.int8, device=X.device),
-                   torch.empty(B * S, dtype=torch.float32, device=X.device))
+        if inv_s is not None:
+            _on(inv_s, dev, "inv_s")
+        out = _codes_out(torch, out, B * S, self.C, X, dev)
         ws = workspace if workspace is not None else self.workspace(B, S, X.device, True)
         _check(L.svdq_group_norm_quantize_int8(self._ref, B, S, X.data_ptr(), xt[X.dtype], bs, ld,
                                                None if inv_s is None else inv_s.data_ptr(), out[0].data_ptr(),
-                                               out[1].data_ptr(), None if ws is None else ws.data_ptr(),
-                                               0 if ws is None else ws.numel(), _raw_stream(X)))
+                                               out[1].data_ptr(), *_scratch(ws, dev), _raw_stream(X)))
         return out
 
     def forward_linear(self, X, layer: Int8Linear, ydtype: int = BF16, out=None, workspace=None):
@@ -791,11 +839,12 @@ class GroupNorm:
         torch, xt, _, L = _rt()
         B, S, bs, ld = self._geometry(X)
         out = layer._out(B * S, ydtype, out, X)
+        dev = self._same(layer._dev)
         ws = workspace
         if ws is None:
             n = L.svdq_norm_linear_int8_workspace_bytes(self._ref, layer._ref, B, S)
             ws = torch.empty(max(n, 256), dtype=torch.uint8, device=X.device)
         _check(L.svdq_norm_linear_forward_int8(self._ref, layer._ref, B, S, X.data_ptr(), xt[X.dtype], bs, ld,
                                                out.data_ptr(), _ld(B * S, out.stride(0), layer.N), ydtype,
-                                               ws.data_ptr(), ws.numel(), _raw_stream(X)))
+                                               *_scratch(ws, dev), _raw_stream(X)))
         return out
