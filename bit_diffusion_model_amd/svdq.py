@@ -559,10 +559,14 @@ def int8_ld(K: int) -> int:
 def pack_weights_int8(W_bits: np.ndarray, act_absmax_: Optional[np.ndarray] = None, alpha: float = 0.5):
     """svdq_pack_weights_int8 on W (bf16 bits [K][N]): (s, inv_s, qW int8 [N][int8_ld(K)], sW fp32 [N])."""
     W = np.ascontiguousarray(W_bits, dtype=np.uint16)
+    if W.ndim != 2:
+        raise SvdqError("W must be [K][N]")
     K, N = W.shape
     s, inv = np.empty(K, np.float32), np.empty(K, np.float32)
     qW, sW = np.empty((N, int8_ld(K)), np.int8), np.empty(N, np.float32)
     a = None if act_absmax_ is None else np.ascontiguousarray(act_absmax_, dtype=np.float32)
+    if a is not None and a.shape != (K,):
+        raise SvdqError(f"act_absmax must be [{K}]")
     _check(lib().svdq_pack_weights_int8(K, N, _ptr(W), _ptr(a), float(alpha), _ptr(s), _ptr(inv), _ptr(qW), _ptr(sW)))
     return s, inv, qW, sW
 
@@ -570,6 +574,8 @@ def pack_weights_int8(W_bits: np.ndarray, act_absmax_: Optional[np.ndarray] = No
 def prepare_weights_int8(K: int, qW: np.ndarray) -> np.ndarray:
     """svdq_prepare_weights_int8: codes [N][int8_ld(K)] in the kernel layout (flat, N rounded up to 16)."""
     qW = np.ascontiguousarray(qW, dtype=np.int8)
+    if qW.ndim != 2 or qW.shape[1] != int8_ld(K):
+        raise SvdqError(f"qW must be [N][{int8_ld(K)}]")
     out = np.empty(lib().svdq_int8_weight_bytes(K, qW.shape[0]), np.int8)
     _check(lib().svdq_prepare_weights_int8(K, qW.shape[0], _ptr(qW), _ptr(out)))
     return out
