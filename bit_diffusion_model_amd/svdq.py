@@ -565,8 +565,8 @@ def pack_weights_int8(W_bits: np.ndarray, act_absmax_: Optional[np.ndarray] = No
     s, inv = np.empty(K, np.float32), np.empty(K, np.float32)
     qW, sW = np.empty((N, int8_ld(K)), np.int8), np.empty(N, np.float32)
     a = None if act_absmax_ is None else np.ascontiguousarray(act_absmax_, dtype=np.float32)
-    if a is not None and a.shape != (K,):
-        raise SvdqError(f"act_absmax must be [{K}]")
+    if a is not None and a.size != K:
+        raise SvdqError(f"act_absmax must hold {K} values")
     _check(lib().svdq_pack_weights_int8(K, N, _ptr(W), _ptr(a), float(alpha), _ptr(s), _ptr(inv), _ptr(qW), _ptr(sW)))
     return s, inv, qW, sW
 

@@ -12,8 +12,9 @@ def test_pack_needs_one_statistic_per_input_channel(n):
     with pytest.raises(svdq.SvdqError, match="act_absmax"):
         svdq.pack_weights_int8(W, np.ones(n, np.float32))
     with pytest.raises(svdq.SvdqError, match="act_absmax"):
-        svdq.pack_weights_int8(W, np.ones((100, n), np.float32))
-    assert svdq.pack_weights_int8(W, np.ones(100, np.float32))[0].shape == (100,)
+        svdq.pack_weights_int8(W, np.ones((2, n), np.float32))
+    for shape in ((100,), (1, 100), (100, 1)):  # a statistic that kept its reduced dimension
+        assert svdq.pack_weights_int8(W, np.ones(shape, np.float32))[0].shape == (100,)
 
 
 def test_pack_needs_a_matrix():
