@@ -145,12 +145,16 @@ __device__ __forceinline__ void row_scale(uint32_t abits, float& s, float& r) {
 
 // Four codes round_half_even(v r) in [-127, 127] as the bytes of a word.  Adding 1.5 * 2^23
 // rounds to a whole number (ties to even) whose two's complement is in the low bits;
-// |v r| <= 127 (1 + 2^-22), so no clamp is needed.  A NaN product (r = 0) has a zero low byte.
+// |v r| <= 127 (1 + 2^-22), so no clamp is needed.  A bad row (r = 0, which no other row has) may hold NaNs, whose
+// payload comes through product and sum: there the bytes are taken from no word at all (selector 0x0C: zero), which
+// costs nothing a value, the two selectors being the row's.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float r) {
   const float m = 12582912.0f;
   const uint32_t x = __float_as_uint(a * r + m), y = __float_as_uint(b * r + m);
   const uint32_t z = __float_as_uint(c * r + m), w = __float_as_uint(d * r + m);
-  const uint32_t lo = __builtin_amdgcn_perm(y, x, 0x0C0C0400u), hi = __builtin_amdgcn_perm(w, z, 0x04000C0Cu);
+  const bool bad = r == 0.0f;
+  const uint32_t lo = __builtin_amdgcn_perm(y, x, bad ? 0x0C0C0C0Cu : 0x0C0C0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(w, z, bad ? 0x0C0C0C0Cu : 0x04000C0Cu);
   return lo | hi;
 }
 
