@@ -161,11 +161,12 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2* scratch) {
 // 3000.7, which eps = 1e-5 would show as 0.15); the second pass takes d = x - p, which is small or exact, and gives
 // mean = p + sum d / n, M2 = sum d^2 - (sum d)^2 / n.
 //
+// Y may be X: a thread loads all that it needs before it stores, so neither is __restrict__.
 // NV vectors of V channels per thread.  stat != NULL: the statistics alone, (mean, rstd) to stat[b][g].
 template <typename T, typename TY, int V, int NV>
-__global__ __launch_bounds__(1024) void k7_one(const T* __restrict__ X, int64_t bsx, int64_t ldx, int S, int C, int G,
-                                               float eps, const float* __restrict__ gamma,
-                                               const float* __restrict__ beta, int act, TY* __restrict__ Y, int64_t bsy,
+__global__ __launch_bounds__(1024) void k7_one(const T* X, int64_t bsx, int64_t ldx, int S, int C, int G, float eps,
+                                               const float* __restrict__ gamma, const float* __restrict__ beta,
+                                               int act, TY* Y, int64_t bsy,
                                                int64_t ldy, float2* __restrict__ stat) {
   extern __shared__ float lds[];  // gamma, beta of the group
   __shared__ float2 scratch[16];
@@ -454,12 +455,13 @@ __global__ __launch_bounds__(JN_NT) void k7_join(Stats st, float2* __restrict__ 
 // ---- the output pass
 
 // Positions [i * chunk, + chunk) of image blockIdx.y, i counted from the end: the statistics pass
-// ended there, so that part of x is the likeliest to be in cache still.
+// ended there, so that part of x is the likeliest to be in cache still.  Y may be X: a value is stored by the thread that
+// loaded it, after it did, so neither is __restrict__; a load past the end takes a value that another thread may have
+// written by then, and does not use it.
 template <typename T, typename TY, int V, bool NT>
-__global__ __launch_bounds__(AP_NT) void k7_apply(const T* __restrict__ X, int64_t bsx, int64_t ldx, int64_t chunk,
-                                                  Stats st, const float* __restrict__ gamma,
-                                                  const float* __restrict__ beta, int act, TY* __restrict__ Y,
-                                                  int64_t bsy, int64_t ldy) {
+__global__ __launch_bounds__(AP_NT) void k7_apply(const T* X, int64_t bsx, int64_t ldx, int64_t chunk, Stats st,
+                                                  const float* __restrict__ gamma, const float* __restrict__ beta,
+                                                  int act, TY* Y, int64_t bsy, int64_t ldy) {
   extern __shared__ float lds[];
   __shared__ double scratch[AP_NT];
   float2* stat = reinterpret_cast<float2*>(lds);

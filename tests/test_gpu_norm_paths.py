@@ -49,3 +49,21 @@ def test_constant_image_gives_zero_codes(B, S, C):
     X = torch.full((B, S, C), 3000.7, device="cuda:0")
     q, s = svdq.GroupNorm(8, C).quantize(X)
     assert not q.any() and torch.equal(s, torch.full_like(s, float(np.float32(2.0 ** -96) / np.float32(127))))
+
+
+@pytest.mark.parametrize("B,S,G,C,one", [(3, 150, 8, 96, True), (2, 6000, 8, 64, False), (1, 5003, 3, 9, False), (1, 5000, 8, 264, False),
+                                         (1, 70001, 4, 128, False)])
+@pytest.mark.parametrize("xd", ["bf16", "f32"])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_in_place(B, S, G, C, one, xd, pad):
+    """Y may be X itself, on every path: the bits of the call into another tensor."""
+    torch = _torch()
+    buf = torch.randn((B, S, C + pad), device="cuda:0", generator=torch.Generator("cuda:0").manual_seed(C))
+    buf = buf.to({"bf16": torch.bfloat16, "f32": torch.float32}[xd])
+    X, rest = buf[:, :, :C], buf[:, :, C:].clone()
+    gn = svdq.GroupNorm(G, C, act=svdq.GN_SILU)
+    assert (gn.workspace(B, S, X.device) is None) == one
+    ydtype = svdq.F32 if xd == "f32" else svdq.BF16
+    want = gn.forward(X, ydtype)
+    assert gn.forward(X, ydtype, out=X) is X
+    assert torch.equal(X, want) and torch.equal(buf[:, :, C:], rest)
