@@ -40,9 +40,12 @@ svdq_status check_dims_int8(const svdq_int8_layer* L) {
   return SVDQ_OK;
 }
 
-// the product's tiles are counted in 31 bits
+// a launch takes fewer than 2^32 threads: 256 or more to a tile, 512 to 16 channels where there are few tokens
 svdq_status check_tiles(int64_t M, int64_t N) {
-  if (((M + 63) / 64) * ((N + 63) / 64) > kMaxRows) return fail(SVDQ_EUNSUPPORTED, "M * N must be < 2^43");
+  const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64);
+  if (tiles > kMaxRows) return fail(SVDQ_EUNSUPPORTED, "M * N must be < 2^43");
+  if (tiles >= int64_t(1) << 24) return fail(SVDQ_EUNSUPPORTED, "ceil(M / 64) * ceil(N / 64) must be < 2^24");
+  if ((N + 15) / 16 >= int64_t(1) << 23) return fail(SVDQ_EUNSUPPORTED, "N must be <= 2^27 - 16");
   return SVDQ_OK;
 }
 
@@ -135,12 +138,14 @@ using namespace svdq;
 extern "C" {
 
 size_t svdq_gemm_w8a8_workspace_bytes(const svdq_int8_layer* layer, int64_t M) {
-  if (M < 1 || check_dims_int8(layer) != SVDQ_OK || check_rows(M) != SVDQ_OK) return 0;
+  if (M < 1 || check_dims_int8(layer) != SVDQ_OK || check_rows(M) != SVDQ_OK || check_tiles(M, layer->N) != SVDQ_OK) return 0;
   return rup(plan_w8a8(M, layer->K, layer->N).bytes);
 }
 
 size_t svdq_int8_workspace_bytes(const svdq_int8_layer* layer, int64_t M, int32_t xdtype) {
-  if (M < 1 || check_dims_int8(layer) != SVDQ_OK || check_rows(M) != SVDQ_OK || check_xdtype(xdtype) != SVDQ_OK) return 0;
+  if (M < 1 || check_dims_int8(layer) != SVDQ_OK || check_rows(M) != SVDQ_OK || check_xdtype(xdtype) != SVDQ_OK ||
+      check_tiles(M, layer->N) != SVDQ_OK)
+    return 0;
   if (few_layer(M, layer->K)) return 0;
   return act_bytes(M, layer->K) + svdq_gemm_w8a8_workspace_bytes(layer, M);
 }
@@ -240,7 +245,7 @@ svdq_status svdq_group_norm_quantize_int8(const svdq_group_norm_desc* norm, int6
 size_t svdq_norm_linear_int8_workspace_bytes(const svdq_group_norm_desc* norm, const svdq_int8_layer* layer,
                                              int64_t B, int64_t S) {
   const size_t n = svdq_group_norm_quantize_workspace_bytes(norm, B, S);
-  if (n == 0 || check_dims_int8(layer) != SVDQ_OK || layer->K != norm->C) return 0;
+  if (n == 0 || check_dims_int8(layer) != SVDQ_OK || layer->K != norm->C || check_tiles(B * S, layer->N) != SVDQ_OK) return 0;
   return n + act_bytes(B * S, layer->K) + svdq_gemm_w8a8_workspace_bytes(layer, B * S);
 }
 

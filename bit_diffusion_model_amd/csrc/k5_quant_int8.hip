@@ -108,16 +108,22 @@ __global__ __launch_bounds__(Q_NT) void k5_quant(const T* __restrict__ X, int64_
 template <typename T, bool VEC, bool SMOOTH>
 void launch(int64_t M, int64_t K, const T* X, int64_t ldx, const float* inv_s, int8_t* qX, float* sX, hipStream_t st) {
   const int ldq = (int)i8_ld(K);
-  auto go = [&](auto kernel, int64_t blocks) {
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)blocks), dim3(Q_NT), 0, st, X, ldx, M, (int)K, inv_s, qX, ldq, sX);
+  // a launch takes fewer than 2^32 threads: more rows than that go in several
+  auto go = [&](auto kernel, int64_t per_block) {
+    const int64_t slab = per_block << 23;
+    for (int64_t m = 0; m < M; m += slab) {
+      const int64_t rows = M - m < slab ? M - m : slab;
+      hipLaunchKernelGGL(kernel, dim3((uint32_t)((rows + per_block - 1) / per_block)), dim3(Q_NT), 0, st, X + m * ldx, ldx,
+                         rows, (int)K, inv_s, qX + m * ldq, ldq, sX + m);
+    }
   };
-  if (ldq <= 512) go(k5_quant<T, VEC, SMOOTH, 1, 1>, (M + 3) / 4);
-  else if (ldq <= 1024) go(k5_quant<T, VEC, SMOOTH, 1, 2>, (M + 3) / 4);
-  else if (ldq <= 2048) go(k5_quant<T, VEC, SMOOTH, 4, 1>, M);
-  else if (ldq <= 4096) go(k5_quant<T, VEC, SMOOTH, 4, 2>, M);
-  else if (ldq <= 8192) go(k5_quant<T, VEC, SMOOTH, 4, 4>, M);
-  else if (ldq <= 16384) go(k5_quant<T, VEC, SMOOTH, 4, 8>, M);
-  else go(k5_quant<T, VEC, SMOOTH, 4, 0>, M);
+  if (ldq <= 512) go(k5_quant<T, VEC, SMOOTH, 1, 1>, 4);
+  else if (ldq <= 1024) go(k5_quant<T, VEC, SMOOTH, 1, 2>, 4);
+  else if (ldq <= 2048) go(k5_quant<T, VEC, SMOOTH, 4, 1>, 1);
+  else if (ldq <= 4096) go(k5_quant<T, VEC, SMOOTH, 4, 2>, 1);
+  else if (ldq <= 8192) go(k5_quant<T, VEC, SMOOTH, 4, 4>, 1);
+  else if (ldq <= 16384) go(k5_quant<T, VEC, SMOOTH, 4, 8>, 1);
+  else go(k5_quant<T, VEC, SMOOTH, 4, 0>, 1);
 }
 
 template <typename T, bool VEC>

@@ -449,8 +449,9 @@ svdq_status svdq_mlp_chain_reduce(const svdq_layer* fc1, const svdq_layer* fc2, 
  * Rows of codes, of activations and weights alike, are svdq_int8_ld(K) = K rounded up to 128
  * bytes long; the bytes past K are zero.  X is fp32 or bf16 (svdq_dtype SVDQ_F32 /
  * SVDQ_BF16) of any K >= 1 and any row stride ldx >= K; rows of X and Y may begin at any
- * element's address.  Limits: K <= 131072 (the integer sums stay below 2^31), M, N, ldx and
- * ldy below 2^31, M N below 2^43 (EUNSUPPORTED beyond). */
+ * element's address.  Limits: K <= 131072 (the integer sums stay below 2^31), M, ldx and ldy
+ * below 2^31; the product also N <= 2^27 - 16 and ceil(M / 64) ceil(N / 64) < 2^24 (EUNSUPPORTED
+ * beyond, with nothing launched). */
 typedef struct svdq_int8_layer {
   int64_t K, N;
   const float* inv_s; /* [K] fp32 reciprocal smoothing factor, or NULL for none */
