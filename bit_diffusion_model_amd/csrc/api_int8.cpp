@@ -110,10 +110,10 @@ svdq_status norm_args(const svdq_group_norm_desc* n, int64_t B, int64_t S, const
                       int64_t ldx, NormArgs& a) {
   svdq_status st = check_in(X, xdtype, ldx, n->C);
   if (st != SVDQ_OK) return st;
-  // images must not overlap (with one image the stride is not used)
+  // images are apart, or one and the same (with one image the stride is not used)
   if (B > 1 && bsx >= (int64_t(1) << 46)) return fail(SVDQ_EUNSUPPORTED, "bsx must be < 2^46");
-  if (B > 1 && (bsx < n->C || (bsx < (S - 1) * ldx + n->C && ldx < (B - 1) * bsx + n->C)))
-    return fail(SVDQ_EINVAL, "bsx must be >= (S - 1) * ldx + C");
+  if (B > 1 && bsx != 0 && (bsx < n->C || (bsx < (S - 1) * ldx + n->C && ldx < (B - 1) * bsx + n->C)))
+    return fail(SVDQ_EINVAL, "bsx must be 0 or >= (S - 1) * ldx + C");
   a = NormArgs{B, S, (int)n->C, n->groups, n->act, n->eps, n->gamma, n->beta, X, xdtype, B > 1 ? bsx : 0, ldx};
   return SVDQ_OK;
 }

@@ -67,3 +67,21 @@ def test_in_place(B, S, G, C, one, xd, pad):
     want = gn.forward(X, ydtype)
     assert gn.forward(X, ydtype, out=X) is X
     assert torch.equal(X, want) and torch.equal(buf[:, :, C:], rest)
+
+
+@pytest.mark.parametrize("B,S,G,C", [(3, 64, 8, 96), (2, 6000, 8, 64), (5, 41, 3, 33), (2, 40000, 4, 128)])
+@pytest.mark.parametrize("xd", ["bf16", "f32"])
+def test_one_image_as_many(B, S, G, C, xd):
+    """An image expanded over the batch (image stride 0) gives the bits of its copies; only Y's images have to be apart."""
+    torch = _torch()
+    one = torch.randn((1, S, C), device="cuda:0", generator=torch.Generator("cuda:0").manual_seed(S))
+    one = one.to({"bf16": torch.bfloat16, "f32": torch.float32}[xd])
+    X, copies = one.expand(B, S, C), one.repeat(B, 1, 1)
+    gn = svdq.GroupNorm(G, C, act=svdq.GN_SILU)
+    assert torch.equal(gn.forward(X, svdq.F32), gn.forward(copies, svdq.F32))
+    for a, b in zip(gn.quantize(X), gn.quantize(copies)):
+        assert torch.equal(a, b)
+    lin = svdq.Int8Linear(np.ones((20, svdq.int8_ld(C)), np.int8), np.ones(20, np.float32), C)
+    assert torch.equal(gn.forward_linear(X, lin), gn.forward_linear(copies, lin))
+    with pytest.raises(svdq.SvdqError, match="bsy"):
+        gn.forward(X, svdq.F32 if xd == "f32" else svdq.BF16, out=X)
