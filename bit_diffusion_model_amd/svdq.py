@@ -696,7 +696,7 @@ class Int8Linear:
             raise SvdqError(f"the layer is on cuda:{self._dev}, the input on {X.device}")
         if out is None:
             return torch.empty((M, self.N), dtype=ty[ydtype], device=X.device)
-        if out.shape != (M, self.N) or out.dtype != ty[ydtype] or out.stride(1) != 1:
+        if out.shape != (M, self.N) or out.dtype != ty[ydtype] or (self.N > 1 and out.stride(1) != 1):
             raise SvdqError(f"out must be a [{M}][{self.N}] {ty[ydtype]} device tensor with unit column stride")
         _on(out, self._dev, "out")
         return out

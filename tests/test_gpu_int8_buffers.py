@@ -93,3 +93,14 @@ def test_layer_and_norm_on_another_device(monkeypatch):
     for call in (lambda: gn.forward(X[None]), lambda: gn.quantize(X[None]), lambda: gn.forward_linear(X[None], lin)):
         with pytest.raises(svdq.SvdqError, match="cuda:1"):
             call()
+
+
+def test_one_channel_out_of_any_stride():
+    """With one channel the column stride of `out` addresses nothing, as with one value a row in X."""
+    torch = _torch()
+    lin = svdq.Int8Linear(np.ones((1, 128), np.int8), np.ones(1, np.float32), 5)
+    for m in (1, 3, 90):
+        X = torch.arange(5.0 * m, device="cuda:0").view(m, 5)
+        out = torch.as_strided(torch.full((3 * m + 7,), 8.0, device="cuda:0"), (m, 1), (3, 7))
+        assert torch.equal(lin.forward(X, out=out), lin.forward(X))
+        assert torch.equal(lin.gemm(*lin.quantize(X), out=out), lin.forward(X))
