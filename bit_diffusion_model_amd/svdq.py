@@ -75,6 +75,10 @@ def lib():
         return _lib
     if not os.path.exists(LIB_PATH):
         raise SvdqError(f"{LIB_PATH} is missing: build it with bit_diffusion_model_amd.build.build()")
+    try:  # torch's own HIP runtime, if there is one, before the library asks for the system's: one to a process
+        import torch  # noqa: F401
+    except ImportError:
+        pass
     L = ctypes.CDLL(LIB_PATH)
     P, I64, I32, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
     sig = {
