@@ -242,6 +242,24 @@ svdq_status svdq_group_norm_quantize_int8(const svdq_group_norm_desc* norm, int6
   return ok();
 }
 
+svdq_status svdq_debug_w8a8_plan(const svdq_int8_layer* layer, int64_t M, int32_t plan[4]) {
+  svdq_status st = check_dims_int8(layer);
+  if (st != SVDQ_OK || (st = check_rows(M)) != SVDQ_OK || (st = check_tiles(M, layer->N)) != SVDQ_OK) return st;
+  if (M < 1 || !plan) return fail(SVDQ_EINVAL, "M must be >= 1 and plan non-NULL");
+  const W8A8Plan p = plan_w8a8(M, layer->K, layer->N);
+  plan[0] = p.tile, plan[1] = p.groups, plan[2] = p.parts, plan[3] = (int32_t)p.halved;
+  return ok();
+}
+
+svdq_status svdq_debug_group_norm_plan(const svdq_group_norm_desc* norm, int64_t B, int64_t S, int32_t plan[4]) {
+  svdq_status st = check_norm(norm, B, S);
+  if (st != SVDQ_OK) return st;
+  if (B < 1 || S < 1 || !plan) return fail(SVDQ_EINVAL, "B and S must be >= 1 and plan non-NULL");
+  const NormPlan p = plan_norm(B, S, (int)norm->C, norm->groups);
+  plan[0] = p.one, plan[1] = p.join, plan[2] = (int32_t)p.parts, plan[3] = (int32_t)p.blocks;
+  return ok();
+}
+
 size_t svdq_norm_linear_int8_workspace_bytes(const svdq_group_norm_desc* norm, const svdq_int8_layer* layer,
                                              int64_t B, int64_t S) {
   const size_t n = svdq_group_norm_quantize_workspace_bytes(norm, B, S);

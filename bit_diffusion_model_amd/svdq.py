@@ -63,7 +63,7 @@ EXPORTS = [
     "svdq_quantize_act_int8", "svdq_gemm_w8a8_workspace_bytes",
     "svdq_int8_workspace_bytes", "svdq_gemm_w8a8", "svdq_linear_forward_int8", "svdq_group_norm_workspace_bytes",
     "svdq_group_norm_quantize_workspace_bytes", "svdq_group_norm", "svdq_group_norm_quantize_int8", "svdq_norm_linear_int8_workspace_bytes",
-    "svdq_norm_linear_forward_int8",
+    "svdq_norm_linear_forward_int8", "svdq_debug_w8a8_plan", "svdq_debug_group_norm_plan",
 ]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -123,6 +123,8 @@ def lib():
         "svdq_group_norm": (I32, [P, I64, I64, P, I32, I64, I64, P, I32, I64, I64, P, SZ, P]),
         "svdq_group_norm_quantize_int8": (I32, [P, I64, I64, P, I32, I64, I64, P, P, P, P, SZ, P]),
         "svdq_norm_linear_int8_workspace_bytes": (SZ, [P, P, I64, I64]),
+        "svdq_debug_w8a8_plan": (I32, [P, I64, P]),
+        "svdq_debug_group_norm_plan": (I32, [P, I64, I64, P]),
         "svdq_norm_linear_forward_int8": (I32, [P, P, I64, I64, P, I32, I64, I64, P, I64, I32, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
@@ -720,6 +722,12 @@ class Int8Linear:
                                 _ld(M, out.stride(0), self.N), ydtype, *_scratch(ws, self._dev), _raw_stream(qX)))
         return out
 
+    def plan(self, M: int):
+        """svdq_debug_w8a8_plan: (tile, K groups, K parts, halved tiles) of the product of M rows."""
+        p = (ctypes.c_int32 * 4)()
+        _check(lib().svdq_debug_w8a8_plan(self._ref, M, p))
+        return tuple(p)
+
     def workspace(self, M: int, xdtype: int = BF16):
         """Device scratch of forward() for M rows of X (None when unused)."""
         torch, _, _, L = _rt()
@@ -801,6 +809,12 @@ class GroupNorm:
                 raise SvdqError(f"{what}'s rows of positions must follow each other at one stride")
             return B, H * W, X.stride(0), _ld(H * W, X.stride(2) if W > 1 else X.stride(1), self.C)
         return X.shape[0], X.shape[1], X.stride(0), _ld(X.shape[1], X.stride(1), self.C)
+
+    def plan(self, B: int, S: int):
+        """svdq_debug_group_norm_plan: (one launch, joined apart, statistics blocks, output blocks)."""
+        p = (ctypes.c_int32 * 4)()
+        _check(lib().svdq_debug_group_norm_plan(self._ref, B, S, p))
+        return tuple(p)
 
     def workspace(self, B: int, S: int, device, quantize: bool = False):
         """Device scratch of forward() (None when unused), or of quantize()."""

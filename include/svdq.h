@@ -553,6 +553,15 @@ svdq_status svdq_norm_linear_forward_int8(const svdq_group_norm_desc* norm, cons
                                           int64_t ldy, int32_t ydtype, void* workspace, size_t ws_bytes,
                                           void* stream);
 
+/* Diagnostics: which kernels a call runs on the current device, so that a test can ask for the one it means.
+ *   svdq_debug_w8a8_plan: plan = {tile (64, 128 or 256; 0: the kernel for few tokens), K groups, K parts, tiles of 256
+ *     that run as halves}; the product of M rows, alone or in a layer.
+ *   svdq_debug_group_norm_plan: plan = {1 where one launch serves the norm, 1 where the blocks' statistics are joined by
+ *     a launch of their own, statistics blocks and output blocks per image}.
+ * EINVAL / EUNSUPPORTED as the calls themselves; host only, nothing is launched. */
+svdq_status svdq_debug_w8a8_plan(const svdq_int8_layer* layer, int64_t M, int32_t plan[4]);
+svdq_status svdq_debug_group_norm_plan(const svdq_group_norm_desc* norm, int64_t B, int64_t S, int32_t plan[4]);
+
 /* Diagnostic: the exact integer group sums I[g][m][n] = sum_{k in group g} qX[m][k]
  * qW[n][k] (INT4 only; the review's section 3 product Q_X Q_W, taken per group) for the
  * window rows [m0, m0+mt) x cols [n0, n0+nt).  out: device int32 [K/64][mt][nt].
