@@ -17,9 +17,11 @@
 //    after k7_join where there are many: an output block would read them all).  A thread keeps
 //    the same V consecutive channels over all its positions, so group boundaries may fall
 //    anywhere: sums are kept per channel and meet per group in LDS.
-// Statistics in fp32: a thread sums d = x - p and d^2 per channel, p its first value, so that
-// (mean, M2) = (p + sum d / n, sum d^2 - (sum d)^2 / n): since p is one of the n values, M2 >=
-// (p - mean)^2 and the subtraction loses at most a factor n (the thread's positions, 32 or so).
+// Statistics in fp32: a thread sums d = x - p and d^2 per channel, so that (mean, M2) = (p + sum d / n,
+// sum d^2 - (sum d)^2 / n).  p is its first value for eight positions, then these eight's mean: M2 >= 8 (p - mean)^2,
+// so that the subtraction loses at most a factor n / 8.  n, the thread's positions, is at most 512 (32 at
+// 65536x256, 64 at 262144x256); with the first value for all of 4096 positions a first value 30 standard
+// deviations off cost 5e-4 of M2.
 // Threads, then blocks, are joined by mean = sum n_i mean_i / n, M2 = sum (M2_i + n_i (mean_i -
 // mean)^2) (the pairwise formula of Chan, Golub and LeVeque, summed).
 #include <type_traits>
@@ -318,11 +320,24 @@ __global__ __launch_bounds__(ST_NT) void k7_stats(const T* __restrict__ X, int64
       };
       Vec<T, V> raw[U];
       int i = pl.row;
-      for (; i + (U - 1) * pl.rp < rows; i += U * pl.rp) {
+      auto whole = [&] { return i + (U - 1) * pl.rp < rows; };
+      auto eight = [&] {
 #pragma unroll
         for (int j = 0; j < U; ++j, at += step) raw[j] = loadv<T, V>(at);
 #pragma unroll
         for (int j = 0; j < U; ++j) add(raw[j]);
+        i += U * pl.rp;
+      };
+      if (whole()) {
+        eight();
+#pragma unroll
+        for (int e = 0; e < V; ++e) {  // the same sums about the eight's mean
+          const float to = p[e] + s[e] * (1.0f / U), d = to - p[e];
+          q[e] = fmaf(-d, fmaf(-(float)U, d, 2.0f * s[e]), q[e]);
+          s[e] = fmaf(-(float)U, d, s[e]);
+          p[e] = to;
+        }
+        while (whole()) eight();
       }
       const T* end = at;  // at most U - 1 more positions
 #pragma unroll
@@ -791,6 +806,7 @@ NormPlan plan_norm(int64_t B, int64_t S, int C, int G) {
   const int cv = C % 8 == 0 ? C / 8 : C, rp = 256 / place_ct(cv, 256);
   p.chunk = (S + parts - 1) / parts;
   if (p.chunk < 2 * rp) p.chunk = 2 * rp;
+  if (p.chunk > 512 * rp) p.chunk = 512 * rp;  // positions that a thread sums
   p.parts = (uint32_t)((S + p.chunk - 1) / p.chunk);
   p.bytes = ((size_t)B * p.parts * G + (size_t)B * G) * sizeof(float2);
   const int64_t blocks = !p.join ? 256 : n <= (int64_t(1) << 25) ? 768 : 2048;

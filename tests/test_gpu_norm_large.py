@@ -174,3 +174,30 @@ def test_other_stream_and_layout(B, S, G, C):
     T = X.transpose(0, 1).contiguous().transpose(0, 1)
     out = torch.empty((S, B, C), dtype=torch.bfloat16, device="cuda:0").transpose(0, 1)
     assert torch.equal(gn.forward(T, out=out), ref)
+
+
+# Long sums: 512 blocks of statistics over inputs so large that a thread would have thousands of positions, the first of
+# which (the pivot of its sums) is an outlier.  One channel to a load, so that a thread owns a single channel.
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,S,G,C", [(512, 4096, 3, 129), (1, 1 << 20, 1, 129), (300, 9000, 1, 136)])
+@pytest.mark.parametrize("sds", [3.0, 30.0, 1000.0])
+def test_outliers_first(B, S, G, C, sds):
+    """A thread has at most 512 positions and sums all but 8 about the mean of these 8, so that its M2 is off by at most
+    512 u from the sums and 512 / 8 times 4 u from the subtraction (M2 >= 8 (pivot - mean)^2): 768 u in all."""
+    torch = _torch()
+    x = torch.randn((B, S, C), device="cuda:0", generator=torch.Generator("cuda:0").manual_seed(7))
+    chunk = -(-S // max(1, -(-512 // B)))  # where blocks may begin
+    for at in {0, chunk, 2 * chunk, 5 * chunk, 512, 1024, S - 1}:
+        if at < S:
+            x[:, at] = sds
+    gn = svdq.GroupNorm(G, C)
+    assert gn.plan(B, S)[:2] == (0, 1)
+    Y = gn.forward(x, svdq.F32)
+    for b in {0, B // 2, B - 1}:
+        v = x[b].double().reshape(S, G, C // G)
+        mean = v.mean((0, 2), keepdim=True)
+        sd = ((v - mean).square().mean((0, 2), keepdim=True) + 1e-5).sqrt()
+        z = ((v - mean) / sd).reshape(S, C)
+        tol = U * (768.0 * z.abs() / 2 + 4 * z.abs()) + 512 * U / 8 + U * ((v.abs() + 2 * mean.abs()) / sd).reshape(S, C)
+        off = (Y[b].double() - z).abs()
+        assert bool((off <= tol).all()), f"image {b}: worst {float((off / tol).max())} of the bound"
