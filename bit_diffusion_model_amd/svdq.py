@@ -641,7 +641,8 @@ def _scratch(ws, dev: int):
     """(address, bytes) of a workspace tensor, or of none."""
     if ws is None:
         return None, 0
-    _on(ws, dev, "the workspace")
+    if ws.get_device() != dev:
+        _on(ws, dev, "the workspace")
     if not ws.is_contiguous():
         raise SvdqError("the workspace must be contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size()
@@ -682,6 +683,7 @@ class Int8Linear:
         self.bias = _dev_tensor(bias, "bias", torch.float32, device, self.N)
         self.device = self.qW.device
         self._dev = _one_device((self.qW, self.sW, self.inv_s, self.bias), "layer")
+        self._ld = int8_ld(self.K)
         self._c = _Int8Layer(self.K, self.N, _dptr(self.inv_s), _dptr(self.qW), _dptr(self.sW), _dptr(self.bias))
         self._ref = ctypes.addressof(self._c)
 
@@ -710,12 +712,13 @@ class Int8Linear:
     def gemm(self, qX, sX, ydtype: int = F32, out=None, workspace=None):
         """svdq_gemm_w8a8: Y [M][N] from codes qX int8 [M][int8_ld(K)] and their scales sX fp32 [M]."""
         torch, _, _, L = _rt()
-        if qX.dim() != 2 or qX.dtype != torch.int8 or sX.dtype != torch.float32 or qX.shape[1] != int8_ld(self.K) or \
-                sX.numel() != qX.shape[0] or not qX.is_contiguous() or not sX.is_contiguous():
-            raise SvdqError(f"qX must be contiguous int8 [M][{int8_ld(self.K)}] and sX contiguous fp32 [M]")
-        M = qX.shape[0]
+        M = sX.numel()
+        if qX.shape != (M, self._ld) or qX.dtype != torch.int8 or sX.dtype != torch.float32 or \
+                not qX.is_contiguous() or not sX.is_contiguous():
+            raise SvdqError(f"qX must be contiguous int8 [M][{self._ld}] and sX contiguous fp32 [M]")
         out = self._out(M, ydtype, out, qX)
-        _on(sX, self._dev, "sX")
+        if sX.get_device() != self._dev:
+            _on(sX, self._dev, "sX")
         n = L.svdq_gemm_w8a8_workspace_bytes(self._ref, M)
         ws = workspace if workspace is not None or n == 0 else torch.empty(n, dtype=torch.uint8, device=qX.device)
         _check(L.svdq_gemm_w8a8(self._ref, M, qX.data_ptr(), sX.data_ptr(), out.data_ptr(),
