@@ -5,13 +5,13 @@
 // group's cpg channels: mean, var (biased); y = act((x - mean) / sqrt(var + eps) gamma_c +
 // beta_c), x - mean formed first so that a mean far from zero costs no digits.
 //
-// Bound by HBM where x and y pass the 256 MB cache (262144x256 fp32, x read twice and y written:
-// 151 us, 5.3 TB/s), by the cache below that (65536x256 bf16 29.3 us), by launches and the
-// blocks' meeting in the smallest.  Three kernels:
+// Bound by HBM where x and y pass the 256 MB cache (262144x256 fp32, x read twice and y written: 157 us a
+// call with inputs in turn, 5.1 TB/s; 151 on one input over and over), by the cache below that (65536x256
+// bf16 26 us), by launches and the blocks' meeting in the smallest.  Three kernels:
 //  * k7_one: a block holds one image's group in registers: x read once, mean and variance by
 //    two passes over the registers, one launch.  Taken where a group's values fit the
 //    registers of 1024 threads in few loads (the plan below holds the figures: 2x64x1280 in
-//    groups of 40 3.8 us against the two launches' 10.5);
+//    groups of 40 3.4 us against the two launches' 9.7);
 //  * k7_stats, then k7_apply (or k7_apply_quant): statistics per block of positions, and the
 //    output pass, which first joins the blocks' statistics (by itself where there are few,
 //    after k7_join where there are many: an output block would read them all).  A thread keeps
@@ -538,8 +538,9 @@ __global__ __launch_bounds__(AP_NT) void k7_apply(const T* X, int64_t bsx, int64
 // The output pass into codes: a wave takes U whole positions (rows of C channels) at once, NC chunks
 // of 512 channels each in registers.  Per channel (mean, rstd gamma, beta, inv_s) wait in LDS, eight
 // planes of C / 8 so that neighbouring lanes read neighbouring 16 bytes, read once for U rows.
-// The next rows' loads are under way while these are computed (4x4096x320 21.4 -> 18.7 us, both
-// launches; about 30 VALU instructions a value are what bounds it now).
+// The next rows' loads are under way while these are computed (4x4096x320 with its statistics 21.4 -> 18.7
+// us back to back).  Bound by vector instructions, 31 to a lane's value; a row of 320, 640 or 1280
+// channels fills 62% of the lanes that it takes, so that is 50 to a value (4x4096x320: 14 us of this pass).
 template <typename T, bool VEC, int NC, int U>
 __global__ __launch_bounds__(AP_NT) void k7_apply_quant(const T* __restrict__ X, int64_t bsx, int64_t ldx,
                                                         int64_t chunk, Stats st, const float* __restrict__ gamma,
@@ -787,10 +788,14 @@ Stats run_stats(const NormArgs& a, const NormPlan& p, void* ws, hipStream_t st) 
 NormPlan plan_norm(int64_t B, int64_t S, int C, int G) {
   NormPlan p{};
   const int64_t cpg = C / G;
-  // Measured (us, one launch / two): groups of 16 over 2048 positions 8.5 / 13.0, of 8 over 4096 10.1 / 12.2, of 10 over
-  // 1024 7.8 / 11.9, over 2000 14.1 / 13.4, of 3 over 2700 9.8 / 11.5, over 5000 16.8 / 12.1, of 4 over 8000 21.7 / 13.1, of
-  // 1 over 8000 10.6 / 11.2, of 35 over 300 10.1 / 10.7, over 794 16.6 / 14.6: what counts are the loads, at most 8 per
-  // thread of 1024, and the rows that they touch.
+  // What counts are the loads, at most 8 per thread of 1024, and the rows that they touch.  Measured (us, bf16, SiLU, back to
+  // back; one launch / two): 2x64x1280 in groups of 40 3.4 / 9.7, 2x256x1280 5.3 / 10.0, 2x1024x640 of 20 8.0 / 11.3,
+  // 2x2048x512 of 16 9.0 / 12.3, 2x1024x320 of 10 7.8 / 10.8, 2x2000x320 11.8 / 11.7, 2x2700x96 of 3 9.2 / 10.7, 2x700x77
+  // of 11 5.8 / 9.9, 2x8000x32 of 1 12.1 / 10.7, 2x8000x128 of 4 22.1 / 12.4.  Statistics alone, in front of the codes (either way
+  // two launches): 2x64x1280 9.1 / 12.5, 2x1024x640 9.2 / 11.8, 2x2048x512 10.0 / 12.4, 2x4096x256 of 8 11.9 / 12.3, 2x2700x96
+  // 8.6 / 11.0, 2x8000x128 13.8 / 12.4.  Not in the rule, and against it: many images (8x1024x640 14.0 / 15.7, 16x1024x640
+  // 26.4 / 22.0, codes 26.5 / 22.1) and short pieces of long rows, whose lines are read by several blocks (2x4096x256 in
+  // groups of 8, 16 bytes to a row, 15.6 / 12.4; one image 10.3).
   p.one = S * cpg <= 32 * 1024 && S * (cpg / one_width((int)cpg)) <= 8 * 1024 && S <= 4096;
   // Measured (us, both launches or all three; statistics blocks / output blocks):
   //   2x4096x320 bf16 256 / 256 13.4, 256 / 512 15.0, 256 joined apart / 256 14.9, 256 / 1024 17.2

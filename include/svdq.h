@@ -510,17 +510,19 @@ svdq_status svdq_linear_forward_int8(const svdq_int8_layer* layer, int64_t M, co
  * groups * cpg.  Per image and group over all positions and the group's channels: mean and
  * biased variance in fp32 (sums of differences to a pivot, joined pairwise: no cancellation
  * however far the mean lies from zero); y = act((x - mean) / sqrt(var + eps) gamma_c + beta_c).
- * A NaN or an infinity makes its group's outputs NaN, as the formula does.  Images of X are apart (bsx >= (S - 1) ldx
- * + C, or positions interleaved: ldx >= (B - 1) bsx + C) or one and the same (bsx = 0).  Limits: C <= 4096, groups <=
- * 1024, B <= 65535, B S below 2^31, bsx and bsy below 2^46 (EUNSUPPORTED beyond).  B == 0 or S == 0 is a no-op. */
+ * A NaN or an infinity makes its group's outputs NaN, as the formula does; sums of squares have to stay within
+ * fp32 (they do at any size while |x - mean| < 2^42), beyond it the variance is not finite.  Images of X are
+ * apart (bsx >= (S - 1) ldx + C, or positions interleaved: ldx >= (B - 1) bsx + C) or one and the same (bsx = 0).
+ * Limits: C <= 4096, groups <= 1024, B <= 65535, B S below 2^31, bsx and bsy below 2^46 (EUNSUPPORTED beyond).
+ * B == 0 or S == 0 is a no-op. */
 typedef enum { SVDQ_GN_NONE = 0, SVDQ_GN_SILU = 1, SVDQ_GN_GELU = 2 } svdq_gn_act;
 typedef struct svdq_group_norm_desc {
   int64_t C;
   int32_t groups;
   int32_t act;        /* svdq_gn_act */
   float eps;          /* > 0 */
-  const float* gamma; /* device [C] fp32, or NULL for 1 */
-  const float* beta;  /* device [C] fp32, or NULL for 0 */
+  const float* gamma; /* device [C] fp32, 16-byte aligned, or NULL for 1 */
+  const float* beta;  /* device [C] fp32, 16-byte aligned, or NULL for 0 */
 } svdq_group_norm_desc;
 
 /* Bytes of device workspace of svdq_group_norm (0: none, where a group fits one block) and of
