@@ -19,7 +19,7 @@
 //    anywhere: sums are kept per channel and meet per group in LDS.
 // Statistics in fp32: a thread sums d = x - p and d^2 per channel, so that (mean, M2) = (p + sum d / n,
 // sum d^2 - (sum d)^2 / n).  p is its first value for eight positions, then these eight's mean: M2 >= 8 (p - mean)^2,
-// so that the subtraction loses at most a factor n / 8.  n, the thread's positions, is at most 512 (32 at
+// so that the subtraction loses at most a factor n / 8.  n, the thread's positions, is at most 512 (16 at
 // 65536x256, 64 at 262144x256); with the first value for all of 4096 positions a first value 30 standard
 // deviations off cost 5e-4 of M2.
 // Threads, then blocks, are joined by mean = sum n_i mean_i / n, M2 = sum (M2_i + n_i (mean_i -

@@ -500,7 +500,7 @@ svdq_status svdq_gemm_w8a8(const svdq_int8_layer* layer, int64_t M, const int8_t
 /* The layer: quantizer, then product, on `stream`, the codes in `workspace` (>=
  * svdq_int8_workspace_bytes, 256-byte aligned, contents on entry irrelevant); for few tokens one
  * launch that quantizes inside and needs no workspace.  The same result, bit for bit, as the
- * two calls above. */
+ * two calls above.  Y must not overlap X (for few tokens every block reads all of X). */
 svdq_status svdq_linear_forward_int8(const svdq_int8_layer* layer, int64_t M, const void* X, int32_t xdtype,
                                      int64_t ldx, void* Y, int64_t ldy, int32_t ydtype, void* workspace,
                                      size_t ws_bytes, void* stream);
@@ -531,7 +531,7 @@ size_t svdq_group_norm_workspace_bytes(const svdq_group_norm_desc* norm, int64_t
 size_t svdq_group_norm_quantize_workspace_bytes(const svdq_group_norm_desc* norm, int64_t B, int64_t S);
 
 /* Y [B][S][C] (position stride ldy, image stride bsy), SVDQ_F32 or SVDQ_BF16; X fp32 or bf16.
- * Y may be X itself (same type and strides).  workspace >= svdq_group_norm_workspace_bytes,
+ * Y may be X itself (same type and strides); otherwise they must not overlap.  workspace >= svdq_group_norm_workspace_bytes,
  * 256-byte aligned.  EINVAL on NULL, misalignment, sizes; EUNSUPPORTED on another type or a
  * limit; EHIP on launch error. */
 svdq_status svdq_group_norm(const svdq_group_norm_desc* norm, int64_t B, int64_t S, const void* X, int32_t xdtype,
