@@ -17,8 +17,9 @@ BUILD = os.path.join(HERE, "_build")
 ARCH = "gfx950"
 
 DEVICE_SOURCES = ["k1_quant_lora_down.hip", "k2_gemm_w4a4.hip", "k3_lora_up.hip", "k4_w4a16.hip", "k5_quant_int8.hip",
-                  "k6_gemm_w8a8.hip", "k7_group_norm.hip", "api.cpp", "api_int8.cpp", "noalloc.hip"]
-HOST_SOURCES = ["pack.cpp", "pack_int8.cpp", "status.cpp"]
+                  "k6_gemm_w8a8.hip", "k7_group_norm.hip", "k8_quant_fp8.hip", "k9_gemm_fp8.hip", "k10_layer_norm.hip",
+                  "api.cpp", "api_int8.cpp", "api_fp8.cpp", "noalloc.hip"]
+HOST_SOURCES = ["pack.cpp", "pack_int8.cpp", "pack_fp8.cpp", "status.cpp"]
 
 HIP_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17",

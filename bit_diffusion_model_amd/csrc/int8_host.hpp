@@ -1,4 +1,4 @@
-// Sizes of the 8-bit layer and the group norm shared by host and device code.
+// Sizes of the 8-bit layers and the norms shared by host and device code.
 #pragma once
 #include <stdint.h>
 
@@ -12,6 +12,8 @@ constexpr int64_t kMaxInt8K = 131072;
 // the norm keeps per-channel and per-group values in LDS
 constexpr int64_t kMaxNormC = 4096;
 constexpr int kMaxNormG = 1024;
+// a row of the layer norm stays in the registers of 16 waves
+constexpr int64_t kMaxLayerNormC = 16384;
 
 // Whether every row (from p, ld values apart; xdtype 0 fp32, 1 bf16) is 4-byte aligned.
 inline bool rows_aligned4(const void* p, int64_t ld, int xdtype) {

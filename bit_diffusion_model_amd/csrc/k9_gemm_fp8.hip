@@ -1,0 +1,637 @@
+// Kernel 9: the matrix product on E4M3 codes with a scale for each block of 128.
+//
+// Mathematics: y[m][n] = sum over blocks b of 128 along K of (sX[b][m] sW[n / 128][b]) D_b[m][n] + bias[n], D_b[m][n]
+// the sum of the block's 128 products of codes (exact products, added by the matrix core in fp32); blocks added in
+// fp32, then optionally GELU, rounded once to the output type.  qX comes as rows of ld bytes, sX as rows of Mp = M
+// rounded up to 4 along the tokens; qW in the fragment order of svdq_prepare_weights_int8: [N / 16][ld / 64] fragments
+// of 1 KB, lane l of a fragment holding channel l & 15 and the 16 codes k = 16 (l >> 4) .., N padded to 16 with zeros.
+// The matrix core takes 64 codes of K (32 x 32 tiles) or 128 (16 x 16) at once, 32 to a lane; a lane's 32 are two
+// 16-byte pieces of a fragment, the same pieces for both operands: a sum does not ask in which order k comes.
+#include <type_traits>
+
+#include "fp8.hpp"
+#include "gemm8.hpp"
+#include "kernels.hpp"
+#include "vec.hpp"
+
+namespace svdq {
+namespace {
+
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, float* lds, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, voff, soff, 0, 0);
+}
+
+__device__ __forceinline__ v8i join8(v4i a, v4i b) { return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
+
+// unscaled E4M3 x E4M3 (both scale operands the constant 0 choose the form without scales)
+__device__ __forceinline__ v16f mfma32(v8i a, v8i b, v16f c) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// Codes as f16 (exact: E4M3 has 4 significant bits and binary exponents from -9 to 8)
+typedef _Float16 v8hf __attribute__((ext_vector_type(8)));
+struct Half64 { v8hf v[8]; };
+__device__ __forceinline__ v8hf widen8(int a, int b) {
+  const h2 p = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false), q = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
+  const h2 r = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false), t = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
+  return v8hf{p.x, p.y, q.x, q.y, r.x, r.y, t.x, t.y};
+}
+__device__ __forceinline__ Half64 widen(v8i lo, v8i hi) {
+  Half64 h;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h.v[i] = widen8(lo[2 * i], lo[2 * i + 1]), h.v[4 + i] = widen8(hi[2 * i], hi[2 * i + 1]);
+  return h;
+}
+
+// 8 codes a lane of a 16 x 16 tile, 32 of K
+__device__ __forceinline__ v4f dot32(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8((int)a0, (int)a1), widen8((int)b0, (int)b1), c, 0, 0, 0);
+}
+
+struct Scales {
+  const float *sX, *sW;
+  int64_t Mp, blocks;  // length of a row of sX; blocks of 128 along K (a row of sW)
+};
+
+// ---- tiles: v_mfma_f32_32x32x64_f8f6f4, both operands through LDS
+//
+// A block owns BM x BN outputs, WM x WN waves with TI x TJ tiles of 32 x 32 each, and walks K in stages of 128 bytes,
+// which are the scales' blocks.  Operands, swizzle, barrier and the order of tiles are the integer product's (kernel 6);
+// what differs is the sum: a stage's two MFMAs of a tile start from zero, and their 16 results a lane go to the tile's
+// sums by 16 FMAs with the one factor sX[token] sW[channel block], for the weights are the A operand, so that a lane is
+// one token, and a wave's channels lie in one block of 128.  The FMAs of a tile run while the next tile's MFMAs do (two
+// sets of results in turn, the last tile's FMAs under the next stage's first MFMAs).  The tokens' scales of a stage come
+// with its operands, by 4-byte loads into LDS (a wave's 64 lanes fetch the BM / waves scales that are its share); the
+// weights' stand in a register, lane s for stage s of 64, and are read out by lane.
+template <int WM, int WN, int TI, int TJ, int KG, int ROOM, int OUT>
+__device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld, const uint8_t* __restrict__ qW,
+                                     const Scales& sc, const Out& o, int64_t m0, int64_t n0, float* __restrict__ part,
+                                     int64_t ldp, uint8_t* la0, uint8_t* la1, uint8_t* lb0, uint8_t* lb1, float* lx0,
+                                     float* lx1) {
+  constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN, NW = WM * WN;  // NW waves per K group
+  constexpr int AB = BM * 128, BB = BN * 128, NA = AB / 1024 / NW, NB = BB / 1024 / NW, NL = NA + NB + 1;
+  constexpr int XW = BM / NW;  // token scales that a wave fetches, into a slot of 64
+  static_assert(AB % (1024 * NW) == 0 && BB % (1024 * NW) == 0, "whole 1 KB loads per wave");
+  static_assert(XW <= 64 && (XW == 16 || XW == 32), "a share of the scales lies within a load and a tile's row block");
+  static_assert(32 * TJ <= 128 && (TI * TJ == 1 || TI % 2 == 0), "one channel block to a wave; operands in turn");
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6), wave = wid % NW, g = wid / NW;
+  const int l32 = lane & 31, kh = lane >> 5;
+  const int ch = (l32 & 19) | (l32 & 4) << 1 | (l32 & 8) >> 1;  // the channel that is row l32 of the A operand
+  const int wr = (wave / WN) * 32 * TI, wc = (wave % WN) * 32 * TJ;
+
+  const uint32_t rows = (uint32_t)(o.M - m0 < BM ? o.M - m0 : BM), cols = (uint32_t)(o.N - n0 < BN ? o.N - n0 : BN);
+  const uint32_t blocks = (cols + 15) / 16;  // channel blocks of 16 (the last one zero past N)
+  const int all = (int)sc.blocks, per = (all + (int)gridDim.y - 1) / (int)gridDim.y;
+  const int s0 = (int)blockIdx.y * per, nst = all - s0 < per ? all - s0 : per;  // this part's stages (>= 1)
+  const int turns = (nst + KG - 1) / KG;  // stages per K group: group g takes g, g + KG, ..
+  uint32_t va[NA], vb[NB];
+#pragma unroll
+  for (int q = 0; q < NB; ++q) {
+    const uint32_t f = wave + NW * q;  // fragment f & 1 of the stage of channel block f >> 1
+    vb[q] = (uint32_t)lane * 16 + (f >> 1) * 16 * (uint32_t)ld + (f & 1) * 1024;
+  }
+#pragma unroll
+  for (int q = 0; q < NA; ++q) {
+    const int row = (wave + NW * q) * 8 + (lane >> 3);
+    va[q] = (uint32_t)row * (uint32_t)ld + (uint32_t)(((lane & 7) ^ swz8(row)) * 16);
+  }
+  // the wave's share of the stage's token scales: one each for its first XW lanes, nothing for the others
+  const uint32_t vx = lane < XW && wave * XW + lane < (int)rows ? (uint32_t)(wave * XW + lane) * 4 : kNoStore;
+  // the weights' scales of this wave's channels (channels past N: the last block's; they are not stored)
+  const int64_t cb = (n0 + wc) / 128, cbs = (o.N + 127) / 128;
+  const float* sw_row = sc.sW + (cb < cbs ? cb : cbs - 1) * sc.blocks;
+  auto load_sw = [&](int k) {  // lane l: turn k + l
+    const int s = s0 + (k + lane) * KG + g;
+    return s < all ? sw_row[s] : 0.0f;
+  };
+  // past the end the buffers have no range: nothing is read and the LDS gets zeros
+  auto issue = [&](int k, uint8_t* a, uint8_t* b, float* x) {
+    const int s = k * KG + g;
+    const uint32_t on = s < nst ? 0xFFFFFFFFu : 0u;
+    const __amdgpu_buffer_rsrc_t rA = make_rsrc(qX + m0 * ld, (rows * (uint32_t)ld) & on);
+    const __amdgpu_buffer_rsrc_t rB = make_rsrc(qW + n0 * ld, (blocks * 16 * (uint32_t)ld) & on);
+    const __amdgpu_buffer_rsrc_t rX = make_rsrc(sc.sX + (int64_t)(s0 + (s < nst ? s : 0)) * sc.Mp + m0, (rows * 4) & on);
+#pragma unroll
+    for (int q = 0; q < NA; ++q) dma16(rA, a + g * AB + (wave + NW * q) * 1024, va[q], (uint32_t)(s0 + s) * 128);
+    // channel block c of the tile: 16 ld bytes from the one before it, 2 KB (two fragments) per stage
+#pragma unroll
+    for (int q = 0; q < NB; ++q)
+      dma16(rB, b + g * BB + (wave + NW * q) * 1024, vb[q], (uint32_t)(s0 + s) * 2048);
+    dma4(rX, x + (g * NW + wave) * 64, vx, 0);
+  };
+
+  // FINE: f16 products (see below); a tile's operands as f16 take 32 registers
+  constexpr bool FINE = OUT == 0;
+  constexpr int UNITS = TI * TJ, NT = UNITS > 4 ? 1 : 2;  // sets of results: registers hold one beside 8 tiles' sums
+  v16f acc[TI][TJ], T[NT];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = v16f{};
+#pragma unroll
+  for (int t = 0; t < NT; ++t) T[t] = v16f{};
+  struct Pair { v8i lo, hi; };  // a lane's 64 codes of a stage
+  Pair fa[2], fb[TJ];
+  float f[TI], held = 0.0f;  // the stage's factors; the factor of the results that still wait
+  // a lane's slots of its token row, 32 i rows on: slot 2 s + kh, XOR the row's swizzle, whose bit 2 changes with i
+  const int r0 = wr + l32;
+  uint32_t slot[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) slot[s] = (uint32_t)(g * AB + r0 * 128 + (((2 * s + kh) ^ swz8(r0)) * 16));
+  auto get_a = [&](const uint8_t* a, int i) {
+    v4i h[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) h[s] = *reinterpret_cast<const v4i*>(a + slot[s ^ (2 * (i & 1))] + 4096 * i);
+    return Pair{join8(h[0], h[1]), join8(h[2], h[3])};
+  };
+  const uint32_t at_b = (uint32_t)(g * BB + ((wc + ch) >> 4) * 2048 + kh * 256 + (ch & 15) * 16);
+  auto get_b = [&](const uint8_t* b, int j) {  // lane (channel % 16) + 16 (k16 % 4) of fragment k16 / 4, k16 = 2 s + kh
+    v4i h[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) h[s] = *reinterpret_cast<const v4i*>(b + at_b + 4096 * j + (s >> 1) * 1024 + (s & 1) * 512);
+    return Pair{join8(h[0], h[1]), join8(h[2], h[3])};
+  };
+  auto get_x = [&](const float* x, int i) {
+    const int r = r0 + 32 * i;
+    return x[(g * NW + r / XW) * 64 + r % XW];
+  };
+  auto add = [&](int u, const v16f& d, float w) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[u / TJ][u % TJ][e] = fmaf(d[e], w, acc[u / TJ][u % TJ][e]);
+  };
+  // par: 0 for even turns, 1 for odd ones: which set of results, and of operands where they number one, comes first
+  auto stage = [&](auto par, int k, float sw, uint8_t* ca, uint8_t* cb_, float* cx, const uint8_t* na, const uint8_t* nb) {
+    constexpr int P = decltype(par)::value, PT = P * UNITS & 1, PA = P * TI & 1;
+#pragma unroll
+    for (int i = 0; i < TI; ++i) f[i] = get_x(cx, i) * sw;
+    Half64 hb[FINE ? TJ : 1];
+    if constexpr (FINE) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) hb[j] = widen(fb[j].lo, fb[j].hi);
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      if (i + 1 < TI) {
+        fa[(i + 1 + PA) & 1] = get_a(ca, i + 1);
+      } else {
+        // every read of this stage's buffers is done or in registers: they may be filled again
+        wait_vm_lgkm0<0>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        issue(k + 2, ca, cb_, cx);
+        fa[(i + 1 + PA) & 1] = get_a(na, 0);
+      }
+      Half64 ha;
+      if constexpr (FINE) ha = widen(fa[(i + PA) & 1].lo, fa[(i + PA) & 1].hi);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const int u = i * TJ + j, pu = (u + UNITS - 1) % UNITS;
+        v16f t;
+        if constexpr (FINE) {
+          t = v16f{};
+#pragma unroll
+          for (int s = 0; s < 8; ++s) t = __builtin_amdgcn_mfma_f32_32x32x16_f16(hb[j].v[s], ha.v[s], t, 0, 0, 0);
+        } else {
+          t = mfma32(fb[j].lo, fa[(i + PA) & 1].lo, v16f{});
+          t = mfma32(fb[j].hi, fa[(i + PA) & 1].hi, t);
+        }
+        if (i + 1 == TI) fb[j] = get_b(nb, j);
+        if constexpr (NT == 1) {
+          add(u, t, f[i]);
+        } else {
+          T[(u + PT) & 1] = t;
+          add(pu, T[(u + 1 + PT) & 1], u == 0 ? held : f[pu / TJ]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    held = f[TI - 1];
+  };
+  issue(0, la0, lb0, lx0);
+  issue(1, la1, lb1, lx1);
+  wait_vm_lgkm0<NL>();
+  __builtin_amdgcn_s_barrier();
+  fa[0] = get_a(la0, 0);
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) fb[j] = get_b(lb0, j);
+  for (int kc = 0; kc < turns; kc += 64) {
+    const int swv = __float_as_int(load_sw(kc));
+    const int end = turns - kc < 64 ? turns : kc + 64;
+    auto sw_at = [&](int k) { return __int_as_float(__builtin_amdgcn_readlane(swv, k - kc)); };
+    int k = kc;
+    for (; k + 2 <= end; k += 2) {
+      stage(std::integral_constant<int, 0>{}, k, sw_at(k), la0, lb0, lx0, la1, lb1);
+      stage(std::integral_constant<int, 1>{}, k + 1, sw_at(k + 1), la1, lb1, lx1, la0, lb0);
+    }
+    if (k < end) stage(std::integral_constant<int, 0>{}, k, sw_at(k), la0, lb0, lx0, la1, lb1);
+  }
+  if constexpr (NT == 2) {  // the last tile's results still wait, in set (turns * UNITS - 1) % 2
+    const bool first = UNITS % 2 == 1 && turns % 2 == 1;
+    v16f d;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) d[e] = first ? T[0][e] : T[1][e];
+    add(UNITS - 1, d, held);
+  }
+  auto owner = [&](int u) { return KG > 1 ? u % KG : g; };  // the K group that finishes unit u of 8 registers
+  if constexpr (KG > 1) {
+    // the K groups' sums meet in LDS, in a fixed order: each unit of 8 registers is finished by one group
+    wait_vm_lgkm0<0>();
+    __builtin_amdgcn_s_barrier();  // the buffers are free
+    constexpr int REGS8 = TI * TJ * 2;
+    static_assert(KG * NW * REGS8 * 2048 <= 4 * ROOM && ROOM % 2048 == 0, "room for the sums");
+    auto slot = [&](int grp, int u, int q) {
+      const int at = ((grp * NW + wave) * REGS8 + u) * 2048 + q * 1024;
+      return reinterpret_cast<v4f*>(one_of(at / ROOM, la0, la1, lb0, lb1) + at % ROOM + lane * 16);
+    };
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int u = (i * TJ + j) * 2 + q / 2;
+          const v16f c = acc[i][j];
+          if (owner(u) != g) *slot(g, u, q & 1) = v4f{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+        }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        v16f c = acc[i][j];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int u = (i * TJ + j) * 2 + q / 2;
+          if (owner(u) != g) continue;
+#pragma unroll
+          for (int h = 1; h < KG; ++h) {
+            const v4f d = *slot((g + h) % KG, u, q & 1);
+            c[4 * q] += d[0], c[4 * q + 1] += d[1], c[4 * q + 2] += d[2], c[4 * q + 3] += d[3];
+          }
+        }
+        acc[i][j] = c;
+      }
+  }
+  const int64_t m1 = m0 + wr + l32, n1 = n0 + wc + 8 * kh;
+  if (KG == 4 && part) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int u = 0; u < 2 * TJ; ++u) {
+        if (owner(i * 2 * TJ + u) != g) continue;
+        const int64_t m = m1 + 32 * i, n = n1 + 16 * u;
+        const v16f& c = acc[i][u / 2];
+        const int r = 8 * (u & 1);
+        if (m < o.M && n < ldp) {
+          float4* q = reinterpret_cast<float4*>(part + ((int64_t)blockIdx.y * o.M + m) * ldp + n);
+          q[0] = make_float4(c[r], c[r + 1], c[r + 2], c[r + 3]);
+          q[1] = make_float4(c[r + 4], c[r + 5], c[r + 6], c[r + 7]);
+        }
+      }
+    wait_vm_lgkm0<0>();
+    return;
+  }
+  float bb[2 * TJ][8];
+#pragma unroll
+  for (int u = 0; u < 2 * TJ; ++u)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bb[u][e] = o.bias && n1 + 16 * u + e < o.N ? o.bias[n1 + 16 * u + e] : kNoBias;
+  auto finish = [&](auto whole) {  // whole: no bounds to check
+    constexpr bool WHOLE = decltype(whole)::value;
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int u = 0; u < 2 * TJ; ++u)
+        if (owner(i * 2 * TJ + u) == g) {
+          const int64_t m = m1 + 32 * i, n = n1 + 16 * u;
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = acc[i][u / 2][8 * (u & 1) + e] + bb[u][e];
+          if (WHOLE || m < o.M) store8<OUT, WHOLE>(o, m, n, y);
+        }
+  };
+  if (rows == BM && cols == BN) finish(std::true_type{});
+  else finish(std::false_type{});
+  wait_vm_lgkm0<0>();  // no load into LDS outlives the block, not the last ones without a range either
+}
+
+// HALVES: the tiles from `whole` on are cut into two of half as many rows, one block each
+template <int WM, int WN, int TI, int TJ, int KG, bool HALVES, int OUT>
+__global__ __launch_bounds__(64 * WM * WN * KG, TI * TJ == 1 ? 4 : 2) void k9_tiles(
+    const uint8_t* __restrict__ qX, int64_t ld, const uint8_t* __restrict__ qW, Scales sc, Out o, uint32_t tiles_m,
+    uint32_t tiles_n, uint32_t whole, float* __restrict__ part, int64_t ldp) {
+  constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN, ROOM = KG * (BM < BN ? BM : BN) * 128;
+  __shared__ __attribute__((aligned(1024))) uint8_t la0[KG * BM * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t la1[KG * BM * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t lb0[KG * BN * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t lb1[KG * BN * 128];
+  __shared__ __attribute__((aligned(16))) float lx0[KG * WM * WN * 64], lx1[KG * WM * WN * 64];
+  uint32_t m, n;
+  if (!HALVES || blockIdx.x < whole) {
+    const uint32_t xcd = blockIdx.x & 7, t8 = whole >> 3, r8 = whole & 7;
+    tile_at(xcd * t8 + (xcd < r8 ? xcd : r8) + (blockIdx.x >> 3), tiles_m, tiles_n, m, n);
+    tile<WM, WN, TI, TJ, KG, ROOM, OUT>(qX, ld, qW, sc, o, (int64_t)m * BM, (int64_t)n * BN, part, ldp, la0, la1, lb0,
+                                        lb1, lx0, lx1);
+  } else if constexpr (HALVES) {
+    const uint32_t h = blockIdx.x - whole;
+    tile_at(whole + (h >> 1), tiles_m, tiles_n, m, n);
+    const int64_t m0 = (int64_t)m * BM + (h & 1) * (BM / 2);
+    if (m0 < o.M)
+      tile<WM, WN, TI / 2, TJ, KG, ROOM, OUT>(qX, ld, qW, sc, o, m0, (int64_t)n * BN, part, ldp, la0, la1, lb0, lb1,
+                                              lx0, lx1);
+  }
+}
+
+// The second step of a K split: the parts' sums in order, then the bias.  A thread owns 8 columns.
+__global__ __launch_bounds__(256) void k9_join(const float* __restrict__ part, int parts, int64_t ldp, Out o) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = ldp / 8;
+  if (i >= o.M * per) return;
+  const int64_t m = i / per, n = i % per * 8;
+  float y[8] = {};
+  for (int p = 0; p < parts; ++p) {
+    const float4* q = reinterpret_cast<const float4*>(part + ((int64_t)p * o.M + m) * ldp + n);
+    const float4 u = q[0], v = q[1];
+    y[0] += u.x, y[1] += u.y, y[2] += u.z, y[3] += u.w, y[4] += v.x, y[5] += v.y, y[6] += v.z, y[7] += v.w;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] += o.bias && n + e < o.N ? o.bias[n + e] : kNoBias;
+  if (o.ydtype == 0) store8<0, false>(o, m, n, y);
+  else if (o.ydtype == 1) store8<1, false>(o, m, n, y);
+  else store8<2, false>(o, m, n, y);
+}
+
+// ---- few tokens: v_mfma_f32_16x16x128_f8f6f4, weights straight from memory
+//
+// Bound by the weights' read.  A block of 8 waves owns 16 channels (one channel block of the weights' fragment order)
+// and up to 16 NT tokens; its waves take the blocks of 128 along K in turn, U of them (2 KB each) in flight, and add
+// their sums in LDS, in the waves' order.  The weights are the A operand, the tokens the B operand: lane l holds token
+// l & 15 and 16 codes from k = 16 (l >> 4) of each half of the block.
+constexpr int FEW_NW = 8, FEW_U = 3;
+constexpr uint32_t kNoLoad = 0x7FFFFF00u;  // past the token rows' range (32 rows of at most 128 KB)
+
+template <int NT>
+struct FewSums {
+  float v[FEW_NW][NT][64][4];
+};
+
+template <int NT>
+__device__ __forceinline__ void few_finish(const v4f acc[NT], FewSums<NT>& sums, int wave, int lane, const Out& o,
+                                           int64_t n0) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) *reinterpret_cast<v4f*>(&sums.v[wave][t][lane][0]) = acc[t];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 256 * NT; i += 64 * FEW_NW) {
+    const int c = i & 15, m = i >> 4;  // consecutive threads: consecutive channels
+    const int64_t n = n0 + c;
+    if (m >= o.M || n >= o.N) continue;
+    float y = 0.0f;
+#pragma unroll
+    for (int w = 0; w < FEW_NW; ++w) y += sums.v[w][m >> 4][(m & 15) + 16 * (c >> 2)][c & 3];
+    if (o.bias) y += o.bias[n];
+    store1(o, m, n, y);
+  }
+}
+
+template <int NT>
+__global__ __launch_bounds__(64 * FEW_NW) void k9_few(const uint8_t* __restrict__ qX, int64_t ld,
+                                                      const uint8_t* __restrict__ qW, Scales sc, Out o) {
+  __shared__ FewSums<NT> sums;
+  constexpr int U = FEW_U;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const uint8_t* wl = qW + n0 * ld + lane * 16;
+  const __amdgpu_buffer_rsrc_t rX = make_rsrc(qX, (uint32_t)o.M * (uint32_t)ld);  // tokens past M read zeros
+  const uint32_t xoff = (uint32_t)(lane & 15) * (uint32_t)ld + (uint32_t)(lane >> 4) * 16;
+  const int nb = (int)sc.blocks;
+  const float* sw = sc.sW + n0 / 128 * nb;
+  const float* sx[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) sx[t] = sc.sX + ((lane & 15) + 16 * t < o.M ? (lane & 15) + 16 * t : 0);
+  v4f acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = v4f{};
+  for (int b0 = wave; b0 < nb; b0 += FEW_NW * U) {
+    uint4 w[U][2], x[U][NT][2];
+    float s[U][NT], c[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = b0 + u * FEW_NW, in = at < nb ? at : nb - 1;  // past the end: any weights, zero tokens, factor 0
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        w[u][h] = *reinterpret_cast<const uint4*>(wl + in * 2048 + h * 1024);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          x[u][t][h] = buf_load16(rX, at < nb ? (uint32_t)at * 128 + h * 64 + (uint32_t)(16 * t) * (uint32_t)ld + xoff : kNoLoad);
+      }
+      c[u] = at < nb ? sw[in] : 0.0f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s[u][t] = sx[t][in * sc.Mp];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        v4f d = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          d = dot32(w[u][h].x, w[u][h].y, x[u][t][h].x, x[u][t][h].y, d);
+          d = dot32(w[u][h].z, w[u][h].w, x[u][t][h].z, x[u][t][h].w, d);
+        }
+        const float k = b0 + u * FEW_NW < nb ? s[u][t] * c[u] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(d[e], k, acc[t][e]);
+      }
+  }
+  few_finish<NT>(acc, sums, wave, lane, o, n0);
+}
+
+// The whole layer for few tokens in one launch.  Blocks of 128 are quantized independently, so a wave quantizes each
+// block's codes in the registers that the MFMA takes them from: 32 values of its token a lane, the block's maximum by
+// two lane swaps.  Every workgroup repeats this for its 16 channels (X is small and in L2).
+template <typename T>
+__global__ __launch_bounds__(64 * FEW_NW) void k9_few_layer(const T* __restrict__ X, int64_t ldx, int K, int64_t ld,
+                                                            const uint8_t* __restrict__ qW, Scales sc, Out o) {
+  __shared__ FewSums<1> sums;
+  constexpr int U = FEW_U;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const uint8_t* wl = qW + n0 * ld + lane * 16;
+  const int nb = (int)sc.blocks, m = lane & 15, kl = 16 * (lane >> 4);
+  const float* sw = sc.sW + n0 / 128 * nb;
+  const T* x = X + (m < o.M ? m : 0) * ldx;
+  const bool on = m < o.M;
+  v4f acc[1] = {};
+  for (int b0 = wave; b0 < nb; b0 += FEW_NW * U) {
+    uint4 w[U][2];
+    Vec<T, 8> raw[U][4];
+    float c[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = b0 + u * FEW_NW, in = at < nb ? at : nb - 1;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[u][h] = *reinterpret_cast<const uint4*>(wl + in * 2048 + h * 1024);
+      c[u] = sw[in];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) raw[u][q] = load8(x, at * 128 + (q >> 1) * 64 + (q & 1) * 8 + kl, on ? K : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b0 + u * FEW_NW >= nb) break;
+      float v[32];
+      uint32_t a = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) valuev<T, 8>(raw[u][q], v + 8 * q);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) a = umax(a, abs_bits(v[e]));
+      {
+        const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+        a = umax(r[0], r[1]);
+        const auto h = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+        a = umax(h[0], h[1]);
+      }
+      float s, r;
+      block_scale(a, s, r);
+      uint32_t q[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = e4m3x4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3], r);
+      v4f d = {};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        d = dot32(w[u][h].x, w[u][h].y, q[4 * h], q[4 * h + 1], d);
+        d = dot32(w[u][h].z, w[u][h].w, q[4 * h + 2], q[4 * h + 3], d);
+      }
+      const float k = s * c[u];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[0][e] = fmaf(d[e], k, acc[0][e]);
+    }
+  }
+  few_finish<1>(acc, sums, wave, lane, o, n0);
+}
+
+template <int WM, int WN, int TI, int TJ, int KG, bool HALVES = false>
+void launch_tiles(const Fp8Plan& p, int64_t ld, const uint8_t* qX, const uint8_t* qW, const Scales& sc, const Out& o, float* part,
+                  hipStream_t st) {
+  constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN;
+  const uint32_t tm = (uint32_t)((o.M + BM - 1) / BM), tn = (uint32_t)((o.N + BN - 1) / BN);
+  const uint32_t whole = HALVES ? tm * tn - (uint32_t)p.halved : tm * tn;
+  const uint32_t blocks = whole + 2 * (tm * tn - whole);
+  const dim3 grid(blocks, (uint32_t)p.parts), block(64 * WM * WN * KG);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, qX, ld, qW, sc, o, tm, tn, whole, part, p.ldp); };
+  if constexpr (TI * TJ <= 4)  // (tiles of 256 have no registers for f16 operands)
+    if (o.ydtype == 0) return go(k9_tiles<WM, WN, TI, TJ, KG, HALVES, 0>);
+  if (o.ydtype == 1) go(k9_tiles<WM, WN, TI, TJ, KG, HALVES, 1>);
+  else go(k9_tiles<WM, WN, TI, TJ, KG, HALVES, 2>);
+}
+
+// ---- the choice of kernel
+
+// Tiles of 256 that a last round leaves for at most half of the CUs, after at least one whole round
+int64_t halved_tiles(int64_t M, int64_t N, int cus) {
+  const int64_t T = ((M + 255) / 256) * ((N + 255) / 256), rest = T % cus;
+  return T > cus && 2 * rest <= cus ? rest : 0;
+}
+
+struct Cost {
+  double us;
+  int tile, groups, parts;
+};
+
+Cost tiles_cost(int64_t M, int64_t N, int S, int cus, int tile, int groups) {
+  const double T = (double)((M + tile - 1) / tile) * (double)((N + tile - 1) / tile);
+  const double rounds = T / cus;
+  double us = 0.0;
+  auto by_line = [&](const double* a, const double* b, int most) {  // a[c - 1], b[c - 1]: c blocks on a CU
+    const double full = (double)(int64_t)(rounds / most), rest = rounds - full * most;
+    us = full * (a[most - 1] * S + b[most - 1]);
+    if (rest > 0) us += a[(int)(rest + 0.999999) - 1] * S + b[(int)(rest + 0.999999) - 1];
+  };
+  static const double a64[] = {0.315, 0.42, 0.42, 0.64}, b64[] = {0.0, 0.8, 0.8, 2.9}, a642[] = {0.26, 0.335},
+                      b642[] = {2.5, 3.6}, a644[] = {0.19}, b644[] = {3.6}, a128[] = {0.575, 0.725}, b128[] = {2.6, 5.6},
+                      a1282[] = {0.46}, b1282[] = {5.7};
+  if (tile == 64 && groups == 1) by_line(a64, b64, 4), us += 2.6;
+  else if (tile == 64 && groups == 2) by_line(a642, b642, 2), us += 1.0;
+  else if (tile == 64) by_line(a644, b644, 1), us += 0.9;
+  else if (tile == 128 && groups == 1) by_line(a128, b128, 2), us += 1.1;
+  else if (tile == 128) by_line(a1282, b1282, 1), us += 0.2;
+  else {
+    const double full = (double)(int64_t)rounds, rest = rounds - full;
+    const bool halved = full > 0 && rest <= 0.5;
+    us = full * (1.245 * S + 8.3) + (rest == 0 ? 0.0 : (halved ? 0.9 : rest <= 0.625 ? 1.08 : 1.245) * S + 8.3);
+  }
+  return Cost{us, tile, groups, 1};
+}
+
+}  // namespace
+
+Fp8Plan plan_fp8(int64_t M, int64_t K, int64_t N, bool fine) {
+  const int cus = device_cus();
+  const int64_t ld = i8_ld(K), ldp = (N + 7) / 8 * 8;
+  const int S = (int)(ld / 128);
+  Cost best{1e30, 64, 1, 1};
+  auto take = [&](const Cost& c) {
+    if (c.us < best.us) best = c;
+  };
+  take(tiles_cost(M, N, S, cus, 64, 1));
+  take(tiles_cost(M, N, S, cus, 128, 1));
+  if (!fine) take(tiles_cost(M, N, S, cus, 256, 1));
+  const int64_t T64 = ((M + 63) / 64) * ((N + 63) / 64), T128 = ((M + 127) / 128) * ((N + 127) / 128);
+  if (T128 <= cus) take(tiles_cost(M, N, S, cus, 128, 2));
+  if (T64 <= 2 * cus) take(tiles_cost(M, N, S, cus, 64, 2));
+  if (T64 <= cus) {
+    for (int parts = 1; parts <= 8 && parts * T64 <= cus && (parts == 1 || S / parts >= 8); parts *= 2) {
+      const int per = (S + parts - 1) / parts;
+      Cost c = tiles_cost(M, N, per, cus, 64, 4);
+      c.parts = (S + per - 1) / per;  // no empty part
+      if (c.parts > 1) c.us += 6.0 + 12.0 * (double)(M * ldp) * c.parts / 6e6;
+      take(c);
+    }
+  }
+  if (M <= 32) take(Cost{2.3 + (double)(N * ld) * 1e-6 * (0.075 + 0.006 * (double)M), 0, 1, 1});
+  Fp8Plan p{best.tile, best.groups, best.parts, ldp, 0, 0};
+  if (p.tile == 256) p.halved = halved_tiles(M, N, cus);
+  if (p.parts > 1) p.bytes = (size_t)p.parts * (size_t)M * (size_t)ldp * 4;
+  return p;
+}
+
+bool few_layer_fp8(int64_t M) { return M <= 16; }
+
+hipError_t launch_few_layer_fp8(int64_t M, int64_t K, int64_t N, const void* X, int xdtype, int64_t ldx,
+                                const uint8_t* qW, const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype,
+                                hipStream_t st) {
+  const Out o{nullptr, nullptr, bias, Y, ldy, M, N, ydtype};
+  const Scales sc{nullptr, sW, 0, fp8_blocks(K)};
+  const dim3 g((uint32_t)((N + 15) / 16)), b(64 * FEW_NW);
+  const int64_t ld = i8_ld(K);
+  if (xdtype == 0) hipLaunchKernelGGL(k9_few_layer<float>, g, b, 0, st, static_cast<const float*>(X), ldx, (int)K, ld, qW, sc, o);
+  else hipLaunchKernelGGL(k9_few_layer<uint16_t>, g, b, 0, st, static_cast<const uint16_t*>(X), ldx, (int)K, ld, qW, sc, o);
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm_fp8(int64_t M, int64_t K, int64_t N, const uint8_t* qX, const float* sX, const uint8_t* qW,
+                           const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype, void* ws,
+                           hipStream_t st) {
+  const int64_t ld = i8_ld(K);
+  const Out o{nullptr, nullptr, bias, Y, ldy, M, N, ydtype};
+  const Scales sc{sX, sW, fp8_pad(M), fp8_blocks(K)};
+  const Fp8Plan p = plan_fp8(M, K, N, ydtype == 0);
+  if (p.tile == 0) {
+    const dim3 g((uint32_t)((N + 15) / 16)), b(64 * FEW_NW);
+    if (M <= 16) hipLaunchKernelGGL(k9_few<1>, g, b, 0, st, qX, ld, qW, sc, o);
+    else hipLaunchKernelGGL(k9_few<2>, g, b, 0, st, qX, ld, qW, sc, o);
+    return hipGetLastError();
+  }
+  float* part = p.parts > 1 ? static_cast<float*>(ws) : nullptr;
+  if (p.tile == 256 && p.halved) launch_tiles<2, 4, 4, 2, 1, true>(p, ld, qX, qW, sc, o, part, st);
+  else if (p.tile == 256) launch_tiles<2, 4, 4, 2, 1>(p, ld, qX, qW, sc, o, part, st);
+  else if (p.tile == 128 && p.groups == 1) launch_tiles<2, 2, 2, 2, 1>(p, ld, qX, qW, sc, o, part, st);
+  else if (p.tile == 128) launch_tiles<2, 2, 2, 2, 2>(p, ld, qX, qW, sc, o, part, st);
+  else if (p.groups == 1) launch_tiles<2, 2, 1, 1, 1>(p, ld, qX, qW, sc, o, part, st);
+  else if (p.groups == 2) launch_tiles<2, 2, 1, 1, 2>(p, ld, qX, qW, sc, o, part, st);
+  else launch_tiles<2, 2, 1, 1, 4>(p, ld, qX, qW, sc, o, part, st);
+  if (p.parts > 1)
+    hipLaunchKernelGGL(k9_join, dim3((uint32_t)((M * (p.ldp / 8) + 255) / 256)), dim3(256), 0, st, part, p.parts, p.ldp, o);
+  return hipGetLastError();
+}
+
+}  // namespace svdq

@@ -104,6 +104,25 @@ hipError_t launch_few_layer(int64_t M, int64_t K, int64_t N, const void* X, int 
 hipError_t launch_w8a8(int64_t M, int64_t K, int64_t N, const int8_t* qX, const float* sX, const int8_t* qW,
                        const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype, void* ws, hipStream_t st);
 
+// ---- the block-scaled 8-bit floating point layer (rows of codes are i8_ld(K) bytes long, zeros past K; a scale for
+// each token and block of 128 along K, [blocks][M rounded up to 4], and for each 128 x 128 weights, [blocks of N][blocks of K])
+
+// E4M3 codes and scales of X [M][ldx] (xdtype 0 fp32, 1 bf16).
+hipError_t launch_quant_fp8(int64_t M, int64_t K, const void* X, int xdtype, int64_t ldx, uint8_t* qX, float* sX,
+                            hipStream_t st);
+// How the product runs on the current device; the fields are W8A8Plan's (partial sums in fp32).
+typedef W8A8Plan Fp8Plan;
+Fp8Plan plan_fp8(int64_t M, int64_t K, int64_t N, bool fine);  // fine: for fp32 outputs
+// Whether the layer runs as one launch for few tokens (which quantizes inside), and that launch.
+bool few_layer_fp8(int64_t M);
+hipError_t launch_few_layer_fp8(int64_t M, int64_t K, int64_t N, const void* X, int xdtype, int64_t ldx,
+                                const uint8_t* qW, const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype,
+                                hipStream_t st);
+// Y = the product + bias (bias may be NULL), qW in fragment order; ydtype 0 fp32, 1 bf16, 2 bf16 of GELU.
+hipError_t launch_gemm_fp8(int64_t M, int64_t K, int64_t N, const uint8_t* qX, const float* sX, const uint8_t* qW,
+                           const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype, void* ws,
+                           hipStream_t st);
+
 // ---- the channels-last group norm
 
 struct NormArgs {
@@ -127,5 +146,39 @@ struct NormPlan {
 NormPlan plan_norm(int64_t B, int64_t S, int C, int G);
 hipError_t launch_norm(const NormArgs& a, void* Y, int ydtype, int64_t bsy, int64_t ldy, void* ws, hipStream_t st);
 hipError_t launch_norm_quant(const NormArgs& a, const float* inv_s, int8_t* qX, float* sX, void* ws, hipStream_t st);
+
+// ---- the layer norm
+
+struct LayerNormArgs {
+  int64_t B, S;
+  int C;
+  bool one_plus;  // the weight is 1 + gamma
+  float eps;
+  const float *gamma, *beta;  // either may be NULL
+  int64_t gs;                 // from one image's gamma and beta to the next one's; 0: the same for all
+  const void* X;
+  int xdtype;  // 0 fp32, 1 bf16
+  int64_t bsx, ldx;
+};
+// y, or its E4M3 codes and scales (rows of i8_ld(C) bytes, [blocks][M rounded up to 4]); mean and rstd [B S] may be NULL.
+hipError_t launch_layer_norm(const LayerNormArgs& a, void* Y, int ydtype, int64_t bsy, int64_t ldy, float* mean,
+                             float* rstd, hipStream_t st);
+hipError_t launch_layer_norm_fp8(const LayerNormArgs& a, uint8_t* qX, float* sX, float* mean, float* rstd, hipStream_t st);
+// How the gradient runs: `runs` of `len` rows whose columns are summed, each in `parts` blocks of `per` rows with
+// `waves` waves, w to a row; bytes: workspace of the blocks' partial sums.
+struct LayerNormGradPlan {
+  int64_t runs, len, per;
+  uint32_t parts;
+  int w, waves;
+  size_t bytes;
+};
+LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, bool sums);
+// dX (X's type); dgamma and dbeta [C], or [B][C] where gs != 0, either may be NULL.
+hipError_t launch_layer_norm_grad(const LayerNormArgs& a, const void* dY, int ddtype, int64_t bsd, int64_t ldd,
+                                  const float* mean, const float* rstd, void* dX, int64_t bso, int64_t ldo,
+                                  float* dgamma, float* dbeta, void* ws, hipStream_t st);
+
+// The sums over no rows: zeros in dgamma and dbeta [runs][C] (either may be NULL).
+hipError_t launch_layer_norm_no_rows(int64_t runs, int C, float* dgamma, float* dbeta, hipStream_t st);
 
 }  // namespace svdq

@@ -49,6 +49,16 @@ class _GroupNorm(ctypes.Structure):
                 ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p)]
 
 
+class _Fp8Layer(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int64), ("N", ctypes.c_int64), ("qW", ctypes.c_void_p), ("sW", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
+
+
+class _LayerNorm(ctypes.Structure):
+    _fields_ = [("C", ctypes.c_int64), ("eps", ctypes.c_float), ("one_plus", ctypes.c_int32), ("gamma", ctypes.c_void_p),
+                ("beta", ctypes.c_void_p), ("image_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 EXPORTS = [
@@ -64,6 +74,10 @@ EXPORTS = [
     "svdq_int8_workspace_bytes", "svdq_gemm_w8a8", "svdq_linear_forward_int8", "svdq_group_norm_workspace_bytes",
     "svdq_group_norm_quantize_workspace_bytes", "svdq_group_norm", "svdq_group_norm_quantize_int8", "svdq_norm_linear_int8_workspace_bytes",
     "svdq_norm_linear_forward_int8", "svdq_debug_w8a8_plan", "svdq_debug_group_norm_plan",
+    "svdq_pack_weights_fp8", "svdq_transpose_weights_fp8", "svdq_quantize_act_fp8", "svdq_gemm_fp8_workspace_bytes",
+    "svdq_fp8_workspace_bytes", "svdq_gemm_fp8", "svdq_linear_forward_fp8", "svdq_layer_norm",
+    "svdq_layer_norm_quantize_fp8", "svdq_norm_linear_fp8_workspace_bytes", "svdq_norm_linear_forward_fp8",
+    "svdq_layer_norm_backward_workspace_bytes", "svdq_layer_norm_backward", "svdq_debug_fp8_plan",
 ]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -126,6 +140,20 @@ def lib():
         "svdq_debug_w8a8_plan": (I32, [P, I64, P]),
         "svdq_debug_group_norm_plan": (I32, [P, I64, I64, P]),
         "svdq_norm_linear_forward_int8": (I32, [P, P, I64, I64, P, I32, I64, I64, P, I64, I32, P, SZ, P]),
+        "svdq_pack_weights_fp8": (I32, [I64, I64, P, P, P]),
+        "svdq_transpose_weights_fp8": (I32, [I64, I64, P, P, P, P]),
+        "svdq_quantize_act_fp8": (I32, [I64, I64, P, I32, I64, P, P, P]),
+        "svdq_gemm_fp8_workspace_bytes": (SZ, [P, I64]),
+        "svdq_fp8_workspace_bytes": (SZ, [P, I64]),
+        "svdq_gemm_fp8": (I32, [P, I64, P, P, P, I64, I32, P, SZ, P]),
+        "svdq_linear_forward_fp8": (I32, [P, I64, P, I32, I64, P, I64, I32, P, SZ, P]),
+        "svdq_layer_norm": (I32, [P, I64, I64, P, I32, I64, I64, P, I32, I64, I64, P, P, P]),
+        "svdq_layer_norm_quantize_fp8": (I32, [P, I64, I64, P, I32, I64, I64, P, P, P, P, P]),
+        "svdq_norm_linear_fp8_workspace_bytes": (SZ, [P, P, I64, I64]),
+        "svdq_norm_linear_forward_fp8": (I32, [P, P, I64, I64, P, I32, I64, I64, P, I64, I32, P, P, P, SZ, P]),
+        "svdq_layer_norm_backward_workspace_bytes": (SZ, [P, I64, I64]),
+        "svdq_layer_norm_backward": (I32, [P, I64, I64, P, I32, I64, I64, P, I32, I64, I64, P, P, P, I64, I64, P, P, P, SZ, P]),
+        "svdq_debug_fp8_plan": (I32, [P, I64, I32, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -875,3 +903,299 @@ class GroupNorm:
                                                out.data_ptr(), _ld(B * S, out.stride(0), layer.N), ydtype,
                                                *_scratch(ws, dev), _raw_stream(X)))
         return out
+
+
+# ------------------------------------------------------------------ the block-scaled layer (E4M3) and the layer norm
+
+def fp8_blocks(n: int) -> int:
+    """Blocks of 128 that n values take."""
+    return (n + 127) // 128
+
+
+def fp8_scale_ld(M: int) -> int:
+    """Length of a row of activation scales: M rounded up to a multiple of 4."""
+    return (M + 3) // 4 * 4
+
+
+def pack_weights_fp8(W_bits: np.ndarray):
+    """svdq_pack_weights_fp8 on W (bf16 bits [K][N]): (qW uint8 [N][int8_ld(K)], sW fp32 [N / 128][K / 128] rounded up)."""
+    W = np.ascontiguousarray(W_bits, dtype=np.uint16)
+    if W.ndim != 2:
+        raise SvdqError("W must be [K][N]")
+    K, N = W.shape
+    qW, sW = np.empty((N, int8_ld(K)), np.uint8), np.empty((fp8_blocks(N), fp8_blocks(K)), np.float32)
+    _check(lib().svdq_pack_weights_fp8(K, N, _ptr(W), _ptr(qW), _ptr(sW)))
+    return qW, sW
+
+
+def transpose_weights_fp8(K: int, qW: np.ndarray, sW: np.ndarray):
+    """svdq_transpose_weights_fp8: (qWt uint8 [K][int8_ld(N)], sWt) of the layer that computes the input's gradient."""
+    qW, sW = np.ascontiguousarray(qW, dtype=np.uint8), np.ascontiguousarray(sW, dtype=np.float32)
+    if qW.ndim != 2 or qW.shape[1] != int8_ld(K) or sW.shape != (fp8_blocks(qW.shape[0]), fp8_blocks(K)):
+        raise SvdqError(f"qW must be [N][{int8_ld(K)}] and sW [N / 128][K / 128], rounded up")
+    N = qW.shape[0]
+    qt, st = np.empty((K, int8_ld(N)), np.uint8), np.empty((fp8_blocks(K), fp8_blocks(N)), np.float32)
+    _check(lib().svdq_transpose_weights_fp8(K, N, _ptr(qW), _ptr(sW), _ptr(qt), _ptr(st)))
+    return qt, st
+
+
+def _fp8_codes_out(torch, out, M: int, K: int, X, dev: int):
+    """The quantizers' two outputs, made, or the caller's checked: the library takes no sizes for them."""
+    qs, ss = (M, int8_ld(K)), (fp8_blocks(K), fp8_scale_ld(M))
+    if out is None:
+        return (torch.empty(qs, dtype=torch.float8_e4m3fn, device=X.device),
+                torch.empty(ss, dtype=torch.float32, device=X.device))
+    q, s = out
+    if q.shape != qs or q.dtype != torch.float8_e4m3fn or not q.is_contiguous() or s.shape != ss or \
+            s.dtype != torch.float32 or not s.is_contiguous():
+        raise SvdqError(f"out must be contiguous float8_e4m3fn {list(qs)} and contiguous fp32 {list(ss)}")
+    _on(q, dev, "out[0]")
+    _on(s, dev, "out[1]")
+    return out
+
+
+def quantize_act_fp8(X, out=None):
+    """svdq_quantize_act_fp8: (qX float8_e4m3fn [M][int8_ld(K)], sX fp32 [K / 128 rounded up][fp8_scale_ld(M)]) of
+    X [M][K]."""
+    torch, xt, _, L = _rt()
+    K = X.shape[-1] if X.dim() else 0
+    M = _check_rows(X, K, xt)
+    dev = _on_current_device(torch, X)
+    out = _fp8_codes_out(torch, out, M, K, X, dev)
+    _check(L.svdq_quantize_act_fp8(M, K, X.data_ptr(), xt[X.dtype], _ld(M, X.stride(0), K), out[0].data_ptr(),
+                                   out[1].data_ptr(), _raw_stream(X)))
+    return out
+
+
+class Fp8Linear:
+    """The block-scaled E4M3 layer on the GPU: codes qW [N][int8_ld(K)] (zeros past K; a float8_e4m3fn device tensor, or
+    uint8 numpy), sW fp32 [N / 128][K / 128] rounded up, bias fp32 [N] or None, as numpy arrays or device tensors.  The
+    codes are laid out once for the kernels (a copy); the other tensors are used as they are."""
+
+    def __init__(self, qW, sW, K: int, bias=None, device="cuda:0"):
+        torch = _torch()
+        if qW.ndim != 2 or qW.shape[1] != int8_ld(int(K)):
+            raise SvdqError(f"qW must be [N][{int8_ld(int(K))}]")
+        if isinstance(qW, np.ndarray):
+            if qW.dtype != np.uint8:
+                raise SvdqError("qW must be uint8 codes")
+            qW = torch.from_numpy(np.ascontiguousarray(qW)).to(device)
+        elif not qW.is_cuda or qW.dtype not in (torch.float8_e4m3fn, torch.uint8) or not qW.is_contiguous():
+            raise SvdqError("qW must be a contiguous float8_e4m3fn device tensor")
+        qW = qW.view(torch.uint8)
+        N = int(qW.shape[0])
+        if tuple(sW.shape) != (fp8_blocks(N), fp8_blocks(int(K))):
+            raise SvdqError(f"sW must be [{fp8_blocks(N)}][{fp8_blocks(int(K))}]")
+        # the layout of svdq_prepare_weights_int8, on the device
+        rows = torch.nn.functional.pad(qW, (0, 0, 0, -N % 16)) if N % 16 else qW
+        codes = rows.view(-1, 16, qW.shape[1] // 16, 16).permute(0, 2, 1, 3).contiguous().view(-1)
+        self._set(int(K), N, codes, _dev_tensor(sW, "sW", torch.float32, qW.device),
+                  _dev_tensor(bias, "bias", torch.float32, qW.device, N))
+
+    def _set(self, K, N, codes, sW, bias):
+        self.K, self.N, self.qW, self.sW, self.bias = K, N, codes, sW, bias
+        self.device = codes.device
+        self._dev = _one_device((codes, sW, bias), "layer")
+        self._ld, self._blocks = int8_ld(K), fp8_blocks(K)
+        self._c = _Fp8Layer(K, N, _dptr(codes), _dptr(sW), _dptr(bias))
+        self._ref = ctypes.addressof(self._c)
+
+    @classmethod
+    def from_weights(cls, W_bits: np.ndarray, bias=None, device="cuda:0"):
+        """Pack W (bf16 bits [K][N]) with svdq_pack_weights_fp8 and upload the result."""
+        return cls(*pack_weights_fp8(W_bits), W_bits.shape[0], bias, device)
+
+    def transposed(self) -> "Fp8Linear":
+        """The layer [N] -> [K] on the transposed weights: forward(dY) is the gradient of the input.  A copy of the codes,
+        laid out on the device."""
+        torch = _torch()
+        if self.N > 131072:
+            raise SvdqError("N must be <= 131072")
+        codes = self.qW.view(-1, self._ld // 16, 16, 16).permute(0, 2, 1, 3).reshape(-1, self._ld)[:self.N, :self.K]
+        t = torch.nn.functional.pad(codes.t(), (0, -self.N % 128)).contiguous()
+        return Fp8Linear(t, self.sW.t().contiguous(), self.N)
+
+    def quantize(self, X, out=None):
+        """(qX, sX) of X [M][K]: quantize_act_fp8."""
+        return quantize_act_fp8(X, out)
+
+    def _out(self, M, ydtype, out, X):
+        torch, _, ty, L = _rt()
+        if _on_current_device(torch, X) != self._dev:
+            raise SvdqError(f"the layer is on cuda:{self._dev}, the input on {X.device}")
+        if out is None:
+            return torch.empty((M, self.N), dtype=ty[ydtype], device=X.device)
+        if out.shape != (M, self.N) or out.dtype != ty[ydtype] or (self.N > 1 and out.stride(1) != 1):
+            raise SvdqError(f"out must be a [{M}][{self.N}] {ty[ydtype]} device tensor with unit column stride")
+        _on(out, self._dev, "out")
+        return out
+
+    def gemm(self, qX, sX, ydtype: int = F32, out=None, workspace=None):
+        """svdq_gemm_fp8: Y [M][N] from codes and scales as quantize_act_fp8 gives them."""
+        torch, _, _, L = _rt()
+        M = qX.shape[0]
+        if qX.dim() != 2 or qX.shape[1] != self._ld or qX.dtype != torch.float8_e4m3fn or sX.dtype != torch.float32 or \
+                sX.shape != (self._blocks, fp8_scale_ld(M)) or not qX.is_contiguous() or not sX.is_contiguous():
+            raise SvdqError(f"qX must be contiguous float8_e4m3fn [M][{self._ld}] and sX contiguous fp32 "
+                            f"[{self._blocks}][M rounded up to 4]")
+        out = self._out(M, ydtype, out, qX)
+        if sX.get_device() != self._dev:
+            _on(sX, self._dev, "sX")
+        n = L.svdq_gemm_fp8_workspace_bytes(self._ref, M)
+        ws = workspace if workspace is not None or n == 0 else torch.empty(n, dtype=torch.uint8, device=qX.device)
+        _check(L.svdq_gemm_fp8(self._ref, M, qX.data_ptr(), sX.data_ptr(), out.data_ptr(), _ld(M, out.stride(0), self.N),
+                               ydtype, *_scratch(ws, self._dev), _raw_stream(qX)))
+        return out
+
+    def plan(self, M: int, ydtype: int = F32):
+        """svdq_debug_fp8_plan: (tile, K groups, K parts, halved tiles) of the product of M rows."""
+        p = (ctypes.c_int32 * 4)()
+        _check(lib().svdq_debug_fp8_plan(self._ref, M, ydtype, p))
+        return tuple(p)
+
+    def workspace(self, M: int):
+        """Device scratch of forward() for M rows of X (None when unused)."""
+        torch, _, _, L = _rt()
+        n = L.svdq_fp8_workspace_bytes(self._ref, M)
+        return torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+
+    def forward(self, X, ydtype: int = F32, out=None, workspace=None):
+        """svdq_linear_forward_fp8: quantizer and product on X [M][K], fp32 or bf16, any row stride."""
+        torch, xt, _, L = _rt()
+        M = _check_rows(X, self.K, xt)
+        out = self._out(M, ydtype, out, X)
+        ws = workspace if workspace is not None else self.workspace(M)
+        _check(L.svdq_linear_forward_fp8(self._ref, M, X.data_ptr(), xt[X.dtype], _ld(M, X.stride(0), self.K),
+                                         out.data_ptr(), _ld(M, out.stride(0), self.N), ydtype,
+                                         *_scratch(ws, self._dev), _raw_stream(X)))
+        return out
+
+
+class LayerNorm:
+    """Layer norm over the last dimension of X [M][C] or [B][S][C], fp32 or bf16, unit channel stride.  gamma and beta
+    fp32 device tensors (or numpy), or None: [C] for all rows, or both [B][C], a row for each image (a modulated norm's
+    scale and shift; an [M][C] input is one image).  one_plus: the weight is 1 + gamma."""
+
+    def __init__(self, C: int, gamma=None, beta=None, eps: float = 1e-5, one_plus: bool = False, device="cuda:0"):
+        torch = _torch()
+        self.C, self.eps, self.one_plus = int(C), float(eps), bool(one_plus)
+        self.gamma = _dev_tensor(gamma, "gamma", torch.float32, device)
+        self.beta = _dev_tensor(beta, "beta", torch.float32, device)
+        shapes = {tuple(t.shape) for t in (self.gamma, self.beta) if t is not None}
+        if len(shapes) > 1 or any(len(s) not in (1, 2) or s[-1] != self.C for s in shapes):
+            raise SvdqError(f"gamma and beta must both be [{self.C}] or [B][{self.C}]")
+        shape = shapes.pop() if shapes else (self.C,)
+        self.images = shape[0] if len(shape) == 2 else 0  # images that have a weight of their own (0: one for all)
+        self._dev = _one_device((self.gamma, self.beta), "norm")
+        self._c = _LayerNorm(self.C, self.eps, int(self.one_plus), _dptr(self.gamma), _dptr(self.beta),
+                             self.C if self.images else 0)
+        self._ref = ctypes.addressof(self._c)
+
+    def _geometry(self, X, what="X"):
+        """(B, S, bs, ld): images, rows, image and row stride of X."""
+        _, xt, _, _ = _rt()
+        if X.dim() not in (2, 3) or X.shape[-1] != self.C or X.dtype not in xt or (self.C > 1 and X.stride(-1) != 1):
+            raise SvdqError(f"{what} must be an fp32 or bf16 [M][{self.C}] or [B][S][{self.C}] tensor with unit channel stride")
+        B = X.shape[0] if X.dim() == 3 else 1
+        S = X.shape[-2]
+        if self.images and self.images != B:
+            raise SvdqError(f"gamma and beta are of {self.images} images, {what} of {B}")
+        return B, S, X.stride(0) if X.dim() == 3 else 0, _ld(S, X.stride(-2), self.C)
+
+    def _place(self, torch, X) -> int:
+        dev = _on_current_device(torch, X)
+        if self._dev not in (-1, dev):
+            raise SvdqError(f"the norm's gamma and beta are on cuda:{self._dev}, the input on cuda:{dev}")
+        return dev
+
+    def alloc_stats(self, X):
+        """(mean, rstd): fp32 tensors for the rows of X, to be filled by a forward call and read by backward."""
+        torch, n = _torch(), X.numel() // self.C
+        return torch.empty(n, dtype=torch.float32, device=X.device), torch.empty(n, dtype=torch.float32, device=X.device)
+
+    @staticmethod
+    def _stats(torch, stats, n: int, dev: int):
+        if stats is None:
+            return None, None
+        for t, name in zip(stats, ("mean", "rstd")):
+            if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+                raise SvdqError(f"{name} must be a contiguous fp32 device tensor of {n} values")
+            _on(t, dev, name)
+        return stats[0].data_ptr(), stats[1].data_ptr()
+
+    def forward(self, X, ydtype: int = BF16, out=None, stats=None):
+        """svdq_layer_norm: the norm in X's shape, fp32 or bf16; stats = (mean, rstd) from alloc_stats are filled in."""
+        torch, xt, ty, L = _rt()
+        B, S, bs, ld = self._geometry(X)
+        dev = self._place(torch, X)
+        if ydtype not in (F32, BF16):
+            raise SvdqError("the norm's output is F32 or BF16")
+        if out is None:
+            out = torch.empty(X.shape, dtype=ty[ydtype], device=X.device)
+            bsy, ldy = S * self.C, self.C
+        elif out.shape != X.shape or out.dtype != ty[ydtype]:
+            raise SvdqError(f"out must be a {tuple(X.shape)} {ty[ydtype]} device tensor")
+        else:
+            _on(out, dev, "out")
+            _, _, bsy, ldy = self._geometry(out, "out")
+        _check(L.svdq_layer_norm(self._ref, B, S, X.data_ptr(), xt[X.dtype], bs, ld, out.data_ptr(), ydtype, bsy, ldy,
+                                 *self._stats(torch, stats, B * S, dev), _raw_stream(X)))
+        return out
+
+    def quantize(self, X, out=None, stats=None):
+        """svdq_layer_norm_quantize_fp8: (qX, sX) of the norm's rows, as quantize_act_fp8 gives them."""
+        torch, xt, _, L = _rt()
+        B, S, bs, ld = self._geometry(X)
+        dev = self._place(torch, X)
+        out = _fp8_codes_out(torch, out, B * S, self.C, X, dev)
+        _check(L.svdq_layer_norm_quantize_fp8(self._ref, B, S, X.data_ptr(), xt[X.dtype], bs, ld, out[0].data_ptr(),
+                                              out[1].data_ptr(), *self._stats(torch, stats, B * S, dev), _raw_stream(X)))
+        return out
+
+    def forward_linear(self, X, layer: Fp8Linear, ydtype: int = BF16, out=None, workspace=None, stats=None):
+        """svdq_norm_linear_forward_fp8: layer(norm(X)) [B S][N], the norm's output in E4M3 codes."""
+        torch, xt, _, L = _rt()
+        B, S, bs, ld = self._geometry(X)
+        out = layer._out(B * S, ydtype, out, X)
+        dev = self._place(torch, X)
+        ws = workspace
+        if ws is None:
+            n = L.svdq_norm_linear_fp8_workspace_bytes(self._ref, layer._ref, B, S)
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=X.device)
+        _check(L.svdq_norm_linear_forward_fp8(self._ref, layer._ref, B, S, X.data_ptr(), xt[X.dtype], bs, ld, out.data_ptr(),
+                                              _ld(B * S, out.stride(0), layer.N), ydtype,
+                                              *self._stats(torch, stats, B * S, dev), *_scratch(ws, dev), _raw_stream(X)))
+        return out
+
+    def backward(self, dY, X, stats, out=None, weights: bool = True, workspace=None):
+        """svdq_layer_norm_backward: (dX, dgamma, dbeta) from dY (fp32 or bf16, X's shape) and the forward's X and stats;
+        dX in X's type (or in `out`, which may be X or dY), dgamma and dbeta fp32 in gamma's shape, None without `weights`."""
+        torch, xt, _, L = _rt()
+        B, S, bs, ld = self._geometry(X)
+        if dY.shape != X.shape:
+            raise SvdqError(f"dY must be {tuple(X.shape)}")
+        _, _, bsd, ldd = self._geometry(dY, "dY")
+        dev = self._place(torch, X)
+        _on(dY, dev, "dY")
+        if stats is None:
+            raise SvdqError("stats must be the forward's (mean, rstd)")
+        if out is None:
+            out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+            bso, ldo = S * self.C, self.C
+        elif out.shape != X.shape or out.dtype != X.dtype:
+            raise SvdqError(f"out must be a {tuple(X.shape)} {X.dtype} device tensor")
+        else:
+            _on(out, dev, "out")
+            _, _, bso, ldo = self._geometry(out, "out")
+        dgamma = dbeta = ws = None
+        if weights:
+            shape = (B, self.C) if self.images else (self.C,)
+            dgamma = torch.empty(shape, dtype=torch.float32, device=X.device)
+            dbeta = torch.empty(shape, dtype=torch.float32, device=X.device)
+            n = 0 if workspace is not None else L.svdq_layer_norm_backward_workspace_bytes(self._ref, B, S)
+            ws = torch.empty(n, dtype=torch.uint8, device=X.device) if n else workspace
+        _check(L.svdq_layer_norm_backward(self._ref, B, S, dY.data_ptr(), xt[dY.dtype], bsd, ldd, X.data_ptr(),
+                                          xt[X.dtype], bs, ld, *self._stats(torch, stats, B * S, dev), out.data_ptr(), bso,
+                                          ldo, None if dgamma is None else dgamma.data_ptr(),
+                                          None if dbeta is None else dbeta.data_ptr(), *_scratch(ws, dev), _raw_stream(X)))
+        return out, dgamma, dbeta

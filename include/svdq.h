@@ -555,14 +555,130 @@ svdq_status svdq_norm_linear_forward_int8(const svdq_group_norm_desc* norm, cons
                                           int64_t ldy, int32_t ydtype, void* workspace, size_t ws_bytes,
                                           void* stream);
 
+/* ------------------- the block-scaled layer in 8-bit floating point (E4M3) ---- */
+/* For the layers that keep 8 bits without a smoothing statistic: a scale for each 128 values of a token and each
+ * 128 x 128 weights confines an outlier to its block, and E4M3 codes keep three bits of mantissa over 18 binades.
+ *   quantize  per row and block of 128 along K (the last one may be shorter): a = max(max |x|, 2^-96); s_X = a / 448;
+ *             r = 448 / a; q = E4M3(x r), to nearest, ties to the even code; every operation one fp32 rounding.  A
+ *             block that holds a NaN or an infinity gets a NaN scale and zero codes, so its row's outputs are NaN and
+ *             no other row's change.
+ *   product   Y[m][n] = sum over blocks b (s_X[b][m] s_W[n / 128][b]) D_b + bias[n], D_b = sum over k in b of qX[m][k]
+ *             qW[n][k] on the matrix core, all sums in fp32, then GELU if asked, rounded once to Y's type.  For fp32 Y
+ *             the codes are multiplied as fp16 (exact).  For bf16 Y above 32 rows they are multiplied as they are, at twice
+ *             the rate: the matrix core then aligns the products of 8 codes to the largest before it adds them, which
+ *             costs 1e-5 to 6e-5 of a sum, far below the rounding to bf16.
+ * E4M3 is the finite variant (bias 7, subnormals to 2^-9, largest 448, 0x7F and 0xFF NaN).  Rows of codes are
+ * svdq_int8_ld(K) = K rounded up to 128 bytes long; the bytes past K are zero.  Scales of activations are
+ * [ceil(K / 128)][Mp] fp32, Mp = M rounded up to 4 (what lies past M is neither written nor used); of weights
+ * [ceil(N / 128)][ceil(K / 128)].  X is fp32 or bf16 of any K >= 1 and any row stride; rows of X and Y may begin at any
+ * element's address.  Limits as for the integer layer (K <= 131072, M, ldx, ldy < 2^31, N <= 2^27 - 16, ceil(M / 64)
+ * ceil(N / 64) < 2^24). */
+typedef struct svdq_fp8_layer {
+  int64_t K, N;
+  const uint8_t* qW; /* codes in the kernel layout of svdq_prepare_weights_int8 (it moves bytes) */
+  const float* sW;   /* [ceil(N / 128)][ceil(K / 128)] fp32 */
+  const float* bias; /* [N] fp32, or NULL for none */
+} svdq_fp8_layer;    /* device pointers, 16-byte aligned, owned by the caller */
+
+/* Offline pack (host): per 128 x 128 weights s_W = fp32(max |W| / 448), q = E4M3(W / s_W) (quotient in fp64, zeros where
+ * s_W is 0).  W host bf16 [K][N]; outputs (host): qW_out [N][svdq_int8_ld(K)], zero past K; sW_out.  EINVAL on NULL or
+ * sizes; EUNSUPPORTED on K > 131072; ENUMERIC on non-finite W. */
+svdq_status svdq_pack_weights_fp8(int64_t K, int64_t N, const uint16_t* W, uint8_t* qW_out, float* sW_out);
+
+/* The transposed weights (host), whose layer (K and N exchanged) computes the gradient of the input from the gradient
+ * of the output: dX = Q(dY) W.  Codes and scales are those of the layer itself, 128 x 128 blocks being the same either
+ * way.  qWt_out [K][svdq_int8_ld(N)], sWt_out [ceil(K / 128)][ceil(N / 128)].  EUNSUPPORTED on N > 131072. */
+svdq_status svdq_transpose_weights_fp8(int64_t K, int64_t N, const uint8_t* qW, const float* sW, uint8_t* qWt_out,
+                                       float* sWt_out);
+
+/* The quantizer alone: X [M][ldx] (device, svdq_dtype xdtype) -> qX [M][svdq_int8_ld(K)], sX (both 16-byte aligned).
+ * M == 0 is a no-op.  EINVAL on NULL, misalignment, sizes; EUNSUPPORTED on another xdtype or a limit; EHIP. */
+svdq_status svdq_quantize_act_fp8(int64_t M, int64_t K, const void* X, int32_t xdtype, int64_t ldx, uint8_t* qX,
+                                  float* sX, void* stream);
+
+/* Bytes of device workspace svdq_gemm_fp8 / svdq_linear_forward_fp8 need for M rows on the current device (0: none, or
+ * bad arguments). */
+size_t svdq_gemm_fp8_workspace_bytes(const svdq_fp8_layer* layer, int64_t M);
+size_t svdq_fp8_workspace_bytes(const svdq_fp8_layer* layer, int64_t M);
+
+/* The product alone on codes and scales as svdq_quantize_act_fp8 writes them.  Y device [M][ldy], svdq_dtype ydtype,
+ * overwritten; columns >= N are not touched.  workspace: >= svdq_gemm_fp8_workspace_bytes, 256-byte aligned (NULL where
+ * that is 0).  A NaN code makes its outputs NaN; the bytes past K have to be zero or other finite codes.  M == 0 is a
+ * no-op.  Deterministic; the order of the fp32 additions depends on the sizes and the device.  Errors as above. */
+svdq_status svdq_gemm_fp8(const svdq_fp8_layer* layer, int64_t M, const uint8_t* qX, const float* sX, void* Y,
+                          int64_t ldy, int32_t ydtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* The layer: quantizer, then product, on `stream`, codes and scales in `workspace` (>= svdq_fp8_workspace_bytes,
+ * 256-byte aligned, contents on entry irrelevant); for few tokens one launch that quantizes inside and needs no
+ * workspace.  Y must not overlap X (for few tokens every block reads all of X). */
+svdq_status svdq_linear_forward_fp8(const svdq_fp8_layer* layer, int64_t M, const void* X, int32_t xdtype, int64_t ldx,
+                                    void* Y, int64_t ldy, int32_t ydtype, void* workspace, size_t ws_bytes,
+                                    void* stream);
+
+/* ------------------------------------------ layer norm and its gradient ---- */
+/* X [B][S][C] (image, row, channel; row stride ldx, image stride bsx, in elements).  Per row: mean and biased variance
+ * in fp32 (sums of differences to a first mean, joined pairwise: no cancellation however far the mean lies from zero); z
+ * = (x - mean) rstd, rstd = 1 / sqrt(var + eps); y = z w + beta with w = gamma, or 1 + gamma where one_plus is 1 (the
+ * scale and shift of a modulated norm).  gamma and beta [C] serve all rows (image_stride 0), or image b those at
+ * b image_stride.  A NaN or an infinity makes its row's outputs NaN and no other row's; sums of values and of squared
+ * differences have to stay within fp32.  Images of X (and dY) are apart, or one and the same (stride 0).  Limits: C <=
+ * 16384, B <= 65535, B S < 2^31, row strides < 2^31, image strides < 2^46 (EUNSUPPORTED beyond). */
+typedef struct svdq_layer_norm_desc {
+  int64_t C;
+  float eps;            /* > 0 */
+  int32_t one_plus;     /* 0 or 1 */
+  const float* gamma;   /* device fp32, or NULL for a weight of 1 (whatever one_plus says) */
+  const float* beta;    /* device fp32, or NULL for 0 */
+  int64_t image_stride; /* elements from one image's gamma (and beta) to the next one's, >= C; 0: the same for all */
+} svdq_layer_norm_desc;
+
+/* Y [B][S][C] (row stride ldy, image stride bsy), SVDQ_F32 or SVDQ_BF16; X fp32 or bf16.  Y may be X itself (same type
+ * and strides, images apart); otherwise they must not overlap.  mean, rstd: device fp32 [B S], or NULL; what the gradient
+ * takes.  One launch, no workspace.  B == 0 or S == 0 is a no-op.  EINVAL on NULL, misalignment, sizes; EUNSUPPORTED on
+ * another type or a limit; EHIP on launch error. */
+svdq_status svdq_layer_norm(const svdq_layer_norm_desc* norm, int64_t B, int64_t S, const void* X, int32_t xdtype,
+                            int64_t bsx, int64_t ldx, void* Y, int32_t ydtype, int64_t bsy, int64_t ldy, float* mean,
+                            float* rstd, void* stream);
+
+/* The norm leaving as E4M3 codes: y as above kept in fp32, then the quantizer of the block-scaled layer on each row:
+ * qX [B S][svdq_int8_ld(C)], sX [ceil(C / 128)][B S rounded up to 4], both 16-byte aligned. */
+svdq_status svdq_layer_norm_quantize_fp8(const svdq_layer_norm_desc* norm, int64_t B, int64_t S, const void* X,
+                                         int32_t xdtype, int64_t bsx, int64_t ldx, uint8_t* qX, float* sX, float* mean,
+                                         float* rstd, void* stream);
+
+/* The norm, its codes and the block-scaled layer on them: Y [B S][ldy] = layer(norm(X)), layer->K == norm->C.  Bit for
+ * bit the two calls svdq_layer_norm_quantize_fp8 and svdq_gemm_fp8.  workspace >= svdq_norm_linear_fp8_workspace_bytes,
+ * 256-byte aligned. */
+size_t svdq_norm_linear_fp8_workspace_bytes(const svdq_layer_norm_desc* norm, const svdq_fp8_layer* layer, int64_t B,
+                                            int64_t S);
+svdq_status svdq_norm_linear_forward_fp8(const svdq_layer_norm_desc* norm, const svdq_fp8_layer* layer, int64_t B,
+                                         int64_t S, const void* X, int32_t xdtype, int64_t bsx, int64_t ldx, void* Y,
+                                         int64_t ldy, int32_t ydtype, float* mean, float* rstd, void* workspace,
+                                         size_t ws_bytes, void* stream);
+
+/* The gradient, from dY (fp32 or bf16) and the forward's X, mean and rstd: with g = dY w, dX = rstd (g - sum(g) / C - z
+ * sum(g z) / C), in X's type; dgamma = sum over rows of dY z, dbeta = sum over rows of dY, device fp32, contiguous, [C]
+ * where image_stride is 0, else [B][C], an image's sums each (either or both may be NULL; sums over no rows are zeros).
+ * All sums in fp32 in a fixed order (no atomics).  dX may be X or dY (same type and strides, images apart); otherwise they
+ * must not overlap.  workspace: >= svdq_layer_norm_backward_workspace_bytes, 256-byte aligned (NULL where that is 0, or
+ * neither sum is asked for). */
+size_t svdq_layer_norm_backward_workspace_bytes(const svdq_layer_norm_desc* norm, int64_t B, int64_t S);
+svdq_status svdq_layer_norm_backward(const svdq_layer_norm_desc* norm, int64_t B, int64_t S, const void* dY,
+                                     int32_t dydtype, int64_t bsdy, int64_t lddy, const void* X, int32_t xdtype,
+                                     int64_t bsx, int64_t ldx, const float* mean, const float* rstd, void* dX,
+                                     int64_t bsdx, int64_t lddx, float* dgamma, float* dbeta, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
 /* Diagnostics: which kernels a call runs on the current device, so that a test can ask for the one it means.
  *   svdq_debug_w8a8_plan: plan = {tile (64, 128 or 256; 0: the kernel for few tokens), K groups, K parts, tiles of 256
  *     that run as halves}; the product of M rows, alone or in a layer.
  *   svdq_debug_group_norm_plan: plan = {1 where one launch serves the norm, 1 where the blocks' statistics are joined by
  *     a launch of their own, statistics blocks and output blocks per image}.
+ *   svdq_debug_fp8_plan: as svdq_debug_w8a8_plan, for the block-scaled product into a svdq_dtype.
  * EINVAL / EUNSUPPORTED as the calls themselves; host only, nothing is launched. */
 svdq_status svdq_debug_w8a8_plan(const svdq_int8_layer* layer, int64_t M, int32_t plan[4]);
 svdq_status svdq_debug_group_norm_plan(const svdq_group_norm_desc* norm, int64_t B, int64_t S, int32_t plan[4]);
+svdq_status svdq_debug_fp8_plan(const svdq_fp8_layer* layer, int64_t M, int32_t ydtype, int32_t plan[4]);
 
 /* Diagnostic: the exact integer group sums I[g][m][n] = sum_{k in group g} qX[m][k]
  * qW[n][k] (INT4 only; the review's section 3 product Q_X Q_W, taken per group) for the
