@@ -24,22 +24,22 @@ __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, float* lds, uint3
 __device__ __forceinline__ v8i join8(v4i a, v4i b) { return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
 
 // unscaled E4M3 x E4M3 (both scale operands the constant 0 choose the form without scales)
-__device__ __forceinline__ v16f mfma32(v8i a, v8i b, v16f c) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+__device__ __forceinline__ v4f mfma16(v8i a, v8i b, v4f c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 
 // Codes as f16 (exact: E4M3 has 4 significant bits and binary exponents from -9 to 8)
 typedef _Float16 v8hf __attribute__((ext_vector_type(8)));
-struct Half64 { v8hf v[8]; };
+struct Half32 { v8hf v[4]; };
 __device__ __forceinline__ v8hf widen8(int a, int b) {
   const h2 p = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false), q = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
   const h2 r = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false), t = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
   return v8hf{p.x, p.y, q.x, q.y, r.x, r.y, t.x, t.y};
 }
-__device__ __forceinline__ Half64 widen(v8i lo, v8i hi) {
-  Half64 h;
+__device__ __forceinline__ Half32 widen(v8i c) {
+  Half32 h;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h.v[i] = widen8(lo[2 * i], lo[2 * i + 1]), h.v[4 + i] = widen8(hi[2 * i], hi[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) h.v[i] = widen8(c[2 * i], c[2 * i + 1]);
   return h;
 }
 
@@ -47,6 +47,11 @@ __device__ __forceinline__ Half64 widen(v8i lo, v8i hi) {
 __device__ __forceinline__ v4f dot32(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8((int)a0, (int)a1), widen8((int)b0, (int)b1), c, 0, 0, 0);
 }
+
+// The swizzle of a token row's eight 16-byte slots.  An operand's 16 lanes of one slot and 16 of the next are read 4 by 4
+// in turn ({0-3, 12-15} of one with {4-11} of the other): so the 8 even rows (and the 8 odd ones) of each such 16
+// fall in 8 different slots.  (Kernel 6's, made for 32 rows of one slot, costs 2 accesses in each here.)
+__device__ __forceinline__ int swz16(int row) { return (row & 6) | (row >> 2 & 1); }
 
 struct Scales {
   const float *sX, *sW;
@@ -71,13 +76,14 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld,
   constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN, NW = WM * WN;  // NW waves per K group
   constexpr int AB = BM * 128, BB = BN * 128, NA = AB / 1024 / NW, NB = BB / 1024 / NW, NL = NA + NB + 1;
   constexpr int XW = BM / NW;  // token scales that a wave fetches, into a slot of 64
+  constexpr int IA = 2 * TI, JB = 2 * TJ;  // a wave's operands: groups of 16 tokens, of 16 channels
   static_assert(AB % (1024 * NW) == 0 && BB % (1024 * NW) == 0, "whole 1 KB loads per wave");
-  static_assert(XW <= 64 && (XW == 16 || XW == 32), "a share of the scales lies within a load and a tile's row block");
-  static_assert(32 * TJ <= 128 && (TI * TJ == 1 || TI % 2 == 0), "one channel block to a wave; operands in turn");
+  static_assert(XW == 16 || XW == 32, "a share of the scales is one load, and holds whole groups of 16");
+  static_assert(32 * TJ <= 128, "one block of channels to a wave");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6), wave = wid % NW, g = wid / NW;
-  const int l32 = lane & 31, kh = lane >> 5;
-  const int ch = (l32 & 19) | (l32 & 4) << 1 | (l32 & 8) >> 1;  // the channel that is row l32 of the A operand
+  const int l16 = lane & 15, l4 = lane >> 4;
+  const int ch = (l16 >> 2) * 8 + (l16 & 3);  // the channel of 32 that is row l16 of an even operand; 4 on: of the odd one
   const int wr = (wave / WN) * 32 * TI, wc = (wave % WN) * 32 * TJ;
 
   const uint32_t rows = (uint32_t)(o.M - m0 < BM ? o.M - m0 : BM), cols = (uint32_t)(o.N - n0 < BN ? o.N - n0 : BN);
@@ -88,13 +94,14 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld,
   uint32_t va[NA], vb[NB];
 #pragma unroll
   for (int q = 0; q < NB; ++q) {
-    const uint32_t f = wave + NW * q;  // fragment f & 1 of the stage of channel block f >> 1
-    vb[q] = (uint32_t)lane * 16 + (f >> 1) * 16 * (uint32_t)ld + (f & 1) * 1024;
+    // fragment f & 1 of the stage of channel block f >> 1; odd blocks with their channels' fours exchanged (see get_b)
+    const uint32_t f = wave + NW * q;
+    vb[q] = (uint32_t)(lane ^ (f >> 1 & 1) * 4) * 16 + (f >> 1) * 16 * (uint32_t)ld + (f & 1) * 1024;
   }
 #pragma unroll
   for (int q = 0; q < NA; ++q) {
     const int row = (wave + NW * q) * 8 + (lane >> 3);
-    va[q] = (uint32_t)row * (uint32_t)ld + (uint32_t)(((lane & 7) ^ swz8(row)) * 16);
+    va[q] = (uint32_t)row * (uint32_t)ld + (uint32_t)(((lane & 7) ^ swz16(row)) * 16);
   }
   // the wave's share of the stage's token scales: one each for its first XW lanes, nothing for the others
   const uint32_t vx = lane < XW && wave * XW + lane < (int)rows ? (uint32_t)(wave * XW + lane) * 4 : kNoStore;
@@ -105,209 +112,193 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld,
     const int s = s0 + (k + lane) * KG + g;
     return s < all ? sw_row[s] : 0.0f;
   };
-  // past the end the buffers have no range: nothing is read and the LDS gets zeros
-  auto issue = [&](int k, uint8_t* a, uint8_t* b, float* x) {
+  // load n of stage k; past the end the buffers have no range: nothing is read and the LDS gets zeros
+  auto issue = [&](int n, int k, uint8_t* a, uint8_t* b, float* x) {
     const int s = k * KG + g;
     const uint32_t on = s < nst ? 0xFFFFFFFFu : 0u;
-    const __amdgpu_buffer_rsrc_t rA = make_rsrc(qX + m0 * ld, (rows * (uint32_t)ld) & on);
-    const __amdgpu_buffer_rsrc_t rB = make_rsrc(qW + n0 * ld, (blocks * 16 * (uint32_t)ld) & on);
-    const __amdgpu_buffer_rsrc_t rX = make_rsrc(sc.sX + (int64_t)(s0 + (s < nst ? s : 0)) * sc.Mp + m0, (rows * 4) & on);
-#pragma unroll
-    for (int q = 0; q < NA; ++q) dma16(rA, a + g * AB + (wave + NW * q) * 1024, va[q], (uint32_t)(s0 + s) * 128);
-    // channel block c of the tile: 16 ld bytes from the one before it, 2 KB (two fragments) per stage
-#pragma unroll
-    for (int q = 0; q < NB; ++q)
-      dma16(rB, b + g * BB + (wave + NW * q) * 1024, vb[q], (uint32_t)(s0 + s) * 2048);
-    dma4(rX, x + (g * NW + wave) * 64, vx, 0);
+    if (n < NA) {
+      dma16(make_rsrc(qX + m0 * ld, (rows * (uint32_t)ld) & on), a + g * AB + (wave + NW * n) * 1024, va[n], (uint32_t)(s0 + s) * 128);
+    } else if (n < NA + NB) {  // channel block c of the tile: 16 ld bytes from the one before it, 2 KB (two fragments) per stage
+      dma16(make_rsrc(qW + n0 * ld, (blocks * 16 * (uint32_t)ld) & on), b + g * BB + (wave + NW * (n - NA)) * 1024, vb[n - NA],
+            (uint32_t)(s0 + s) * 2048);
+    } else {
+      dma4(make_rsrc(sc.sX + (int64_t)(s0 + (s < nst ? s : 0)) * sc.Mp + m0, (rows * 4) & on), x + (g * NW + wave) * 64, vx, 0);
+    }
   };
 
-  // FINE: f16 products (see below); a tile's operands as f16 take 32 registers
   constexpr bool FINE = OUT == 0;
-  constexpr int UNITS = TI * TJ, NT = UNITS > 4 ? 1 : 2;  // sets of results: registers hold one beside 8 tiles' sums
-  v16f acc[TI][TJ], T[NT];
+  // Token operands in registers; how many groups ahead they are read; a stage's loads go out over STEPS groups, PER in each,
+  // the first AHEAD of them behind the barrier, the others in the next stage
+  constexpr int RING = IA > 2 ? 4 : 2, AHEAD = IA > 4 ? 3 : IA > 2 ? 2 : 1, STEPS = IA > 4 ? 5 : IA > 2 ? 3 : 1;
+  constexpr int PER = (NL + STEPS - 1) / STEPS, FIRST = PER * AHEAD < NL ? PER * AHEAD : NL;
+  v4f acc[IA][JB], T[JB];
 #pragma unroll
-  for (int i = 0; i < TI; ++i)
+  for (int j = 0; j < JB; ++j) {
+    T[j] = v4f{};
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) acc[i][j] = v16f{};
+    for (int i = 0; i < IA; ++i) acc[i][j] = v4f{};
+  }
+  v8i fa[RING], fb[JB];  // a lane's 32 codes of a stage
+  float fx[RING];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) T[t] = v16f{};
-  struct Pair { v8i lo, hi; };  // a lane's 64 codes of a stage
-  Pair fa[2], fb[TJ];
-  float f[TI], held = 0.0f;  // the stage's factors; the factor of the results that still wait
-  // a lane's slots of its token row, 32 i rows on: slot 2 s + kh, XOR the row's swizzle, whose bit 2 changes with i
-  const int r0 = wr + l32;
-  uint32_t slot[4];
-#pragma unroll
-  for (int s = 0; s < 4; ++s) slot[s] = (uint32_t)(g * AB + r0 * 128 + (((2 * s + kh) ^ swz8(r0)) * 16));
+  for (int i = 0; i < RING; ++i) fx[i] = 0.0f;
+  const int r0 = wr + l16;
+  const uint32_t at_a = (uint32_t)(g * AB + r0 * 128 + ((l4 ^ swz16(r0)) * 16));  // and the slot 4 on: bit 6
   auto get_a = [&](const uint8_t* a, int i) {
-    v4i h[4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) h[s] = *reinterpret_cast<const v4i*>(a + slot[s ^ (2 * (i & 1))] + 4096 * i);
-    return Pair{join8(h[0], h[1]), join8(h[2], h[3])};
+    return join8(*reinterpret_cast<const v4i*>(a + at_a + 2048 * i), *reinterpret_cast<const v4i*>(a + (at_a ^ 64) + 2048 * i));
   };
-  const uint32_t at_b = (uint32_t)(g * BB + ((wc + ch) >> 4) * 2048 + kh * 256 + (ch & 15) * 16);
-  auto get_b = [&](const uint8_t* b, int j) {  // lane (channel % 16) + 16 (k16 % 4) of fragment k16 / 4, k16 = 2 s + kh
-    v4i h[4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) h[s] = *reinterpret_cast<const v4i*>(b + at_b + 4096 * j + (s >> 1) * 1024 + (s & 1) * 512);
-    return Pair{join8(h[0], h[1]), join8(h[2], h[3])};
+  // An operand's 16 rows are channels of two blocks of 16: with the fours of the odd one exchanged they lie in 16 different
+  // slots (without: two in each, 16 M cycles of bank conflicts in 70 M)
+  const uint32_t at_b = (uint32_t)(g * BB + ((wc + ch) >> 4) * 2048 + l4 * 256 + ((ch & 15) ^ (ch >> 2 & 4)) * 16);
+  auto get_b = [&](const uint8_t* b, int j) {
+    const uint8_t* q = b + (at_b ^ 64 * (j & 1)) + 4096 * (j >> 1);
+    return join8(*reinterpret_cast<const v4i*>(q), *reinterpret_cast<const v4i*>(q + 1024));
   };
   auto get_x = [&](const float* x, int i) {
-    const int r = r0 + 32 * i;
+    const int r = r0 + 16 * i;
     return x[(g * NW + r / XW) * 64 + r % XW];
   };
-  auto add = [&](int u, const v16f& d, float w) {
+  auto add = [&](int i, int j, float w) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[u / TJ][u % TJ][e] = fmaf(d[e], w, acc[u / TJ][u % TJ][e]);
+    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(T[j][e], w, acc[i][j][e]);
   };
-  // par: 0 for even turns, 1 for odd ones: which set of results, and of operands where they number one, comes first
-  auto stage = [&](auto par, int k, float sw, uint8_t* ca, uint8_t* cb_, float* cx, const uint8_t* na, const uint8_t* nb) {
-    constexpr int P = decltype(par)::value, PT = P * UNITS & 1, PA = P * TI & 1;
-#pragma unroll
-    for (int i = 0; i < TI; ++i) f[i] = get_x(cx, i) * sw;
-    Half64 hb[FINE ? TJ : 1];
+  auto stage = [&](int k, float sw, uint8_t* ca, uint8_t* cb_, float* cx, uint8_t* na, uint8_t* nb, float* nx) {
+    Half32 hb[FINE ? JB : 1];
     if constexpr (FINE) {
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) hb[j] = widen(fb[j].lo, fb[j].hi);
+      for (int j = 0; j < JB; ++j) hb[j] = widen(fb[j]);
     }
 #pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      if (i + 1 < TI) {
-        fa[(i + 1 + PA) & 1] = get_a(ca, i + 1);
-      } else {
+    for (int i = 0; i < IA; ++i) {
+      const float held = fx[(i + RING - 1) % RING];  // the factor of the group before this one
+      if (i == IA - AHEAD) {
         // every read of this stage's buffers is done or in registers: they may be filled again
         wait_vm_lgkm0<0>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        issue(k + 2, ca, cb_, cx);
-        fa[(i + 1 + PA) & 1] = get_a(na, 0);
       }
-      Half64 ha;
-      if constexpr (FINE) ha = widen(fa[(i + PA) & 1].lo, fa[(i + PA) & 1].hi);
+      const int part = (i + AHEAD) % IA;  // this group's share of the loads
+      const int from = part * PER, to = part < STEPS ? (from + PER < NL ? from + PER : NL) : from;
+      const int ahead = (i + AHEAD) % IA;
+      fa[(i + AHEAD) % RING] = get_a(i + AHEAD < IA ? ca : na, ahead);
+      fx[(i + AHEAD) % RING] = get_x(i + AHEAD < IA ? cx : nx, ahead);
+      fx[i % RING] *= sw;
+      Half32 ha;
+      if constexpr (FINE) ha = widen(fa[i % RING]);
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        const int u = i * TJ + j, pu = (u + UNITS - 1) % UNITS;
-        v16f t;
+      for (int j = 0; j < JB; ++j) {
+        add((i + IA - 1) % IA, j, held);
+        v4f t = {};
         if constexpr (FINE) {
-          t = v16f{};
 #pragma unroll
-          for (int s = 0; s < 8; ++s) t = __builtin_amdgcn_mfma_f32_32x32x16_f16(hb[j].v[s], ha.v[s], t, 0, 0, 0);
+          for (int s = 0; s < 4; ++s) t = __builtin_amdgcn_mfma_f32_16x16x32_f16(hb[j].v[s], ha.v[s], t, 0, 0, 0);
         } else {
-          t = mfma32(fb[j].lo, fa[(i + PA) & 1].lo, v16f{});
-          t = mfma32(fb[j].hi, fa[(i + PA) & 1].hi, t);
+          t = mfma16(fb[j], fa[i % RING], t);
         }
-        if (i + 1 == TI) fb[j] = get_b(nb, j);
-        if constexpr (NT == 1) {
-          add(u, t, f[i]);
-        } else {
-          T[(u + PT) & 1] = t;
-          add(pu, T[(u + 1 + PT) & 1], u == 0 ? held : f[pu / TJ]);
+        T[j] = t;
+        if (i + 1 == IA) fb[j] = get_b(nb, j);
+#pragma unroll
+        for (int n = from + j; n < to; n += JB)
+          i < IA - AHEAD ? issue(n, k + 1, na, nb, nx) : issue(n, k + 2, ca, cb_, cx);
+      }
+      if constexpr (!FINE) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          if (i + 1 == IA) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+          if (from + j < to) __builtin_amdgcn_sched_group_barrier(0x020, (PER + JB - 1) / JB, 0);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    held = f[TI - 1];
   };
-  issue(0, la0, lb0, lx0);
-  issue(1, la1, lb1, lx1);
-  wait_vm_lgkm0<NL>();
-  __builtin_amdgcn_s_barrier();
-  fa[0] = get_a(la0, 0);
 #pragma unroll
-  for (int j = 0; j < TJ; ++j) fb[j] = get_b(lb0, j);
+  for (int n = 0; n < NL; ++n) issue(n, 0, la0, lb0, lx0);
+#pragma unroll
+  for (int n = 0; n < FIRST; ++n) issue(n, 1, la1, lb1, lx1);
+  wait_vm_lgkm0<FIRST>();
+  __builtin_amdgcn_s_barrier();
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) fa[i] = get_a(la0, i), fx[i] = get_x(lx0, i);
+#pragma unroll
+  for (int j = 0; j < JB; ++j) fb[j] = get_b(lb0, j);
   for (int kc = 0; kc < turns; kc += 64) {
     const int swv = __float_as_int(load_sw(kc));
     const int end = turns - kc < 64 ? turns : kc + 64;
     auto sw_at = [&](int k) { return __int_as_float(__builtin_amdgcn_readlane(swv, k - kc)); };
     int k = kc;
     for (; k + 2 <= end; k += 2) {
-      stage(std::integral_constant<int, 0>{}, k, sw_at(k), la0, lb0, lx0, la1, lb1);
-      stage(std::integral_constant<int, 1>{}, k + 1, sw_at(k + 1), la1, lb1, lx1, la0, lb0);
+      stage(k, sw_at(k), la0, lb0, lx0, la1, lb1, lx1);
+      stage(k + 1, sw_at(k + 1), la1, lb1, lx1, la0, lb0, lx0);
     }
-    if (k < end) stage(std::integral_constant<int, 0>{}, k, sw_at(k), la0, lb0, lx0, la1, lb1);
+    if (k < end) stage(k, sw_at(k), la0, lb0, lx0, la1, lb1, lx1);
   }
-  if constexpr (NT == 2) {  // the last tile's results still wait, in set (turns * UNITS - 1) % 2
-    const bool first = UNITS % 2 == 1 && turns % 2 == 1;
-    v16f d;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) d[e] = first ? T[0][e] : T[1][e];
-    add(UNITS - 1, d, held);
-  }
+  for (int j = 0; j < JB; ++j) add(IA - 1, j, fx[(IA - 1) % RING]);  // the last group's results still wait
   auto owner = [&](int u) { return KG > 1 ? u % KG : g; };  // the K group that finishes unit u of 8 registers
   if constexpr (KG > 1) {
     // the K groups' sums meet in LDS, in a fixed order: each unit of 8 registers is finished by one group
     wait_vm_lgkm0<0>();
     __builtin_amdgcn_s_barrier();  // the buffers are free
-    constexpr int REGS8 = TI * TJ * 2;
+    constexpr int REGS8 = IA * JB / 2;
     static_assert(KG * NW * REGS8 * 2048 <= 4 * ROOM && ROOM % 2048 == 0, "room for the sums");
-    auto slot = [&](int grp, int u, int q) {
+    auto slot_of = [&](int grp, int u, int q) {
       const int at = ((grp * NW + wave) * REGS8 + u) * 2048 + q * 1024;
       return reinterpret_cast<v4f*>(one_of(at / ROOM, la0, la1, lb0, lb1) + at % ROOM + lane * 16);
     };
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+    for (int i = 0; i < IA; ++i)
 #pragma unroll
-      for (int j = 0; j < TJ; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int u = (i * TJ + j) * 2 + q / 2;
-          const v16f c = acc[i][j];
-          if (owner(u) != g) *slot(g, u, q & 1) = v4f{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
-        }
+      for (int j = 0; j < JB; ++j) {
+        const int u = (i * JB + j) / 2;
+        if (owner(u) != g) *slot_of(g, u, j & 1) = acc[i][j];
+      }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+    for (int i = 0; i < IA; ++i)
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        v16f c = acc[i][j];
+      for (int j = 0; j < JB; ++j) {
+        const int u = (i * JB + j) / 2;
+        if (owner(u) != g) continue;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int u = (i * TJ + j) * 2 + q / 2;
-          if (owner(u) != g) continue;
-#pragma unroll
-          for (int h = 1; h < KG; ++h) {
-            const v4f d = *slot((g + h) % KG, u, q & 1);
-            c[4 * q] += d[0], c[4 * q + 1] += d[1], c[4 * q + 2] += d[2], c[4 * q + 3] += d[3];
-          }
-        }
-        acc[i][j] = c;
+        for (int h = 1; h < KG; ++h) acc[i][j] += *slot_of((g + h) % KG, u, j & 1);
       }
   }
-  const int64_t m1 = m0 + wr + l32, n1 = n0 + wc + 8 * kh;
+  // lane: token l16 of each group; of each pair of channel groups 8 consecutive channels
+  const int64_t m1 = m0 + wr + l16, n1 = n0 + wc + 8 * l4;
   if (KG == 4 && part) {
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+    for (int i = 0; i < IA; ++i)
 #pragma unroll
-      for (int u = 0; u < 2 * TJ; ++u) {
-        if (owner(i * 2 * TJ + u) != g) continue;
-        const int64_t m = m1 + 32 * i, n = n1 + 16 * u;
-        const v16f& c = acc[i][u / 2];
-        const int r = 8 * (u & 1);
+      for (int u = 0; u < TJ; ++u) {
+        if (owner(i * TJ + u) != g) continue;
+        const int64_t m = m1 + 16 * i, n = n1 + 32 * u;
         if (m < o.M && n < ldp) {
-          float4* q = reinterpret_cast<float4*>(part + ((int64_t)blockIdx.y * o.M + m) * ldp + n);
-          q[0] = make_float4(c[r], c[r + 1], c[r + 2], c[r + 3]);
-          q[1] = make_float4(c[r + 4], c[r + 5], c[r + 6], c[r + 7]);
+          v4f* q = reinterpret_cast<v4f*>(part + ((int64_t)blockIdx.y * o.M + m) * ldp + n);
+          q[0] = acc[i][2 * u], q[1] = acc[i][2 * u + 1];
         }
       }
     wait_vm_lgkm0<0>();
     return;
   }
-  float bb[2 * TJ][8];
+  float bb[TJ][8];
 #pragma unroll
-  for (int u = 0; u < 2 * TJ; ++u)
+  for (int u = 0; u < TJ; ++u)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) bb[u][e] = o.bias && n1 + 16 * u + e < o.N ? o.bias[n1 + 16 * u + e] : kNoBias;
+    for (int e = 0; e < 8; ++e) bb[u][e] = o.bias && n1 + 32 * u + e < o.N ? o.bias[n1 + 32 * u + e] : kNoBias;
   auto finish = [&](auto whole) {  // whole: no bounds to check
     constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+    for (int i = 0; i < IA; ++i)
 #pragma unroll
-      for (int u = 0; u < 2 * TJ; ++u)
-        if (owner(i * 2 * TJ + u) == g) {
-          const int64_t m = m1 + 32 * i, n = n1 + 16 * u;
+      for (int u = 0; u < TJ; ++u)
+        if (owner(i * TJ + u) == g) {
+          const int64_t m = m1 + 16 * i, n = n1 + 32 * u;
           float y[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = acc[i][u / 2][8 * (u & 1) + e] + bb[u][e];
+          for (int e = 0; e < 8; ++e) y[e] = acc[i][2 * u + e / 4][e % 4] + bb[u][e];
           if (WHOLE || m < o.M) store8<OUT, WHOLE>(o, m, n, y);
         }
   };
