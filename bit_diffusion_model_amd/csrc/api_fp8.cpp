@@ -103,7 +103,7 @@ size_t svdq_gemm_fp8_workspace_bytes(const svdq_fp8_layer* layer, int64_t M) {
 
 size_t svdq_fp8_workspace_bytes(const svdq_fp8_layer* layer, int64_t M) {
   if (M < 1 || check_dims_fp8(layer) != SVDQ_OK || check_rows(M) != SVDQ_OK || check_tiles(M, layer->N) != SVDQ_OK) return 0;
-  if (few_layer_fp8(M)) return 0;
+  if (few_layer_fp8(M, layer->K)) return 0;
   return act_bytes_fp8(M, layer->K) + svdq_gemm_fp8_workspace_bytes(layer, M);
 }
 
@@ -141,7 +141,7 @@ svdq_status svdq_linear_forward_fp8(const svdq_fp8_layer* layer, int64_t M, cons
       (st = check_ws(workspace, ws_bytes, svdq_fp8_workspace_bytes(layer, M))) != SVDQ_OK)
     return st;
   hipError_t e;
-  if (few_layer_fp8(M)) {
+  if (few_layer_fp8(M, layer->K)) {
     e = launch_few_layer_fp8(M, layer->K, layer->N, X, xdtype, ldx, layer->qW, layer->sW, layer->bias, Y, ldy, ydtype,
                              (hipStream_t)stream);
     if (e != hipSuccess) return fail(SVDQ_EHIP, "block-scaled layer launch: %s", hipGetErrorString(e));

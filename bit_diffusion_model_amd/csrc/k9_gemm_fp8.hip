@@ -437,67 +437,93 @@ __global__ __launch_bounds__(64 * FEW_NW) void k9_few(const uint8_t* __restrict_
   few_finish<NT>(acc, sums, wave, lane, o, n0);
 }
 
-// The whole layer for few tokens in one launch.  Blocks of 128 are quantized independently, so a wave quantizes each
-// block's codes in the registers that the MFMA takes them from: 32 values of its token a lane, the block's maximum by
-// two lane swaps.  Every workgroup repeats this for its 16 channels (X is small and in L2).
-template <typename T>
+// The whole layer for few tokens in one launch.  Blocks of 128 are quantized independently: four lanes take one, 32
+// values each, so a workgroup does 128 of the M x nb at a time (one step up to 5 tokens of 3072 values), its first weights
+// on their way; codes and scales go to LDS, and each wave takes the NU blocks that are its share of K (b = wave, wave +
+// 8, ..) from there to registers.  Every workgroup repeats this (X is small and in L2), so it stays and takes `turns`
+// channel blocks, the next one's weights on their way while one's sums meet in LDS.
+template <typename T, int NU>
 __global__ __launch_bounds__(64 * FEW_NW) void k9_few_layer(const T* __restrict__ X, int64_t ldx, int K, int64_t ld,
-                                                            const uint8_t* __restrict__ qW, Scales sc, Out o) {
-  __shared__ FewSums<1> sums;
-  constexpr int U = FEW_U;
+                                                            const uint8_t* __restrict__ qW, Scales sc, Out o, int turns) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // codes [M][nb][128], scales [M][nb]
+  __shared__ FewSums<1> sums[2];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const uint8_t* wl = qW + n0 * ld + lane * 16;
-  const int nb = (int)sc.blocks, m = lane & 15, kl = 16 * (lane >> 4);
-  const float* sw = sc.sW + n0 / 128 * nb;
-  const T* x = X + (m < o.M ? m : 0) * ldx;
-  const bool on = m < o.M;
-  v4f acc[1] = {};
-  for (int b0 = wave; b0 < nb; b0 += FEW_NW * U) {
-    uint4 w[U][2];
-    Vec<T, 8> raw[U][4];
-    float c[U];
+  const int64_t cbs = (o.N + 15) / 16, cb0 = (int64_t)blockIdx.x * turns, cb1 = cb0 + turns < cbs ? cb0 + turns : cbs;
+  const int nb = (int)sc.blocks, l4 = lane >> 4, m = lane & 15, jobs = (int)o.M * nb;
+  float* lds_s = reinterpret_cast<float*>(lds + jobs * 128);
+  uint4 w[NU][2];
+  float c[NU];
+  auto load_w = [&](int64_t cb) {
+    const uint8_t* wl = qW + cb * 16 * ld + lane * 16;
+    const float* sw = sc.sW + (cb >> 3) * nb;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = b0 + u * FEW_NW, in = at < nb ? at : nb - 1;
+    for (int u = 0; u < NU; ++u) {
+      const int at = wave + u * FEW_NW, in = at < nb ? at : nb - 1;  // past the end: any weights, zero tokens
 #pragma unroll
       for (int h = 0; h < 2; ++h) w[u][h] = *reinterpret_cast<const uint4*>(wl + in * 2048 + h * 1024);
       c[u] = sw[in];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) raw[u][q] = load8(x, at * 128 + (q >> 1) * 64 + (q & 1) * 8 + kl, on ? K : 0);
     }
+  };
+  for (int j0 = wave * 16; j0 == wave * 16 || j0 < jobs; j0 += FEW_NW * 16) {
+    const int j = j0 + m, row = j / nb, k0 = (j - row * nb) * 128 + 16 * l4;
+    Vec<T, 8> raw[4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (b0 + u * FEW_NW >= nb) break;
-      float v[32];
-      uint32_t a = 0;
+    for (int q = 0; q < 4; ++q) raw[q] = load8(X + (j < jobs ? row : 0) * ldx, k0 + (q >> 1) * 64 + (q & 1) * 8, j < jobs ? K : 0);
+    if (j0 == wave * 16) load_w(cb0);
+    if (j0 >= jobs) break;
+    float v[32], s, r;
+    uint32_t a = 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) valuev<T, 8>(raw[u][q], v + 8 * q);
+    for (int q = 0; q < 4; ++q) valuev<T, 8>(raw[q], v + 8 * q);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) a = umax(a, abs_bits(v[e]));
-      {
-        const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-        a = umax(r[0], r[1]);
-        const auto h = __builtin_amdgcn_permlane32_swap(a, a, false, false);
-        a = umax(h[0], h[1]);
+    for (int e = 0; e < 32; ++e) a = umax(a, abs_bits(v[e]));
+    const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    a = umax(p[0], p[1]);
+    const auto t = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    a = umax(t[0], t[1]);
+    block_scale(a, s, r);
+    if (j < jobs) {
+      if (l4 == 0) lds_s[j] = s;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4 q;
+        q.x = e4m3x4(v[16 * h], v[16 * h + 1], v[16 * h + 2], v[16 * h + 3], r);
+        q.y = e4m3x4(v[16 * h + 4], v[16 * h + 5], v[16 * h + 6], v[16 * h + 7], r);
+        q.z = e4m3x4(v[16 * h + 8], v[16 * h + 9], v[16 * h + 10], v[16 * h + 11], r);
+        q.w = e4m3x4(v[16 * h + 12], v[16 * h + 13], v[16 * h + 14], v[16 * h + 15], r);
+        *reinterpret_cast<uint4*>(lds + j * 128 + h * 64 + l4 * 16) = q;
       }
-      float s, r;
-      block_scale(a, s, r);
-      uint32_t q[8];
+    }
+  }
+  __syncthreads();
+  uint4 codes[NU][2];
+  float s[NU];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = e4m3x4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3], r);
+  for (int u = 0; u < NU; ++u) {
+    const bool in = m < o.M && wave + u * FEW_NW < nb;
+    const int j = in ? m * nb + wave + u * FEW_NW : 0;
+    s[u] = in ? lds_s[j] : 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      codes[u][h] = in ? *reinterpret_cast<const uint4*>(lds + j * 128 + h * 64 + l4 * 16) : make_uint4(0, 0, 0, 0);
+  }
+  for (int64_t cb = cb0; cb < cb1; ++cb) {
+    v4f acc[1] = {};
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
       v4f d = {};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        d = dot32(w[u][h].x, w[u][h].y, q[4 * h], q[4 * h + 1], d);
-        d = dot32(w[u][h].z, w[u][h].w, q[4 * h + 2], q[4 * h + 3], d);
+        d = dot32(w[u][h].x, w[u][h].y, codes[u][h].x, codes[u][h].y, d);
+        d = dot32(w[u][h].z, w[u][h].w, codes[u][h].z, codes[u][h].w, d);
       }
-      const float k = s * c[u];
+      const float k = s[u] * c[u];
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[0][e] = fmaf(d[e], k, acc[0][e]);
     }
+    if (cb + 1 < cb1) load_w(cb + 1);
+    few_finish<1>(acc, sums[(cb - cb0) & 1], wave, lane, o, cb * 16);
   }
-  few_finish<1>(acc, sums, wave, lane, o, n0);
 }
 
 template <int WM, int WN, int TI, int TJ, int KG, bool HALVES = false>
@@ -585,17 +611,28 @@ Fp8Plan plan_fp8(int64_t M, int64_t K, int64_t N, bool fine) {
   return p;
 }
 
-bool few_layer_fp8(int64_t M) { return M <= 16; }
+bool few_layer_fp8(int64_t M, int64_t K) { return M <= 16 && K <= 4 * FEW_NW * 128 && M * fp8_blocks(K) <= 256; }
 
 hipError_t launch_few_layer_fp8(int64_t M, int64_t K, int64_t N, const void* X, int xdtype, int64_t ldx,
                                 const uint8_t* qW, const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype,
                                 hipStream_t st) {
   const Out o{nullptr, nullptr, bias, Y, ldy, M, N, ydtype};
   const Scales sc{nullptr, sW, 0, fp8_blocks(K)};
-  const dim3 g((uint32_t)((N + 15) / 16)), b(64 * FEW_NW);
-  const int64_t ld = i8_ld(K);
-  if (xdtype == 0) hipLaunchKernelGGL(k9_few_layer<float>, g, b, 0, st, static_cast<const float*>(X), ldx, (int)K, ld, qW, sc, o);
-  else hipLaunchKernelGGL(k9_few_layer<uint16_t>, g, b, 0, st, static_cast<const uint16_t*>(X), ldx, (int)K, ld, qW, sc, o);
+  // as many workgroups as the card holds (two to a unit), and no more turns than that takes
+  const int64_t ld = i8_ld(K), cbs = (N + 15) / 16, most = 2 * (int64_t)device_cus(), turns = (cbs + most - 1) / most;
+  const dim3 g((uint32_t)((cbs + turns - 1) / turns)), b(64 * FEW_NW);
+  const size_t lds = (size_t)(M * sc.blocks) * 132;  // at most 66 KB
+  auto typed = [&](auto x) {
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, g, b, lds, st, x, ldx, (int)K, ld, qW, sc, o, (int)turns); };
+    typedef typename std::remove_const<typename std::remove_pointer<decltype(x)>::type>::type T;
+    const int64_t nu = (sc.blocks + FEW_NW - 1) / FEW_NW;
+    if (nu <= 1) go(k9_few_layer<T, 1>);
+    else if (nu <= 2) go(k9_few_layer<T, 2>);
+    else if (nu <= 3) go(k9_few_layer<T, 3>);
+    else go(k9_few_layer<T, 4>);
+  };
+  if (xdtype == 0) typed(static_cast<const float*>(X));
+  else typed(static_cast<const uint16_t*>(X));
   return hipGetLastError();
 }
 

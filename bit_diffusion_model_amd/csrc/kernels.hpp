@@ -114,7 +114,7 @@ hipError_t launch_quant_fp8(int64_t M, int64_t K, const void* X, int xdtype, int
 typedef W8A8Plan Fp8Plan;
 Fp8Plan plan_fp8(int64_t M, int64_t K, int64_t N, bool fine);  // fine: for fp32 outputs
 // Whether the layer runs as one launch for few tokens (which quantizes inside), and that launch.
-bool few_layer_fp8(int64_t M);
+bool few_layer_fp8(int64_t M, int64_t K);
 hipError_t launch_few_layer_fp8(int64_t M, int64_t K, int64_t N, const void* X, int xdtype, int64_t ldx,
                                 const uint8_t* qW, const float* sW, const float* bias, void* Y, int64_t ldy, int ydtype,
                                 hipStream_t st);
