@@ -5,15 +5,16 @@
 // mean and rstd: g = dy (o + gamma); dx = rstd (g - sum(g) / C - z sum(g z) / C); dgamma = sum over rows dy z,
 // dbeta = sum over rows dy.
 //
-// Design (gfx950): bound by HBM, x (and dy) read once: a row stays in registers, 8 values a lane and chunk.  A row takes
-// L = 16, 32 or 64 lanes (up to 512 values, or 1024 in two chunks), or a team of several waves (two chunks: 1024 values
-// a wave); a block has several rows or teams at a time and walks over a range of rows, the next row on its way while one is
-// computed, with gamma and beta in registers as long as the image stays the same.
+// Design (gfx950): bound by HBM, x (and dy) read once: a row stays in registers, 8 values a lane and chunk, NC chunks.  A
+// row takes L = 16, 32 or 64 lanes, or a team of several waves: few waves of up to 4 chunks where there are rows enough
+// to fill the card, more waves of fewer chunks where there are not.
 // Statistics: a first mean p of the lanes' own group, then d = x - p, sum d and sum d^2: mean = p + sum d / n,
 // M2 = sum d^2 - (sum d)^2 / n, so that neither a mean far from zero nor the rounding of p costs digits (a constant row
-// gives beta).  Waves join by the pairwise formula (Chan, Golub and LeVeque) about the first one's mean.  One barrier a row.
-// The columns' sums of the gradient stay in registers over a block's rows; a block adds its rows' in LDS in turn and leaves
-// one partial sum; a second launch adds the blocks'.  Every order is fixed: no atomics.
+// gives beta).  Waves join by the pairwise formula (Chan, Golub and LeVeque) about the first one's mean, at one barrier.
+// The columns' sums of the gradient stay in registers over a block's rows, the next row on its way while one is
+// computed; a block joins its teams in LDS and leaves one partial sum; a second launch adds the blocks'.  Every
+// order is fixed: no atomics.
+#include <algorithm>
 #include <type_traits>
 
 #include "fp8.hpp"
@@ -46,16 +47,16 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
-// f(e) for the values e of a vector at k that lie within the row
+// f(e, in) for the 8 values from k, in: whether e lies within the row; whole: all of the chunk's do (the same for all lanes)
 template <typename F>
-__device__ __forceinline__ void within(int k, int C, F&& f) {
-  if (k + 8 <= C) {
+__device__ __forceinline__ void within(bool whole, int k, int C, F&& f) {
+  if (whole) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f(e);
-  } else if (k < C) {
+    for (int e = 0; e < 8; ++e) f(e, true);
+  } else {
+    asm("" : "+v"(k));  // compared here, not kept from one use to the next (8 masks each)
 #pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (k + e < C) f(e);
+    for (int e = 0; e < 8; ++e) f(e, k + e < C);
   }
 }
 
@@ -87,81 +88,88 @@ struct Seat {
 
 constexpr int MAX_WAVES = 16;
 
-// OUT: 0 fp32, 1 bf16, 2 codes.  A block takes rows [blockIdx.x * per, + per) of the B * S; w waves to a row.
-// Y may be X: a row is loaded whole, by the block that stores it, before it is stored.
-template <typename T, int OUT, int L, int NC>
-__global__ __launch_bounds__(1024) void k10_norm(LayerNormArgs a, int w, int64_t per, void* Y, int64_t bsy, int64_t ldy,
-                                                float* __restrict__ sX, int64_t Mp, float* __restrict__ mean_out,
-                                                float* __restrict__ rstd_out) {
+// Reads of a row's chunks.  Where a wave has one row, by the row's buffer (what lies past it reads as 0, no branch); VEC:
+// bf16 rows begin at words.
+template <typename T, int L, bool VEC>
+struct Chunks {
+  typedef Row<T, VEC> R;
+  typedef typename R::Raw Raw;
+  R r;
+  __device__ __forceinline__ Chunks(const T* p, int C) : r(p, C) {}
+  __device__ __forceinline__ Raw load(int k) const { return r.load(k); }
+  __device__ __forceinline__ void value(const Raw& w, int k, float v[8]) const { r.value(w, k, v); }
+};
+template <typename T, bool VEC>
+struct Chunks<T, 32, VEC> {
+  typedef Vec<T, 8> Raw;
+  const T* p;
+  int C;
+  __device__ __forceinline__ Chunks(const T* p, int C) : p(p), C(C) {}
+  __device__ __forceinline__ Raw load(int k) const { return load8(p, k, C); }
+  __device__ __forceinline__ void value(const Raw& w, int, float v[8]) const { valuev<T, 8>(w, v); }
+};
+template <typename T, bool VEC>
+struct Chunks<T, 16, VEC> : Chunks<T, 32, VEC> {
+  using Chunks<T, 32, VEC>::Chunks;
+};
+
+// Most waves of a block whose rows are held in NC chunks (at C = 16384)
+constexpr int norm_waves(int NC) { return NC <= 2 ? 16 : NC == 3 ? 11 : 8; }
+
+// OUT: 0 fp32, 1 bf16, 2 codes.  w waves to a row.
+// Y may be X: a row is loaded whole, by the team that stores it, before it is stored.
+template <typename T, int OUT, int L, int NC, bool VEC>
+__global__ __launch_bounds__(64 * norm_waves(NC)) void k10_norm(LayerNormArgs a, int w, void* Y, int64_t bsy, int64_t ldy,
+                                                               float* __restrict__ sX, int64_t Mp,
+                                                               float* __restrict__ mean_out, float* __restrict__ rstd_out) {
   typedef typename std::conditional<OUT == 0, float, uint16_t>::type TY;
   __shared__ float2 meet[2][MAX_WAVES];
   const Seat<L> at(w);
   const int C = a.C, step = (L == 64 ? 64 * w : L) * 8;
-  const int64_t M = a.B * a.S, r0 = (int64_t)blockIdx.x * per, r1 = r0 + per < M ? r0 + per : M;
-  const T* X = static_cast<const T*>(a.X);
-  auto locate = [&](int64_t r, int64_t& b, int64_t& s) {
-    b = (uint32_t)r / (uint32_t)a.S;
-    s = r - b * a.S;
-  };
-  Vec<T, 8> raw[NC];
-  auto fetch = [&](int64_t r, Vec<T, 8>* v) {
-    int64_t b, s;
-    locate(r < r1 ? r : r0, b, s);
-    const T* x = X + b * a.bsx + s * a.ldx;
-#pragma unroll
-    for (int j = 0; j < NC; ++j) v[j] = load8(x, 8 * at.li + j * step, r < r1 ? C : 0);
-  };
-  fetch(r0 + at.sub, raw);
-  float gm[NC][8], bt[NC][8];
-  int64_t image = -1;
+  const int64_t M = a.B * a.S;
   // the values that this wave (or group of lanes) holds of a row
-  const int mine = L < 64 ? C : [&] {
+  auto count = [&](int i) {
     int n = 0;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int k = (at.li & ~63) * 8 + j * step;
+      const int k = i * 512 + j * step;
       n += C - k < 0 ? 0 : C - k < 512 ? C - k : 512;
     }
-    return n;
-  }();
-  const float n = (float)mine, rn = mine ? 1.0f / n : 0.0f;
+    return (float)n;
+  };
+  const float n = L < 64 ? (float)C : count(at.wave - at.team * w), rn = 1.0f / n;
+  auto whole = [&](int j) { return j + (L == 64 ? 2 : 1) < NC || (j + 1) * step <= C; };  // (the launch sees to the first)
   int turn = 0;
-  for (int64_t rb = r0; rb < r1; rb += at.rpb, turn ^= 1) {
+  for (int64_t rb = (int64_t)blockIdx.x * at.rpb; rb < M; rb += (int64_t)gridDim.x * at.rpb, turn ^= 1) {
     const int64_t r = rb + at.sub;
-    const bool on = r < r1;
+    const bool on = r < M;
+    const int64_t b = (uint32_t)(on ? r : 0) / (uint32_t)a.S, s = (on ? r : 0) - b * a.S;
+    const Chunks<T, L, VEC> x(static_cast<const T*>(a.X) + b * a.bsx + s * a.ldx, on ? C : 0);
+    const Chunks<float, L, true> gamma(a.gamma ? a.gamma + b * a.gs : nullptr, a.gamma ? C : 0);
+    const Chunks<float, L, true> beta(a.beta ? a.beta + b * a.gs : nullptr, a.beta ? C : 0);
+    const float one = !a.gamma || a.one_plus ? 1.0f : 0.0f;  // without gamma: 1 + 0
+    typedef typename Chunks<float, L, true>::Raw RawF;
     float v[NC][8];
+    typename Chunks<T, L, VEC>::Raw raw[NC];
 #pragma unroll
-    for (int j = 0; j < NC; ++j) valuev<T, 8>(raw[j], v[j]);
-    Vec<T, 8> next[NC];
-    fetch(r + at.rpb, next);
-    int64_t b, s;
-    locate(on ? r : r0, b, s);
-    if (a.gs ? b != image : image < 0) {
-      image = b;
-      const float *g = a.gamma + (a.gs ? b * a.gs : 0), *t = a.beta + (a.gs ? b * a.gs : 0);
+    for (int j = 0; j < NC; ++j) raw[j] = x.load(8 * at.li + j * step);
+    // gamma and beta come from cache, two chunks ahead of their use
+    RawF gw[2], bw[2];
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const int k = 8 * at.li + j * step;
-        if (a.gamma) valuev<float, 8>(load8(g, k, C), gm[j]);
-        if (a.beta) valuev<float, 8>(load8(t, k, C), bt[j]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          gm[j][e] = a.gamma ? a.one_plus ? 1.0f + gm[j][e] : gm[j][e] : 1.0f;
-          bt[j][e] = a.beta ? bt[j][e] : 0.0f;
-        }
-      }
-    }
+    for (int j = 0; j < 2 && j < NC; ++j) gw[j] = gamma.load(8 * at.li + j * step), bw[j] = beta.load(8 * at.li + j * step);
     float sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NC; ++j)
+    for (int j = 0; j < NC; ++j) {
+      x.value(raw[j], 8 * at.li + j * step, v[j]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum += v[j][e];  // what lies past C is 0
+    }
     const float p = lane_sum<L>(sum) * rn;
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j)
-      within(8 * at.li + j * step, C, [&](int e) {
-        const float d = v[j][e] - p;
+      within(whole(j), 8 * at.li + j * step, C, [&](int e, bool in) {
+        const float d = in ? v[j][e] - p : 0.0f;
         s1 += d;
         s2 = fmaf(d, d, s2);
       });
@@ -173,15 +181,6 @@ __global__ __launch_bounds__(1024) void k10_norm(LayerNormArgs a, int w, int64_t
       __syncthreads();
       const float2* t = meet[turn] + at.team * w;
       const float m0 = t[0].x;
-      auto count = [&](int i) {
-        int c = 0;
-#pragma unroll
-        for (int j = 0; j < NC; ++j) {
-          const int k = i * 512 + j * step;
-          c += C - k < 0 ? 0 : C - k < 512 ? C - k : 512;
-        }
-        return (float)c;
-      };
       float d = 0.0f, q = 0.0f;
       for (int i = 1; i < w; ++i) d += count(i) * (t[i].x - m0);
       mean = m0 + d / (float)C;
@@ -196,18 +195,25 @@ __global__ __launch_bounds__(1024) void k10_norm(LayerNormArgs a, int w, int64_t
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int k = 8 * at.li + j * step;
+      float g[8], t[8];
+      gamma.value(gw[j & 1], k, g);
+      beta.value(bw[j & 1], k, t);
+      if (j + 2 < NC) gw[j & 1] = gamma.load(k + 2 * step), bw[j & 1] = beta.load(k + 2 * step);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] = fmaf((v[j][e] - mean) * rstd, gm[j][e], bt[j][e]);
+      for (int e = 0; e < 8; ++e) v[j][e] = fmaf((v[j][e] - mean) * rstd, one + g[e], t[e]);
       if constexpr (OUT < 2) {
-        store_row8(static_cast<TY*>(Y) + b * bsy + s * ldy, k, on ? C : 0, v[j]);
+        TY* y = static_cast<TY*>(Y) + b * bsy + s * ldy;
+        if (whole(j)) {
+          if (on) storev<TY, 8>(y + k, v[j]);
+        } else {
+          store_row8(y, k, on ? C : 0, v[j]);
+        }
       } else {
         uint32_t top = 0;
-        if (k + 8 > C) {  // past the row: zeros
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[j][e] = k + e < C ? v[j][e] : 0.0f;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = umax(top, abs_bits(v[j][e]));
+        within(whole(j), k, C, [&](int e, bool in) {
+          v[j][e] = in ? v[j][e] : 0.0f;  // past the row: zeros
+          top = umax(top, abs_bits(v[j][e]));
+        });
         top = wave_umax<16>(top);
         float sc, f;
         block_scale(top, sc, f);
@@ -216,9 +222,8 @@ __global__ __launch_bounds__(1024) void k10_norm(LayerNormArgs a, int w, int64_t
               make_uint2(e4m3x4(v[j][0], v[j][1], v[j][2], v[j][3], f), e4m3x4(v[j][4], v[j][5], v[j][6], v[j][7], f));
         if (on && (at.li & 15) == 0 && k < C) sX[(int64_t)(k >> 7) * Mp + r] = sc;
       }
+      if constexpr (NC > 2) __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int j = 0; j < NC; ++j) raw[j] = next[j];
   }
 }
 
@@ -226,80 +231,77 @@ __global__ __launch_bounds__(1024) void k10_norm(LayerNormArgs a, int w, int64_t
 // [blockIdx.x * per, + per) of run blockIdx.y and leaves its columns' sums in part[run][blockIdx.x][2][C], or with one
 // block to a run in dgamma and dbeta [run][C] themselves.  SUMS: whether they are wanted.
 // dX may be X or dY: a row is loaded whole, by the block that stores it, before it is stored.
-template <typename T, typename TD, int L, int NC, bool SUMS>
+template <typename T, typename TD, int L, int NC, bool SUMS, bool VEC>
 __global__ __launch_bounds__(1024) void k10_grad(LayerNormArgs a, int w, int64_t len, int64_t per, const TD* dY,
                                                 int64_t bsd, int64_t ldd, const float* __restrict__ mean_in,
                                                 const float* __restrict__ rstd_in, T* dX, int64_t bso, int64_t ldo,
                                                 float* __restrict__ part, float* __restrict__ dgamma,
                                                 float* __restrict__ dbeta) {
-  extern __shared__ float cols[];  // [2][step * NC], where several teams meet
+  extern __shared__ float cols[];  // [teams][2][step * NC], where several meet
   __shared__ float2 meet[2][MAX_WAVES];
   const Seat<L> at(w);
   const int C = a.C, step = (L == 64 ? 64 * w : L) * 8;
   const int64_t base = (int64_t)blockIdx.y * len, r0 = base + (int64_t)blockIdx.x * per;
   const int64_t r1 = r0 + per < base + len ? r0 + per : base + len;
-  const T* X = static_cast<const T*>(a.X);
+  auto whole = [&](int j) { return L == 64 && (j + 1) * step <= C; };
   struct Row1 {
-    Vec<T, 8> x[NC];
-    Vec<TD, 8> d[NC];
+    typename Chunks<T, L, VEC>::Raw x[NC];
+    typename Chunks<TD, L, VEC>::Raw d[NC];
     float mean, rstd;
   };
   auto locate = [&](int64_t r, int64_t& b, int64_t& s) {
     b = (uint32_t)r / (uint32_t)a.S;
     s = r - b * a.S;
   };
-  auto fetch = [&](int64_t r, Row1& w1) {
-    const bool on = r < r1;
+  auto x_of = [&](int64_t r) {
     int64_t b, s;
-    if (!on) r = r0;
-    locate(r, b, s);
-    const T* x = X + b * a.bsx + s * a.ldx;
-    const TD* d = dY + b * bsd + s * ldd;
-    w1.mean = mean_in[r], w1.rstd = rstd_in[r];
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      w1.x[j] = load8(x, 8 * at.li + j * step, on ? C : 0);
-      w1.d[j] = load8(d, 8 * at.li + j * step, on ? C : 0);
-    }
+    locate(r < r1 ? r : r0, b, s);
+    return Chunks<T, L, VEC>(static_cast<const T*>(a.X) + b * a.bsx + s * a.ldx, r < r1 ? C : 0);
   };
+  auto d_of = [&](int64_t r) {
+    int64_t b, s;
+    locate(r < r1 ? r : r0, b, s);
+    return Chunks<TD, L, VEC>(dY + b * bsd + s * ldd, r < r1 ? C : 0);
+  };
+  auto fetch = [&](int64_t r, Row1& w1) {
+    const auto x = x_of(r);
+    const auto d = d_of(r);
+    w1.mean = mean_in[r < r1 ? r : r0], w1.rstd = rstd_in[r < r1 ? r : r0];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) w1.x[j] = x.load(8 * at.li + j * step), w1.d[j] = d.load(8 * at.li + j * step);
+  };
+  constexpr bool FETCH_AHEAD = NC == 1;  // (two chunks of two rows do not fit the registers of 16 waves)
   Row1 cur, next;
-  if (r0 < r1) fetch(r0 + at.sub, cur);
+  fetch(r0 + at.sub, cur);
   float gm[NC][8], ag[NC][8], ab[NC][8];
+  const float rc = 1.0f / (float)C, one = !a.gamma || a.one_plus ? 1.0f : 0.0f;  // without gamma: 1 + 0
+  // a block's rows share their gamma: a run is an image where images have their own
+  const Chunks<float, L, true> gamma(a.gamma ? a.gamma + blockIdx.y * a.gs : nullptr, a.gamma ? C : 0);
 #pragma unroll
-  for (int j = 0; j < NC; ++j)
+  for (int j = 0; j < NC; ++j) {
+    gamma.value(gamma.load(8 * at.li + j * step), 8 * at.li + j * step, gm[j]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ag[j][e] = ab[j][e] = 0.0f;
-  int64_t image = -1;
-  const float rc = 1.0f / (float)C;
+    for (int e = 0; e < 8; ++e) gm[j][e] += one, ag[j][e] = ab[j][e] = 0.0f;
+  }
   int turn = 0;
   for (int64_t rb = r0; rb < r1; rb += at.rpb, turn ^= 1) {
     const int64_t r = rb + at.sub;
     const bool on = r < r1;
-    fetch(r + at.rpb, next);
+    if constexpr (FETCH_AHEAD) fetch(r + at.rpb, next);
     int64_t b, s;
     locate(on ? r : r0, b, s);
-    if (a.gs ? b != image : image < 0) {
-      image = b;
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        if (a.gamma) valuev<float, 8>(load8(a.gamma + (a.gs ? b * a.gs : 0), 8 * at.li + j * step, C), gm[j]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) gm[j][e] = a.gamma ? a.one_plus ? 1.0f + gm[j][e] : gm[j][e] : 1.0f;
-      }
-    }
     float z[NC][8], d[NC][8], s1 = 0.0f, s2 = 0.0f;
+    const auto x = x_of(r);
+    const auto dy = d_of(r);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      valuev<T, 8>(cur.x[j], z[j]);
-      valuev<TD, 8>(cur.d[j], d[j]);  // zeros past the row and past the last row: nothing of theirs is added
+      const int k = 8 * at.li + j * step;
+      x.value(cur.x[j], k, z[j]);
+      dy.value(cur.d[j], k, d[j]);  // zeros past the row and past the last row: nothing of theirs is added
 #pragma unroll
       for (int e = 0; e < 8; ++e) z[j][e] = (z[j][e] - cur.mean) * cur.rstd;
-      if (!on || 8 * at.li + j * step + 8 > C) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[j][e] = on && 8 * at.li + j * step + e < C ? z[j][e] : 0.0f;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      within(whole(j) && (L < 64 || on), k, on ? C : 0, [&](int e, bool in) {
+        z[j][e] = in ? z[j][e] : 0.0f;
         if constexpr (SUMS) {
           ag[j][e] = fmaf(d[j][e], z[j][e], ag[j][e]);
           ab[j][e] += d[j][e];
@@ -307,7 +309,7 @@ __global__ __launch_bounds__(1024) void k10_grad(LayerNormArgs a, int w, int64_t
         d[j][e] *= gm[j][e];
         s1 += d[j][e];
         s2 = fmaf(d[j][e], z[j][e], s2);
-      }
+      });
     }
     s1 = lane_sum<L>(s1), s2 = lane_sum<L>(s2);
     if (L == 64 && w > 1) {
@@ -321,11 +323,17 @@ __global__ __launch_bounds__(1024) void k10_grad(LayerNormArgs a, int w, int64_t
     T* o = dX + b * bso + s * ldo;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
+      const int k = 8 * at.li + j * step;
 #pragma unroll
       for (int e = 0; e < 8; ++e) d[j][e] = (d[j][e] - s1 - z[j][e] * s2) * cur.rstd;
-      store_row8(o, 8 * at.li + j * step, on ? C : 0, d[j]);
+      if (whole(j)) {
+        if (on) storev<T, 8>(o + k, d[j]);
+      } else {
+        store_row8(o, k, on ? C : 0, d[j]);
+      }
     }
-    cur = next;
+    if constexpr (FETCH_AHEAD) cur = next;
+    else if (rb + at.rpb < r1) fetch(r + at.rpb, cur);
   }
   if constexpr (SUMS) {
     // the rows that a wave has side by side, then the block's teams in turn
@@ -349,56 +357,56 @@ __global__ __launch_bounds__(1024) void k10_grad(LayerNormArgs a, int w, int64_t
     const int64_t run = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     float* pg = gridDim.x > 1 ? part + run * 2 * C : dgamma ? dgamma + run * C : nullptr;
     float* pb = gridDim.x > 1 ? part + run * 2 * C + C : dbeta ? dbeta + run * C : nullptr;
+    const bool mine = L == 64 || (int)(threadIdx.x & 63) < L;  // one group of a wave's lanes has its sums
     if (teams == 1) {
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
-        const int k = 8 * at.li + j * step, end = L == 64 || (int)(threadIdx.x & 63) < L ? C : 0;
-        if (pg) store_row8(pg, k, end, ag[j]);
-        if (pb) store_row8(pb, k, end, ab[j]);
+        const int k = 8 * at.li + j * step;
+        if (pg) store_row8(pg, k, mine ? C : 0, ag[j]);
+        if (pb) store_row8(pb, k, mine ? C : 0, ab[j]);
       }
       return;
     }
-    for (int t = 0; t < teams; ++t) {
-      if (at.team == t && (L == 64 || (int)(threadIdx.x & 63) < L)) {
+    if (mine) {
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-          float4* g = reinterpret_cast<float4*>(cols + 8 * at.li + j * step);
-          float4* b = reinterpret_cast<float4*>(cols + wide + 8 * at.li + j * step);
+      for (int j = 0; j < NC; ++j) {
+        float4* g = reinterpret_cast<float4*>(cols + at.team * 2 * wide + 8 * at.li + j * step);
+        float4* b = reinterpret_cast<float4*>(cols + (at.team * 2 + 1) * wide + 8 * at.li + j * step);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float4 u = make_float4(0, 0, 0, 0), v = u;
-            if (t) u = g[h], v = b[h];
-            g[h] = make_float4(u.x + ag[j][4 * h], u.y + ag[j][4 * h + 1], u.z + ag[j][4 * h + 2], u.w + ag[j][4 * h + 3]);
-            b[h] = make_float4(v.x + ab[j][4 * h], v.y + ab[j][4 * h + 1], v.z + ab[j][4 * h + 2], v.w + ab[j][4 * h + 3]);
-          }
+        for (int h = 0; h < 2; ++h) {
+          g[h] = make_float4(ag[j][4 * h], ag[j][4 * h + 1], ag[j][4 * h + 2], ag[j][4 * h + 3]);
+          b[h] = make_float4(ab[j][4 * h], ab[j][4 * h + 1], ab[j][4 * h + 2], ab[j][4 * h + 3]);
         }
       }
-      __syncthreads();
     }
+    __syncthreads();
     for (int c = threadIdx.x; c < C; c += blockDim.x) {
-      if (pg) pg[c] = cols[c];
-      if (pb) pb[c] = cols[wide + c];
+      float g = cols[c], b = cols[wide + c];
+      for (int t = 1; t < teams; ++t) g += cols[t * 2 * wide + c], b += cols[(t * 2 + 1) * wide + c];
+      if (pg) pg[c] = g;
+      if (pb) pb[c] = b;
     }
   }
 }
 
-// The blocks' partial sums of a run, added in a fixed order: 32 columns, 8 threads each.
-__global__ __launch_bounds__(256) void k10_join(const float* __restrict__ part, int parts, int C,
-                                                float* __restrict__ dgamma, float* __restrict__ dbeta) {
-  __shared__ float2 sums[8][32];
+// The blocks' partial sums of a run, added in a fixed order: 32 columns, 32 threads each.
+constexpr int JOIN = 32;
+__global__ __launch_bounds__(32 * JOIN) void k10_join(const float* __restrict__ part, int parts, int C,
+                                                     float* __restrict__ dgamma, float* __restrict__ dbeta) {
+  __shared__ float2 sums[JOIN][33];
   const int c = (int)blockIdx.x * 32 + (threadIdx.x & 31), q = threadIdx.x >> 5;
   const float* p = part + (int64_t)blockIdx.y * parts * 2 * C + c;
   float2 s = make_float2(0.0f, 0.0f);
   if (c < C) {
-#pragma unroll 8
-    for (int i = q; i < parts; i += 8) s.x += p[(int64_t)i * 2 * C], s.y += p[(int64_t)i * 2 * C + C];
+#pragma unroll 4
+    for (int i = q; i < parts; i += JOIN) s.x += p[(int64_t)i * 2 * C], s.y += p[(int64_t)i * 2 * C + C];
   }
   sums[q][threadIdx.x & 31] = s;
   __syncthreads();
   if (q == 0 && c < C) {
     s = sums[0][threadIdx.x];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s.x += sums[i][threadIdx.x].x, s.y += sums[i][threadIdx.x].y;
+    for (int i = 1; i < JOIN; ++i) s.x += sums[i][threadIdx.x].x, s.y += sums[i][threadIdx.x].y;
     if (dgamma) dgamma[(int64_t)blockIdx.y * C + c] = s.x;
     if (dbeta) dbeta[(int64_t)blockIdx.y * C + c] = s.y;
   }
@@ -408,44 +416,57 @@ __global__ __launch_bounds__(256) void k10_join(const float* __restrict__ part, 
 struct Hold {
   int L, NC, w;
 };
-Hold hold(int C) {
+Hold hold(int C, int NC) {
   if (C <= 128) return Hold{16, 1, 1};
   if (C <= 256) return Hold{32, 1, 1};
-  if (C <= 512) return Hold{64, 1, 1};
-  return Hold{64, 2, (C + 1023) / 1024};
+  return Hold{64, NC, (C + 512 * NC - 1) / (512 * NC)};
 }
 
-template <typename F>
-void by_hold(const Hold& h, F&& f) {
-  if (h.L == 16) f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-  else if (h.L == 32) f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
-  else if (h.NC == 1) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-  else f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+// f(L, NC) as constants.  The norm: 16 lanes of 1 to 4 chunks, 32 of 1, 3 or 4, 64 of 1 to 4; the gradient: one chunk, or
+// 64 lanes of 2.
+template <int L, int... NCs, typename F>
+void by_chunks(int NC, F&& f) {
+  (void)((NC == NCs ? (f(std::integral_constant<int, L>{}, std::integral_constant<int, NCs>{}), true) : false) || ...);
+}
+
+// Where the rows fill the card with few waves each, those that leave the fewest lanes idle; else more waves of one
+// chunk.
+Hold hold_norm(int64_t M, int C) {
+  const int one = (C + 511) / 512;  // waves of one chunk
+  if (M * one < 16 * (int64_t)device_cus()) return hold(C, one <= MAX_WAVES ? 1 : 2);
+  if (C <= 512) return Hold{16, (C + 127) / 128, 1};
+  if (C <= 1024) return Hold{32, (C + 255) / 256, 1};
+  Hold best = hold(C, 2);
+  for (int NC : {3, 4}) {
+    const Hold h = hold(C, NC);
+    if (h.w * NC <= best.w * best.NC && (NC - 2) * 512 * h.w <= C) best = h;  // all chunks but the last two are whole
+  }
+  return best;
 }
 
 template <int OUT>
 hipError_t launch(const LayerNormArgs& a, void* Y, int64_t bsy, int64_t ldy, float* sX, float* mean, float* rstd,
                   hipStream_t st) {
-  const Hold h = hold(a.C);
   const int64_t M = a.B * a.S;
-  const int waves = h.w > 1 ? h.w : 4;
-  const int rpb = h.w > 1 ? 1 : 4 * (64 / h.L);
-  // enough blocks to fill the card, then rows to a block
-  const int64_t most = (int64_t)device_cus() * (32 / waves);
-  int64_t turns = (M + rpb * most - 1) / (rpb * most);
-  const int64_t per = turns * rpb;
-  const dim3 grid((uint32_t)((M + per - 1) / per)), block(64 * waves);
-  by_hold(h, [&](auto l, auto c) {
+  const Hold h = hold_norm(M, a.C);
+  const int waves = h.w >= 3 ? h.w : 4;
+  const int64_t rpb = h.L == 64 ? waves / h.w : 4 * (64 / h.L), blocks = (M + rpb - 1) / rpb;
+  const dim3 grid((uint32_t)(blocks < (1 << 22) ? blocks : 1 << 22)), block(64 * waves);  // (a launch takes fewer than 2^32 threads)
+  auto run = [&](auto l, auto c) {
     constexpr int L = decltype(l)::value, NC = decltype(c)::value;
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, a, h.w, per, Y, bsy, ldy, sX, fp8_pad(M), mean, rstd); };
-    if (a.xdtype == 0) go(k10_norm<float, OUT, L, NC>);
-    else go(k10_norm<uint16_t, OUT, L, NC>);
-  });
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, a, h.w, Y, bsy, ldy, sX, fp8_pad(M), mean, rstd); };
+    if (a.xdtype == 0) go(k10_norm<float, OUT, L, NC, true>);
+    else if (L < 64 || (rows_aligned4(a.X, a.ldx, 1) && a.bsx % 2 == 0)) go(k10_norm<uint16_t, OUT, L, NC, true>);
+    else if constexpr (L == 64) go(k10_norm<uint16_t, OUT, L, NC, false>);
+  };
+  if (h.L == 16) by_chunks<16, 1, 2, 3, 4>(h.NC, run);
+  else if (h.L == 32) by_chunks<32, 1, 3, 4>(h.NC, run);
+  else by_chunks<64, 1, 2, 3, 4>(h.NC, run);
   return hipGetLastError();
 }
 
 hipError_t launch_join(const float* part, uint32_t parts, int64_t runs, int C, float* dgamma, float* dbeta, hipStream_t st) {
-  hipLaunchKernelGGL(k10_join, dim3((uint32_t)((C + 31) / 32), (uint32_t)runs), dim3(256), 0, st, part, (int)parts, C, dgamma, dbeta);
+  hipLaunchKernelGGL(k10_join, dim3((uint32_t)((C + 31) / 32), (uint32_t)runs), dim3(32 * JOIN), 0, st, part, (int)parts, C, dgamma, dbeta);
   return hipGetLastError();
 }
 
@@ -461,15 +482,16 @@ hipError_t launch_layer_norm_fp8(const LayerNormArgs& a, uint8_t* qX, float* sX,
 }
 
 LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, bool sums) {
-  const Hold h = hold(C);
+  const Hold h = hold(C, C <= 8192 ? 1 : 2);
   LayerNormGradPlan p;
   p.runs = each ? B : 1;
   p.len = each ? S : B * S;
-  // teams to a block: up to 12 waves
+  // as many teams to a block as 16 waves hold, and one such block to a unit: half the partial sums of two blocks of 8
+  // waves (2x4608x3072 bf16 41.7 us against 48.8, 1024x4096 16.2 against 19.8, 39787x176 36.0 against 36.3)
   p.w = h.w;
-  p.waves = h.w > 1 ? (h.w > 12 ? h.w : 12 / h.w * h.w) : 8;
-  const int64_t rpb = h.w > 1 ? p.waves / h.w : p.waves * (64 / h.L);
-  const int64_t most = (device_cus() * 2 + p.runs - 1) / p.runs;  // blocks to a run
+  p.waves = MAX_WAVES / h.w * h.w;
+  const int64_t rpb = h.L == 64 ? p.waves / h.w : p.waves * (64 / h.L);
+  const int64_t most = (device_cus() + p.runs - 1) / p.runs;  // blocks to a run
   const int64_t turns = (p.len + rpb * most - 1) / (rpb * most);
   p.per = turns * rpb;
   p.parts = (uint32_t)((p.len + p.per - 1) / p.per);
@@ -482,11 +504,14 @@ hipError_t launch_layer_norm_grad(const LayerNormArgs& a, const void* dY, int dd
                                   float* dgamma, float* dbeta, void* ws, hipStream_t st) {
   const bool sums = dgamma || dbeta;
   const LayerNormGradPlan p = plan_layer_norm_grad(a.B, a.S, a.C, a.gs != 0, sums);
-  const Hold h = hold(a.C);
+  const Hold h = hold(a.C, a.C <= 8192 ? 1 : 2);
   float* part = p.parts > 1 ? static_cast<float*>(ws) : nullptr;
   const dim3 grid(p.parts, (uint32_t)p.runs), block(64 * p.waves);
-  const size_t lds = sums && p.waves > h.w ? (size_t)2 * (h.L == 64 ? 64 * h.w : h.L) * 8 * h.NC * 4 : 0;  // at most 48 KB
-  by_hold(h, [&](auto l, auto c) {
+  const int teams = p.waves / h.w;
+  const size_t lds = sums && teams > 1 ? (size_t)teams * 2 * (h.L == 64 ? 64 * h.w : h.L) * 8 * 4 : 0;  // at most 64 KB
+  const bool words = rows_aligned4(a.X, a.ldx, a.xdtype) && (a.xdtype == 0 || a.bsx % 2 == 0) &&
+                     rows_aligned4(dY, ldd, ddtype) && (ddtype == 0 || bsd % 2 == 0);  // bf16 rows begin at words
+  auto run = [&](auto l, auto c) {
     constexpr int L = decltype(l)::value, NC = decltype(c)::value;
     auto typed = [&](auto tx, auto td) {
       typedef decltype(tx) T;
@@ -495,12 +520,21 @@ hipError_t launch_layer_norm_grad(const LayerNormArgs& a, const void* dY, int dd
         hipLaunchKernelGGL(kernel, grid, block, lds, st, a, p.w, p.len, p.per, static_cast<const TD*>(dY), bsd, ldd, mean,
                            rstd, static_cast<T*>(dX), bso, ldo, part, dgamma, dbeta);
       };
-      if (sums) go(k10_grad<T, TD, L, NC, true>);
-      else go(k10_grad<T, TD, L, NC, false>);
+      auto kind = [&](auto vec) {
+        if (sums) go(k10_grad<T, TD, L, NC, true, decltype(vec)::value>);
+        else go(k10_grad<T, TD, L, NC, false, decltype(vec)::value>);
+      };
+      if constexpr (L == 64 && (sizeof(T) == 2 || sizeof(TD) == 2)) {
+        if (!words) return kind(std::false_type{});
+      }
+      kind(std::true_type{});
     };
     if (a.xdtype == 0) ddtype == 0 ? typed(float{}, float{}) : typed(float{}, uint16_t{});
     else ddtype == 0 ? typed(uint16_t{}, float{}) : typed(uint16_t{}, uint16_t{});
-  });
+  };
+  if (h.L == 16) by_chunks<16, 1>(h.NC, run);
+  else if (h.L == 32) by_chunks<32, 1>(h.NC, run);
+  else by_chunks<64, 1, 2>(h.NC, run);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !part || !sums) return e;
   return launch_join(part, p.parts, p.runs, a.C, dgamma, dbeta, st);

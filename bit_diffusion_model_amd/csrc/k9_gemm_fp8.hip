@@ -542,7 +542,20 @@ void launch_tiles(const Fp8Plan& p, int64_t ld, const uint8_t* qX, const uint8_t
 }
 
 // ---- the choice of kernel
-
+//
+// By estimated time alone (us; S = blocks of 128 along K, c = workgroups that share a compute unit; a round of c takes
+// a[c] S + b[c], a launch once more const).  The lines are least squares over 220 drawn sizes at both output kinds (256
+// CUs, launches back to back, inputs in turn; M x K x N); over those the choice costs 1% more than the best of the seven.
+// bf16 outputs, then fp32 ones (whose products in f16 take twice the MFMA time and the conversions besides):
+//   few     up to 32 tokens, the weights' read: 1x3072x18432 11.2, 32x3072x18432 15.0
+//   64      one K group: 333x1000x1111 5.8 (64 x 2: 6.1, 128: 8.9) / 6.8; 154x768x2304 5.1 (5.4, 7.0) / 6.1
+//   64 x 2  two K groups: 512x9216x3072 30.3 (64: 39.9, 128 x 2: 39.9) / 45.3 (53.2, 65.7)
+//   64 x 4  four K groups, and K in parts of at least 8 blocks: 64x12288x3072 16.4 in 4 parts, 28.3 in one, 64 x 2 33.8 /
+//           17.2, 30.8, 34.6
+//   128     4608x3072x9216 150 (64: 200) / 252 (325)
+//   128 x 2 two K groups: 1024x4096x4096 24.6 (128: 27.8, 64: 29.4) / 40.4 (44.7, 46.3)
+//   256     4608x3072x9216 127 (128: 150), 4608x12288x3072 154 (195), 2048x1280x5120 22.4 (24.6); bf16 outputs only; a
+//           last round for at most half of the CUs runs as tiles of 128 x 256
 // Tiles of 256 that a last round leaves for at most half of the CUs, after at least one whole round
 int64_t halved_tiles(int64_t M, int64_t N, int cus) {
   const int64_t T = ((M + 255) / 256) * ((N + 255) / 256), rest = T % cus;
@@ -554,7 +567,7 @@ struct Cost {
   int tile, groups, parts;
 };
 
-Cost tiles_cost(int64_t M, int64_t N, int S, int cus, int tile, int groups) {
+Cost tiles_cost(int64_t M, int64_t N, int S, int cus, int tile, int groups, bool fine) {
   const double T = (double)((M + tile - 1) / tile) * (double)((N + tile - 1) / tile);
   const double rounds = T / cus;
   double us = 0.0;
@@ -563,18 +576,22 @@ Cost tiles_cost(int64_t M, int64_t N, int S, int cus, int tile, int groups) {
     us = full * (a[most - 1] * S + b[most - 1]);
     if (rest > 0) us += a[(int)(rest + 0.999999) - 1] * S + b[(int)(rest + 0.999999) - 1];
   };
-  static const double a64[] = {0.315, 0.42, 0.42, 0.64}, b64[] = {0.0, 0.8, 0.8, 2.9}, a642[] = {0.26, 0.335},
-                      b642[] = {2.5, 3.6}, a644[] = {0.19}, b644[] = {3.6}, a128[] = {0.575, 0.725}, b128[] = {2.6, 5.6},
-                      a1282[] = {0.46}, b1282[] = {5.7};
-  if (tile == 64 && groups == 1) by_line(a64, b64, 4), us += 2.6;
-  else if (tile == 64 && groups == 2) by_line(a642, b642, 2), us += 1.0;
-  else if (tile == 64) by_line(a644, b644, 1), us += 0.9;
-  else if (tile == 128 && groups == 1) by_line(a128, b128, 2), us += 1.1;
-  else if (tile == 128) by_line(a1282, b1282, 1), us += 0.2;
+  // [0] bf16 outputs, [1] fp32
+  static const double a64[2][4] = {{0.352, 0.512, 0.552, 0.712}, {0.42, 0.661, 0.903, 1.115}},
+                      b64[2][4] = {{0.52, 1.59, 2.25, 3.67}, {0.17, 1.92, 3.27, 3.97}},
+                      a642[2][2] = {{0.251, 0.361}, {0.308, 0.534}}, b642[2][2] = {{0.0, 2.08}, {0.0, 2.58}},
+                      a644[2][1] = {{0.2}, {0.258}}, b644[2][1] = {{5.53}, {5.94}},
+                      a128[2][2] = {{0.523, 0.819}, {0.905, 1.567}}, b128[2][2] = {{3.6, 7.46}, {2.64, 8.89}},
+                      a1282[2][1] = {{0.401}, {0.779}}, b1282[2][1] = {{6.09}, {6.55}};
+  if (tile == 64 && groups == 1) by_line(a64[fine], b64[fine], 4), us += fine ? 3.2 : 2.7;
+  else if (tile == 64 && groups == 2) by_line(a642[fine], b642[fine], 2), us += fine ? 4.3 : 4.0;
+  else if (tile == 64) by_line(a644[fine], b644[fine], 1);
+  else if (tile == 128 && groups == 1) by_line(a128[fine], b128[fine], 2), us += fine ? 1.9 : 0.6;
+  else if (tile == 128) by_line(a1282[fine], b1282[fine], 1);
   else {
     const double full = (double)(int64_t)rounds, rest = rounds - full;
     const bool halved = full > 0 && rest <= 0.5;
-    us = full * (1.245 * S + 8.3) + (rest == 0 ? 0.0 : (halved ? 0.9 : rest <= 0.625 ? 1.08 : 1.245) * S + 8.3);
+    us = full * (1.067 * S + 8.3) + (rest == 0 ? 0.0 : (halved ? 0.78 : rest <= 0.625 ? 0.93 : 1.067) * S + 8.3);
   }
   return Cost{us, tile, groups, 1};
 }
@@ -589,22 +606,22 @@ Fp8Plan plan_fp8(int64_t M, int64_t K, int64_t N, bool fine) {
   auto take = [&](const Cost& c) {
     if (c.us < best.us) best = c;
   };
-  take(tiles_cost(M, N, S, cus, 64, 1));
-  take(tiles_cost(M, N, S, cus, 128, 1));
-  if (!fine) take(tiles_cost(M, N, S, cus, 256, 1));
+  take(tiles_cost(M, N, S, cus, 64, 1, fine));
+  take(tiles_cost(M, N, S, cus, 128, 1, fine));
+  if (!fine) take(tiles_cost(M, N, S, cus, 256, 1, fine));
   const int64_t T64 = ((M + 63) / 64) * ((N + 63) / 64), T128 = ((M + 127) / 128) * ((N + 127) / 128);
-  if (T128 <= cus) take(tiles_cost(M, N, S, cus, 128, 2));
-  if (T64 <= 2 * cus) take(tiles_cost(M, N, S, cus, 64, 2));
+  if (T128 <= cus) take(tiles_cost(M, N, S, cus, 128, 2, fine));
+  if (T64 <= 2 * cus) take(tiles_cost(M, N, S, cus, 64, 2, fine));
   if (T64 <= cus) {
     for (int parts = 1; parts <= 8 && parts * T64 <= cus && (parts == 1 || S / parts >= 8); parts *= 2) {
       const int per = (S + parts - 1) / parts;
-      Cost c = tiles_cost(M, N, per, cus, 64, 4);
+      Cost c = tiles_cost(M, N, per, cus, 64, 4, fine);
       c.parts = (S + per - 1) / per;  // no empty part
-      if (c.parts > 1) c.us += 6.0 + 12.0 * (double)(M * ldp) * c.parts / 6e6;
+      if (c.parts > 1) c.us += 2.4 + 5.2e-6 * (double)(M * ldp) * c.parts;
       take(c);
     }
   }
-  if (M <= 32) take(Cost{2.3 + (double)(N * ld) * 1e-6 * (0.075 + 0.006 * (double)M), 0, 1, 1});
+  if (M <= 32) take(Cost{3.0 + (double)(N * ld) * 1e-6 * (0.11 + 0.009 * (double)M), 0, 1, 1});
   Fp8Plan p{best.tile, best.groups, best.parts, ldp, 0, 0};
   if (p.tile == 256) p.halved = halved_tiles(M, N, cus);
   if (p.parts > 1) p.bytes = (size_t)p.parts * (size_t)M * (size_t)ldp * 4;

@@ -92,19 +92,22 @@ __device__ __forceinline__ void storev(TY* p, const float v[V]) {
   }
 }
 
-// Values k .. k + 7 of a row of K values from p; what lies at or past K reads as 0
+// Values k .. k + 7 of a row of K values from p; what lies at or past K reads as 0.  At a row's end every value comes from
+// an address of the row, so that the eight loads go out together (a branch each: one after the other's wait).
 template <typename T>
 __device__ __forceinline__ Vec<T, 8> load8(const T* p, int k, int K) {
   Vec<T, 8> r = {};
   if (k + 8 <= K) {
     r = loadv<T, 8>(p + k);
   } else if (k < K) {
+    T t[7];
 #pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (k + e < K) {
-        if constexpr (sizeof(T) == 4) r.w[e] = __float_as_uint(p[k + e]);
-        else r.w[e / 2] |= (uint32_t)p[k + e] << (16 * (e & 1));
-      }
+    for (int e = 0; e < 7; ++e) t[e] = p[k + e < K ? k + e : K - 1];
+#pragma unroll
+    for (int e = 0; e < 7; ++e) {
+      if constexpr (sizeof(T) == 4) r.w[e] = k + e < K ? __float_as_uint(t[e]) : 0u;
+      else r.w[e / 2] |= k + e < K ? (uint32_t)t[e] << (16 * (e & 1)) : 0u;
+    }
   }
   return r;
 }
