@@ -163,6 +163,16 @@ svdq_status svdq_debug_fp8_plan(const svdq_fp8_layer* layer, int64_t M, int32_t 
   return ok();
 }
 
+svdq_status svdq_debug_layer_norm_plan(const svdq_layer_norm_desc* norm, int64_t B, int64_t S, int32_t plan[4]) {
+  svdq_status st = check_layer_norm(norm, B, S);
+  if (st != SVDQ_OK) return st;
+  if (B < 1 || S < 1 || !plan) return fail(SVDQ_EINVAL, "B and S must be >= 1 and plan non-NULL");
+  const LayerNormPlan p = plan_layer_norm(B * S, (int)norm->C);
+  const LayerNormGradPlan g = plan_layer_norm_grad(B, S, (int)norm->C, norm->image_stride != 0, true);
+  plan[0] = p.lanes, plan[1] = p.chunks, plan[2] = p.waves, plan[3] = (int32_t)g.parts;
+  return ok();
+}
+
 svdq_status svdq_layer_norm(const svdq_layer_norm_desc* norm, int64_t B, int64_t S, const void* X, int32_t xdtype,
                             int64_t bsx, int64_t ldx, void* Y, int32_t ydtype, int64_t bsy, int64_t ldy, float* mean,
                             float* rstd, void* stream) {

@@ -200,7 +200,7 @@ __global__ __launch_bounds__(64 * norm_waves(NC)) void k10_norm(LayerNormArgs a,
       beta.value(bw[j & 1], k, t);
       if (j + 2 < NC) gw[j & 1] = gamma.load(k + 2 * step), bw[j & 1] = beta.load(k + 2 * step);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] = fmaf((v[j][e] - mean) * rstd, one + g[e], t[e]);
+      for (int e = 0; e < 8; ++e) v[j][e] = (v[j][e] - mean) * rstd * (one + g[e]) + t[e];  // one rounding an operation
       if constexpr (OUT < 2) {
         TY* y = static_cast<TY*>(Y) + b * bsy + s * ldy;
         if (whole(j)) {
@@ -451,7 +451,7 @@ hipError_t launch(const LayerNormArgs& a, void* Y, int64_t bsy, int64_t ldy, flo
   const Hold h = hold_norm(M, a.C);
   const int waves = h.w >= 3 ? h.w : 4;
   const int64_t rpb = h.L == 64 ? waves / h.w : 4 * (64 / h.L), blocks = (M + rpb - 1) / rpb;
-  const dim3 grid((uint32_t)(blocks < (1 << 22) ? blocks : 1 << 22)), block(64 * waves);  // (a launch takes fewer than 2^32 threads)
+  const dim3 grid((uint32_t)(blocks < (1 << 21) ? blocks : 1 << 21)), block(64 * waves);  // (a launch takes fewer than 2^32 threads)
   auto run = [&](auto l, auto c) {
     constexpr int L = decltype(l)::value, NC = decltype(c)::value;
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, a, h.w, Y, bsy, ldy, sX, fp8_pad(M), mean, rstd); };
@@ -479,6 +479,11 @@ hipError_t launch_layer_norm(const LayerNormArgs& a, void* Y, int ydtype, int64_
 
 hipError_t launch_layer_norm_fp8(const LayerNormArgs& a, uint8_t* qX, float* sX, float* mean, float* rstd, hipStream_t st) {
   return launch<2>(a, qX, 0, i8_ld(a.C), sX, mean, rstd, st);
+}
+
+LayerNormPlan plan_layer_norm(int64_t M, int C) {
+  const Hold h = hold_norm(M, C);
+  return LayerNormPlan{h.L, h.NC, h.w};
 }
 
 LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, bool sums) {

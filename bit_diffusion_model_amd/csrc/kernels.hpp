@@ -173,6 +173,11 @@ struct LayerNormGradPlan {
   size_t bytes;
 };
 LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, bool sums);
+// How the norm holds a row: `lanes` lanes (64: `waves` waves of them), `chunks` chunks of 8 values each.
+struct LayerNormPlan {
+  int lanes, chunks, waves;
+};
+LayerNormPlan plan_layer_norm(int64_t M, int C);
 // dX (X's type); dgamma and dbeta [C], or [B][C] where gs != 0, either may be NULL.
 hipError_t launch_layer_norm_grad(const LayerNormArgs& a, const void* dY, int ddtype, int64_t bsd, int64_t ldd,
                                   const float* mean, const float* rstd, void* dX, int64_t bso, int64_t ldo,

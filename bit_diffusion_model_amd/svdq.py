@@ -78,6 +78,7 @@ EXPORTS = [
     "svdq_fp8_workspace_bytes", "svdq_gemm_fp8", "svdq_linear_forward_fp8", "svdq_layer_norm",
     "svdq_layer_norm_quantize_fp8", "svdq_norm_linear_fp8_workspace_bytes", "svdq_norm_linear_forward_fp8",
     "svdq_layer_norm_backward_workspace_bytes", "svdq_layer_norm_backward", "svdq_debug_fp8_plan",
+    "svdq_debug_layer_norm_plan",
 ]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -154,6 +155,7 @@ def lib():
         "svdq_layer_norm_backward_workspace_bytes": (SZ, [P, I64, I64]),
         "svdq_layer_norm_backward": (I32, [P, I64, I64, P, I32, I64, I64, P, I32, I64, I64, P, P, P, I64, I64, P, P, P, SZ, P]),
         "svdq_debug_fp8_plan": (I32, [P, I64, I32, P]),
+        "svdq_debug_layer_norm_plan": (I32, [P, I64, I64, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -1112,6 +1114,12 @@ class LayerNorm:
         """(mean, rstd): fp32 tensors for the rows of X, to be filled by a forward call and read by backward."""
         torch, n = _torch(), X.numel() // self.C
         return torch.empty(n, dtype=torch.float32, device=X.device), torch.empty(n, dtype=torch.float32, device=X.device)
+
+    def plan(self, B: int, S: int):
+        """svdq_debug_layer_norm_plan: (lanes, chunks, waves to a row, blocks that the gradient's sums are joined from)."""
+        p = (ctypes.c_int32 * 4)()
+        _check(lib().svdq_debug_layer_norm_plan(self._ref, B, S, p))
+        return tuple(p)
 
     @staticmethod
     def _stats(torch, stats, n: int, dev: int):

@@ -566,7 +566,7 @@ svdq_status svdq_norm_linear_forward_int8(const svdq_group_norm_desc* norm, cons
  *             qW[n][k] on the matrix core, all sums in fp32, then GELU if asked, rounded once to Y's type.  For fp32 Y
  *             the codes are multiplied as fp16 (exact).  For bf16 Y above 32 rows they are multiplied as they are, at twice
  *             the rate: the matrix core then aligns the products of 8 codes to the largest before it adds them, which
- *             costs 1e-5 to 6e-5 of a sum, far below the rounding to bf16.
+ *             costs 1e-5 to 6e-5 of a sum, far below the rounding to bf16.  The factors s_X s_W have to stay within fp32.
  * E4M3 is the finite variant (bias 7, subnormals to 2^-9, largest 448, 0x7F and 0xFF NaN).  Rows of codes are
  * svdq_int8_ld(K) = K rounded up to 128 bytes long; the bytes past K are zero.  Scales of activations are
  * [ceil(K / 128)][Mp] fp32, Mp = M rounded up to 4 (what lies past M is neither written nor used); of weights
@@ -618,7 +618,7 @@ svdq_status svdq_linear_forward_fp8(const svdq_fp8_layer* layer, int64_t M, cons
 /* ------------------------------------------ layer norm and its gradient ---- */
 /* X [B][S][C] (image, row, channel; row stride ldx, image stride bsx, in elements).  Per row: mean and biased variance
  * in fp32 (sums of differences to a first mean, joined pairwise: no cancellation however far the mean lies from zero); z
- * = (x - mean) rstd, rstd = 1 / sqrt(var + eps); y = z w + beta with w = gamma, or 1 + gamma where one_plus is 1 (the
+ * = (x - mean) rstd, rstd = 1 / sqrt(var + eps); y = z w + beta, one rounding an operation, w = gamma, or 1 + gamma where one_plus is 1 (the
  * scale and shift of a modulated norm).  gamma and beta [C] serve all rows (image_stride 0), or image b those at
  * b image_stride.  A NaN or an infinity makes its row's outputs NaN and no other row's; sums of values and of squared
  * differences have to stay within fp32.  Images of X (and dY) are apart, or one and the same (stride 0).  Limits: C <=
@@ -675,10 +675,13 @@ svdq_status svdq_layer_norm_backward(const svdq_layer_norm_desc* norm, int64_t B
  *   svdq_debug_group_norm_plan: plan = {1 where one launch serves the norm, 1 where the blocks' statistics are joined by
  *     a launch of their own, statistics blocks and output blocks per image}.
  *   svdq_debug_fp8_plan: as svdq_debug_w8a8_plan, for the block-scaled product into a svdq_dtype.
+ *   svdq_debug_layer_norm_plan: plan = {lanes that hold a row (16, 32 or 64), chunks of 8 values to a lane, waves to a row,
+ *     blocks whose column sums the gradient joins for each gamma (1: no second launch)}.
  * EINVAL / EUNSUPPORTED as the calls themselves; host only, nothing is launched. */
 svdq_status svdq_debug_w8a8_plan(const svdq_int8_layer* layer, int64_t M, int32_t plan[4]);
 svdq_status svdq_debug_group_norm_plan(const svdq_group_norm_desc* norm, int64_t B, int64_t S, int32_t plan[4]);
 svdq_status svdq_debug_fp8_plan(const svdq_fp8_layer* layer, int64_t M, int32_t ydtype, int32_t plan[4]);
+svdq_status svdq_debug_layer_norm_plan(const svdq_layer_norm_desc* norm, int64_t B, int64_t S, int32_t plan[4]);
 
 /* Diagnostic: the exact integer group sums I[g][m][n] = sum_{k in group g} qX[m][k]
  * qW[n][k] (INT4 only; the review's section 3 product Q_X Q_W, taken per group) for the
