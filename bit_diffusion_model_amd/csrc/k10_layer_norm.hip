@@ -60,10 +60,10 @@ __device__ __forceinline__ void within(bool whole, int k, int C, F&& f) {
   }
 }
 
-template <typename TY, bool NT = false>
+template <typename TY>
 __device__ __forceinline__ void store_row8(TY* p, int k, int C, const float v[8]) {
   if (k + 8 <= C) {
-    storev<TY, 8, NT>(p + k, v);
+    storev<TY, 8>(p + k, v);
   } else if (k < C) {
 #pragma unroll
     for (int e = 0; e < 7; ++e)
@@ -496,7 +496,8 @@ LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, b
   p.w = h.w;
   p.waves = MAX_WAVES / h.w * h.w;
   const int64_t rpb = h.L == 64 ? p.waves / h.w : p.waves * (64 / h.L);
-  const int64_t most = (device_cus() + p.runs - 1) / p.runs;  // blocks to a run
+  // (up to 4 turns one block does them all: the second launch would take longer)
+  const int64_t most = p.len <= 4 * rpb ? 1 : (device_cus() + p.runs - 1) / p.runs;  // blocks to a run
   const int64_t turns = (p.len + rpb * most - 1) / (rpb * most);
   p.per = turns * rpb;
   p.parts = (uint32_t)((p.len + p.per - 1) / p.per);

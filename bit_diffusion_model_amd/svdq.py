@@ -1095,14 +1095,15 @@ class LayerNorm:
 
     def _geometry(self, X, what="X"):
         """(B, S, bs, ld): images, rows, image and row stride of X."""
-        _, xt, _, _ = _rt()
-        if X.dim() not in (2, 3) or X.shape[-1] != self.C or X.dtype not in xt or (self.C > 1 and X.stride(-1) != 1):
-            raise SvdqError(f"{what} must be an fp32 or bf16 [M][{self.C}] or [B][S][{self.C}] tensor with unit channel stride")
-        B = X.shape[0] if X.dim() == 3 else 1
-        S = X.shape[-2]
+        shape, strides, C = X.shape, X.stride(), self.C
+        n = len(shape)
+        if n not in (2, 3) or shape[-1] != C or X.dtype not in _cfg[1] or (C > 1 and strides[-1] != 1):
+            raise SvdqError(f"{what} must be an fp32 or bf16 [M][{C}] or [B][S][{C}] tensor with unit channel stride")
+        B, bs = (shape[0], strides[0]) if n == 3 else (1, 0)
         if self.images and self.images != B:
             raise SvdqError(f"gamma and beta are of {self.images} images, {what} of {B}")
-        return B, S, X.stride(0) if X.dim() == 3 else 0, _ld(S, X.stride(-2), self.C)
+        S, ld = shape[-2], strides[-2]
+        return B, S, bs, ld if S > 1 or ld > C else C
 
     def _place(self, torch, X) -> int:
         dev = _on_current_device(torch, X)
@@ -1112,8 +1113,8 @@ class LayerNorm:
 
     def alloc_stats(self, X):
         """(mean, rstd): fp32 tensors for the rows of X, to be filled by a forward call and read by backward."""
-        torch, n = _torch(), X.numel() // self.C
-        return torch.empty(n, dtype=torch.float32, device=X.device), torch.empty(n, dtype=torch.float32, device=X.device)
+        torch = _rt()[0]
+        return X.new_empty((2, X.numel() // self.C), dtype=torch.float32).unbind()
 
     def plan(self, B: int, S: int):
         """svdq_debug_layer_norm_plan: (lanes, chunks, waves to a row, blocks that the gradient's sums are joined from)."""
@@ -1139,7 +1140,7 @@ class LayerNorm:
         if ydtype not in (F32, BF16):
             raise SvdqError("the norm's output is F32 or BF16")
         if out is None:
-            out = torch.empty(X.shape, dtype=ty[ydtype], device=X.device)
+            out = torch.empty_like(X, dtype=ty[ydtype], memory_format=torch.contiguous_format)
             bsy, ldy = S * self.C, self.C
         elif out.shape != X.shape or out.dtype != ty[ydtype]:
             raise SvdqError(f"out must be a {tuple(X.shape)} {ty[ydtype]} device tensor")
@@ -1182,13 +1183,13 @@ class LayerNorm:
         B, S, bs, ld = self._geometry(X)
         if dY.shape != X.shape:
             raise SvdqError(f"dY must be {tuple(X.shape)}")
-        _, _, bsd, ldd = self._geometry(dY, "dY")
+        bsd, ldd = (bs, ld) if dY.dtype is X.dtype and dY.stride() == X.stride() else self._geometry(dY, "dY")[2:]
         dev = self._place(torch, X)
         _on(dY, dev, "dY")
         if stats is None:
             raise SvdqError("stats must be the forward's (mean, rstd)")
         if out is None:
-            out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+            out = torch.empty_like(X, memory_format=torch.contiguous_format)
             bso, ldo = S * self.C, self.C
         elif out.shape != X.shape or out.dtype != X.dtype:
             raise SvdqError(f"out must be a {tuple(X.shape)} {X.dtype} device tensor")
@@ -1197,9 +1198,8 @@ class LayerNorm:
             _, _, bso, ldo = self._geometry(out, "out")
         dgamma = dbeta = ws = None
         if weights:
-            shape = (B, self.C) if self.images else (self.C,)
-            dgamma = torch.empty(shape, dtype=torch.float32, device=X.device)
-            dbeta = torch.empty(shape, dtype=torch.float32, device=X.device)
+            shape = (2, B, self.C) if self.images else (2, self.C)
+            dgamma, dbeta = X.new_empty(shape, dtype=torch.float32).unbind()
             n = 0 if workspace is not None else L.svdq_layer_norm_backward_workspace_bytes(self._ref, B, S)
             ws = torch.empty(n, dtype=torch.uint8, device=X.device) if n else workspace
         _check(L.svdq_layer_norm_backward(self._ref, B, S, dY.data_ptr(), xt[dY.dtype], bsd, ldd, X.data_ptr(),
