@@ -57,7 +57,7 @@ svdq_status check_layer_norm(const svdq_layer_norm_desc* n, int64_t B, int64_t S
   if (n->C < 1) return fail(SVDQ_EINVAL, "C must be >= 1 (got %lld)", (long long)n->C);
   if (n->C > kMaxLayerNormC)
     return fail(SVDQ_EUNSUPPORTED, "C must be <= %lld (got %lld)", (long long)kMaxLayerNormC, (long long)n->C);
-  if (!(n->eps > 0.0f && n->eps < 3.0e38f)) return fail(SVDQ_EINVAL, "eps must be positive and finite");
+  if (!(n->eps >= 1.17549435e-38f && n->eps < 3.0e38f)) return fail(SVDQ_EINVAL, "eps must be positive, normal and finite");
   if (n->one_plus != 0 && n->one_plus != 1) return fail(SVDQ_EINVAL, "one_plus must be 0 or 1");
   if (!aligned(n->gamma, 4) || !aligned(n->beta, 4)) return fail(SVDQ_EINVAL, "gamma and beta must be 4-byte aligned");
   if (B < 0 || S < 0) return fail(SVDQ_EINVAL, "B and S must be >= 0");
@@ -80,7 +80,7 @@ svdq_status layer_norm_args(const svdq_layer_norm_desc* n, int64_t B, int64_t S,
                             int64_t bsx, int64_t ldx, LayerNormArgs& a) {
   svdq_status st = check_in(X, xdtype, ldx, n->C);
   if (st != SVDQ_OK || (st = check_images("X", B, S, n->C, bsx, ldx, true)) != SVDQ_OK) return st;
-  a = LayerNormArgs{B, S, (int)n->C, n->one_plus != 0, n->eps, n->gamma, n->beta, n->image_stride, X, xdtype, B > 1 ? bsx : 0, ldx};
+  a = LayerNormArgs{B, S, (int)n->C, n->one_plus != 0, n->eps, n->gamma, n->beta, n->image_stride, X, xdtype, B > 1 ? bsx : 0, ldx, 0, 0};
   return SVDQ_OK;
 }
 

@@ -14,13 +14,14 @@ constexpr int64_t fp8_pad(int64_t M) { return (M + 3) / 4 * 4; }
 
 typedef int v8i_t __attribute__((ext_vector_type(8)));
 
-// A block's scale s = a / 448 and the factor r = 448 / a of its codes (both IEEE quotients), from the bits of its
-// largest magnitude; a is floored at 2^-96 (zeros get zero codes, r stays finite).  A block that holds a NaN or an
+// A block's scale s = a / 448 and the factor r = 448 / a of its codes (both IEEE quotients: the first by a product and one
+// correction with the exact residual, which gives the correctly rounded one for every a), from the bits of its largest magnitude; a is floored at 2^-96 (zeros get zero codes, r stays finite).  A block that holds a NaN or an
 // infinity gets a NaN scale and r = 0, so that its codes are 0 and the row's outputs NaN.
 __device__ __forceinline__ void block_scale(uint32_t abits, float& s, float& r) {
   const bool bad = abits >= 0x7F800000u;
   const float a = __uint_as_float(umax(abits, 0x0F800000u));  // 2^-96
-  s = bad ? __uint_as_float(0x7FC00000u) : a / 448.0f;
+  const float q = a * (1.0f / 448.0f);
+  s = bad ? __uint_as_float(0x7FC00000u) : fmaf(fmaf(-448.0f, q, a), 1.0f / 448.0f, q);
   r = bad ? 0.0f : 448.0f / a;
 }
 

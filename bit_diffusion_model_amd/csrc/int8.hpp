@@ -11,7 +11,7 @@ namespace svdq {
 
 // Row reads without branches, so that all of a row's loads can be issued before the first is
 // waited for.  A Row covers K values from p; load(k) starts the read of values k .. k+7 and
-// value() turns it into fp32; what lies at or past K reads as 0 (the buffer's range).
+// value() turns it into fp32; what lies at or past K reads as 0 (the buffer's range); inner() does where all eight lie before K.
 // VEC: p is 4-byte aligned (16-byte loads need no more).  A bf16 row that may begin in the middle
 // of a word is read from the word's start, 20 bytes for 8 values, and shifted.  Only whole aligned
 // words are read: the first and the last may hold a neighbour's value, never an unmapped byte, and
@@ -31,6 +31,7 @@ struct Row<float, VEC> {
     v[0] = __uint_as_float(w.a.x), v[1] = __uint_as_float(w.a.y), v[2] = __uint_as_float(w.a.z), v[3] = __uint_as_float(w.a.w);
     v[4] = __uint_as_float(w.b.x), v[5] = __uint_as_float(w.b.y), v[6] = __uint_as_float(w.b.z), v[7] = __uint_as_float(w.b.w);
   }
+  __device__ __forceinline__ void inner(const Raw& w, float v[8]) const { value(w, 0, v); }
 };
 
 template <>
@@ -41,9 +42,12 @@ struct Row<uint16_t, true> {
   __device__ __forceinline__ Row(const uint16_t* p, int K)
       : r(make_rsrc(p, ((uint32_t)K + 1) / 2 * 4)), odd_end(K & 1 ? K : 0x7FFFFFFF) {}
   __device__ __forceinline__ Raw load(int k) const { return buf_load16(r, (uint32_t)k * 2); }
-  __device__ __forceinline__ void value(const Raw& w, int k, float v[8]) const {
+  __device__ __forceinline__ void inner(const Raw& w, float v[8]) const {
     v[0] = bf16_lo_to_f32(w.x), v[1] = bf16_hi_to_f32(w.x), v[2] = bf16_lo_to_f32(w.y), v[3] = bf16_hi_to_f32(w.y);
     v[4] = bf16_lo_to_f32(w.z), v[5] = bf16_hi_to_f32(w.z), v[6] = bf16_lo_to_f32(w.w), v[7] = bf16_hi_to_f32(w.w);
+  }
+  __device__ __forceinline__ void value(const Raw& w, int k, float v[8]) const {
+    inner(w, v);
     if (odd_end != 0x7FFFFFFF) {
 #pragma unroll
       for (int e = 1; e < 8; e += 2)
@@ -66,13 +70,16 @@ struct Row<uint16_t, false> {
   __device__ __forceinline__ Raw load(int k) const {
     return Raw{buf_load16(r, (uint32_t)k * 2), buf_load4(r, (uint32_t)k * 2 + 16)};
   }
-  __device__ __forceinline__ void value(const Raw& w, int k, float v[8]) const {
+  __device__ __forceinline__ void inner(const Raw& w, float v[8]) const {
     const uint32_t x[5] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t d = __builtin_amdgcn_alignbit(x[i + 1], x[i], shift);
       v[2 * i] = bf16_lo_to_f32(d), v[2 * i + 1] = bf16_hi_to_f32(d);
     }
+  }
+  __device__ __forceinline__ void value(const Raw& w, int k, float v[8]) const {
+    inner(w, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (k + e == end) v[e] = 0.0f;

@@ -88,6 +88,18 @@ struct Seat {
 
 constexpr int MAX_WAVES = 16;
 
+// Row r of image b: r = b S + s by the launch's reciprocal of S (see divisor())
+__device__ __forceinline__ void locate(const LayerNormArgs& a, int64_t r, int64_t& b, int64_t& s) {
+  b = (int64_t)(((uint64_t)r * a.div_m) >> a.div_p);
+  s = r - b * a.S;
+}
+
+// 1 / sqrt(v), v >= 2^-126: the hardware's and one Newton step (within a step of fp32); 0 of an infinite v
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float y = __builtin_amdgcn_rsqf(v);
+  return v < INFINITY ? fmaf(y, fmaf(-0.5f * v * y, y, 0.5f), y) : y;
+}
+
 // Reads of a row's chunks.  Where a wave has one row, by the row's buffer (what lies past it reads as 0, no branch); VEC:
 // bf16 rows begin at words.
 template <typename T, int L, bool VEC>
@@ -98,6 +110,7 @@ struct Chunks {
   __device__ __forceinline__ Chunks(const T* p, int C) : r(p, C) {}
   __device__ __forceinline__ Raw load(int k) const { return r.load(k); }
   __device__ __forceinline__ void value(const Raw& w, int k, float v[8]) const { r.value(w, k, v); }
+  __device__ __forceinline__ void inner(const Raw& w, float v[8]) const { r.inner(w, v); }
 };
 template <typename T, bool VEC>
 struct Chunks<T, 32, VEC> {
@@ -107,6 +120,7 @@ struct Chunks<T, 32, VEC> {
   __device__ __forceinline__ Chunks(const T* p, int C) : p(p), C(C) {}
   __device__ __forceinline__ Raw load(int k) const { return load8(p, k, C); }
   __device__ __forceinline__ void value(const Raw& w, int, float v[8]) const { valuev<T, 8>(w, v); }
+  __device__ __forceinline__ void inner(const Raw& w, float v[8]) const { valuev<T, 8>(w, v); }
 };
 template <typename T, bool VEC>
 struct Chunks<T, 16, VEC> : Chunks<T, 32, VEC> {
@@ -123,7 +137,7 @@ __global__ __launch_bounds__(64 * norm_waves(NC)) void k10_norm(LayerNormArgs a,
                                                                float* __restrict__ sX, int64_t Mp,
                                                                float* __restrict__ mean_out, float* __restrict__ rstd_out) {
   typedef typename std::conditional<OUT == 0, float, uint16_t>::type TY;
-  __shared__ float2 meet[2][MAX_WAVES];
+  __shared__ float4 meet[2][MAX_WAVES];
   const Seat<L> at(w);
   const int C = a.C, step = (L == 64 ? 64 * w : L) * 8;
   const int64_t M = a.B * a.S;
@@ -137,13 +151,14 @@ __global__ __launch_bounds__(64 * norm_waves(NC)) void k10_norm(LayerNormArgs a,
     }
     return (float)n;
   };
-  const float n = L < 64 ? (float)C : count(at.wave - at.team * w), rn = 1.0f / n;
+  const float n = L < 64 ? (float)C : count(at.wave - at.team * w), rn = 1.0f / n, rc = 1.0f / (float)C;
   auto whole = [&](int j) { return j + (L == 64 ? 2 : 1) < NC || (j + 1) * step <= C; };  // (the launch sees to the first)
   int turn = 0;
   for (int64_t rb = (int64_t)blockIdx.x * at.rpb; rb < M; rb += (int64_t)gridDim.x * at.rpb, turn ^= 1) {
     const int64_t r = rb + at.sub;
     const bool on = r < M;
-    const int64_t b = (uint32_t)(on ? r : 0) / (uint32_t)a.S, s = (on ? r : 0) - b * a.S;
+    int64_t b, s;
+    locate(a, on ? r : 0, b, s);
     const Chunks<T, L, VEC> x(static_cast<const T*>(a.X) + b * a.bsx + s * a.ldx, on ? C : 0);
     const Chunks<float, L, true> gamma(a.gamma ? a.gamma + b * a.gs : nullptr, a.gamma ? C : 0);
     const Chunks<float, L, true> beta(a.beta ? a.beta + b * a.gs : nullptr, a.beta ? C : 0);
@@ -160,7 +175,8 @@ __global__ __launch_bounds__(64 * norm_waves(NC)) void k10_norm(LayerNormArgs a,
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      x.value(raw[j], 8 * at.li + j * step, v[j]);
+      if (whole(j)) x.inner(raw[j], v[j]);
+      else x.value(raw[j], 8 * at.li + j * step, v[j]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum += v[j][e];  // what lies past C is 0
     }
@@ -177,17 +193,17 @@ __global__ __launch_bounds__(64 * norm_waves(NC)) void k10_norm(LayerNormArgs a,
     float mean = p + s1 * rn, m2 = s2 - s1 * (s1 * rn);
     m2 = m2 < 0.0f ? 0.0f : m2;  // (a NaN passes)
     if (L == 64 && w > 1) {
-      if ((threadIdx.x & 63) == 0) meet[turn][at.wave] = make_float2(mean, m2);
+      if ((threadIdx.x & 63) == 0) meet[turn][at.wave] = make_float4(mean, m2, n, 0.0f);
       __syncthreads();
-      const float2* t = meet[turn] + at.team * w;
+      const float4* t = meet[turn] + at.team * w;
       const float m0 = t[0].x;
       float d = 0.0f, q = 0.0f;
-      for (int i = 1; i < w; ++i) d += count(i) * (t[i].x - m0);
-      mean = m0 + d / (float)C;
-      for (int i = 0; i < w; ++i) q += t[i].y + count(i) * (t[i].x - mean) * (t[i].x - mean);
+      for (int i = 1; i < w; ++i) d += t[i].z * (t[i].x - m0);
+      mean = m0 + d * rc;
+      for (int i = 0; i < w; ++i) q += t[i].y + t[i].z * (t[i].x - mean) * (t[i].x - mean);
       m2 = q;
     }
-    const float rstd = 1.0f / sqrtf(m2 / (float)C + a.eps);
+    const float rstd = inv_sqrt(m2 * rc + a.eps);
     if (on && at.li == 0) {
       if (mean_out) mean_out[r] = mean;
       if (rstd_out) rstd_out[r] = rstd;
@@ -249,18 +265,14 @@ __global__ __launch_bounds__(1024) void k10_grad(LayerNormArgs a, int w, int64_t
     typename Chunks<TD, L, VEC>::Raw d[NC];
     float mean, rstd;
   };
-  auto locate = [&](int64_t r, int64_t& b, int64_t& s) {
-    b = (uint32_t)r / (uint32_t)a.S;
-    s = r - b * a.S;
-  };
   auto x_of = [&](int64_t r) {
     int64_t b, s;
-    locate(r < r1 ? r : r0, b, s);
+    locate(a, r < r1 ? r : r0, b, s);
     return Chunks<T, L, VEC>(static_cast<const T*>(a.X) + b * a.bsx + s * a.ldx, r < r1 ? C : 0);
   };
   auto d_of = [&](int64_t r) {
     int64_t b, s;
-    locate(r < r1 ? r : r0, b, s);
+    locate(a, r < r1 ? r : r0, b, s);
     return Chunks<TD, L, VEC>(dY + b * bsd + s * ldd, r < r1 ? C : 0);
   };
   auto fetch = [&](int64_t r, Row1& w1) {
@@ -289,15 +301,15 @@ __global__ __launch_bounds__(1024) void k10_grad(LayerNormArgs a, int w, int64_t
     const bool on = r < r1;
     if constexpr (FETCH_AHEAD) fetch(r + at.rpb, next);
     int64_t b, s;
-    locate(on ? r : r0, b, s);
+    locate(a, on ? r : r0, b, s);
     float z[NC][8], d[NC][8], s1 = 0.0f, s2 = 0.0f;
     const auto x = x_of(r);
     const auto dy = d_of(r);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int k = 8 * at.li + j * step;
-      x.value(cur.x[j], k, z[j]);
-      dy.value(cur.d[j], k, d[j]);  // zeros past the row and past the last row: nothing of theirs is added
+      if (whole(j)) x.inner(cur.x[j], z[j]), dy.inner(cur.d[j], d[j]);
+      else x.value(cur.x[j], k, z[j]), dy.value(cur.d[j], k, d[j]);  // zeros past the row and past the last row: nothing of theirs is added
 #pragma unroll
       for (int e = 0; e < 8; ++e) z[j][e] = (z[j][e] - cur.mean) * cur.rstd;
       within(whole(j) && (L < 64 || on), k, on ? C : 0, [&](int e, bool in) {
@@ -444,9 +456,19 @@ Hold hold_norm(int64_t M, int C) {
   return best;
 }
 
+// a with the reciprocal of S that locate() uses: for r < 2^31, r m >> p = floor(r / S) with p = 31 + ceil(log2 S) and m =
+// ceil(2^p / S), since m S - 2^p < S <= 2^(p - 31), so that r (m S - 2^p) < 2^p
+LayerNormArgs divisor(LayerNormArgs a) {
+  a.div_p = 31;
+  while ((int64_t(1) << (a.div_p - 31)) < a.S) ++a.div_p;
+  a.div_m = ((uint64_t(1) << a.div_p) + (uint64_t)a.S - 1) / (uint64_t)a.S;
+  return a;
+}
+
 template <int OUT>
-hipError_t launch(const LayerNormArgs& a, void* Y, int64_t bsy, int64_t ldy, float* sX, float* mean, float* rstd,
+hipError_t launch(const LayerNormArgs& args, void* Y, int64_t bsy, int64_t ldy, float* sX, float* mean, float* rstd,
                   hipStream_t st) {
+  const LayerNormArgs a = divisor(args);
   const int64_t M = a.B * a.S;
   const Hold h = hold_norm(M, a.C);
   const int waves = h.w >= 3 ? h.w : 4;
@@ -505,9 +527,10 @@ LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, b
   return p;
 }
 
-hipError_t launch_layer_norm_grad(const LayerNormArgs& a, const void* dY, int ddtype, int64_t bsd, int64_t ldd,
+hipError_t launch_layer_norm_grad(const LayerNormArgs& args, const void* dY, int ddtype, int64_t bsd, int64_t ldd,
                                   const float* mean, const float* rstd, void* dX, int64_t bso, int64_t ldo,
                                   float* dgamma, float* dbeta, void* ws, hipStream_t st) {
+  const LayerNormArgs a = divisor(args);
   const bool sums = dgamma || dbeta;
   const LayerNormGradPlan p = plan_layer_norm_grad(a.B, a.S, a.C, a.gs != 0, sums);
   const Hold h = hold(a.C, a.C <= 8192 ? 1 : 2);

@@ -159,6 +159,8 @@ struct LayerNormArgs {
   const void* X;
   int xdtype;  // 0 fp32, 1 bf16
   int64_t bsx, ldx;
+  uint64_t div_m;  // set by the launches
+  int div_p;
 };
 // y, or its E4M3 codes and scales (rows of i8_ld(C) bytes, [blocks][M rounded up to 4]); mean and rstd [B S] may be NULL.
 hipError_t launch_layer_norm(const LayerNormArgs& a, void* Y, int ydtype, int64_t bsy, int64_t ldy, float* mean,

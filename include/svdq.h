@@ -625,7 +625,7 @@ svdq_status svdq_linear_forward_fp8(const svdq_fp8_layer* layer, int64_t M, cons
  * 16384, B <= 65535, B S < 2^31, row strides < 2^31, image strides < 2^46 (EUNSUPPORTED beyond). */
 typedef struct svdq_layer_norm_desc {
   int64_t C;
-  float eps;            /* > 0 */
+  float eps;            /* > 0 (a normal fp32 value) */
   int32_t one_plus;     /* 0 or 1 */
   const float* gamma;   /* device fp32, or NULL for a weight of 1 (whatever one_plus says) */
   const float* beta;    /* device fp32, or NULL for 0 */
