@@ -159,7 +159,7 @@ svdq_status svdq_debug_fp8_plan(const svdq_fp8_layer* layer, int64_t M, int32_t 
   if (st != SVDQ_OK || (st = check_rows(M)) != SVDQ_OK || (st = check_tiles(M, layer->N)) != SVDQ_OK) return st;
   if (M < 1 || !plan) return fail(SVDQ_EINVAL, "M must be >= 1 and plan non-NULL");
   const Fp8Plan p = plan_fp8(M, layer->K, layer->N, ydtype == SVDQ_F32);
-  plan[0] = p.tile, plan[1] = p.groups, plan[2] = p.parts, plan[3] = (int32_t)p.halved;
+  plan[0] = p.rows, plan[1] = p.cols, plan[2] = p.groups, plan[3] = p.parts;
   return ok();
 }
 

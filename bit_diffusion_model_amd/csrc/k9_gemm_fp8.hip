@@ -53,6 +53,9 @@ __device__ __forceinline__ v4f dot32(uint32_t a0, uint32_t a1, uint32_t b0, uint
 // fall in 8 different slots.  (Kernel 6's, made for 32 rows of one slot, costs 2 accesses in each here.)
 __device__ __forceinline__ int swz16(int row) { return (row & 6) | (row >> 2 & 1); }
 
+// Token rows of a stage in LDS: whole loads of 8 rows for each wave
+constexpr int tile_rows(int WM, int WN, int IA) { return (2 * IA * WM + WM * WN - 1) / (WM * WN) * WM * WN * 8; }
+
 struct Scales {
   const float *sX, *sW;
   int64_t Mp, blocks;  // length of a row of sX; blocks of 128 along K (a row of sW)
@@ -60,31 +63,32 @@ struct Scales {
 
 // ---- tiles: v_mfma_f32_32x32x64_f8f6f4, both operands through LDS
 //
-// A block owns BM x BN outputs, WM x WN waves with TI x TJ tiles of 32 x 32 each, and walks K in stages of 128 bytes,
-// which are the scales' blocks.  Operands, swizzle, barrier and the order of tiles are the integer product's (kernel 6);
+// A block owns BM x BN outputs, WM x WN waves with IA groups of 16 tokens by TJ of 32 channels each, and walks K in stages
+// of 128 bytes, which are the scales' blocks.  Operands, swizzle, barrier and the order of tiles are the integer product's (kernel 6);
 // what differs is the sum: a stage's two MFMAs of a tile start from zero, and their 16 results a lane go to the tile's
 // sums by 16 FMAs with the one factor sX[token] sW[channel block], for the weights are the A operand, so that a lane is
 // one token, and a wave's channels lie in one block of 128.  The FMAs of a tile run while the next tile's MFMAs do (two
 // sets of results in turn, the last tile's FMAs under the next stage's first MFMAs).  The tokens' scales of a stage come
 // with its operands, by 4-byte loads into LDS (a wave's 64 lanes fetch the BM / waves scales that are its share); the
 // weights' stand in a register, lane s for stage s of 64, and are read out by lane.
-template <int WM, int WN, int TI, int TJ, int KG, int ROOM, int OUT>
+template <int WM, int WN, int IA, int TJ, int KG, int ROOM, int OUT>
 __device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld, const uint8_t* __restrict__ qW,
                                      const Scales& sc, const Out& o, int64_t m0, int64_t n0, float* __restrict__ part,
                                      int64_t ldp, uint8_t* la0, uint8_t* la1, uint8_t* lb0, uint8_t* lb1, float* lx0,
                                      float* lx1) {
-  constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN, NW = WM * WN;  // NW waves per K group
-  constexpr int AB = BM * 128, BB = BN * 128, NA = AB / 1024 / NW, NB = BB / 1024 / NW, NL = NA + NB + 1;
-  constexpr int XW = BM / NW;  // token scales that a wave fetches, into a slot of 64
-  constexpr int IA = 2 * TI, JB = 2 * TJ;  // a wave's operands: groups of 16 tokens, of 16 channels
-  static_assert(AB % (1024 * NW) == 0 && BB % (1024 * NW) == 0, "whole 1 KB loads per wave");
-  static_assert(XW == 16 || XW == 32, "a share of the scales is one load, and holds whole groups of 16");
+  constexpr int BM = 16 * IA * WM, BN = 32 * TJ * WN, NW = WM * WN;  // NW waves per K group
+  // Whole 1 KB loads per wave and stage: the token rows in LDS are BM rounded up to that (the rest is not read)
+  constexpr int AB = tile_rows(WM, WN, IA) * 128, BB = BN * 128, NA = AB / 1024 / NW, NB = BB / 1024 / NW, NL = NA + NB + 1;
+  constexpr int XW = BM / NW > 16 ? 32 : 16;  // token scales that a wave fetches, into a slot of 64
+  constexpr int JB = 2 * TJ;  // a wave's operands: IA groups of 16 tokens, JB of 16 channels
+  static_assert(BB % (1024 * NW) == 0, "whole 1 KB loads per wave");
+  static_assert(XW * NW >= BM, "a share of the scales is one load, and holds whole groups of 16");
   static_assert(32 * TJ <= 128, "one block of channels to a wave");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6), wave = wid % NW, g = wid / NW;
   const int l16 = lane & 15, l4 = lane >> 4;
   const int ch = (l16 >> 2) * 8 + (l16 & 3);  // the channel of 32 that is row l16 of an even operand; 4 on: of the odd one
-  const int wr = (wave / WN) * 32 * TI, wc = (wave % WN) * 32 * TJ;
+  const int wr = (wave / WN) * 16 * IA, wc = (wave % WN) * 32 * TJ;
 
   const uint32_t rows = (uint32_t)(o.M - m0 < BM ? o.M - m0 : BM), cols = (uint32_t)(o.N - n0 < BN ? o.N - n0 : BN);
   const uint32_t blocks = (cols + 15) / 16;  // channel blocks of 16 (the last one zero past N)
@@ -129,7 +133,9 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld,
   constexpr bool FINE = OUT == 0;
   // Token operands in registers; how many groups ahead they are read; a stage's loads go out over STEPS groups, PER in each,
   // the first AHEAD of them behind the barrier, the others in the next stage
-  constexpr int RING = IA > 2 ? 4 : 2, AHEAD = IA > 4 ? 3 : IA > 2 ? 2 : 1, STEPS = IA > 4 ? 5 : IA > 2 ? 3 : 1;
+  // (7 groups a stage: with 4 sets of registers, group i in set i & 3, only two groups are ahead without meeting)
+  constexpr int RING = IA == 6 ? 3 : IA > 2 ? 4 : 2, AHEAD = IA % 8 == 0 ? 3 : IA > 2 ? 2 : 1, STEPS = IA > 4 ? 5 : IA > 2 ? 3 : 1;
+  static_assert(IA % RING == 0 || (IA % RING == 3 && AHEAD == 2), "the groups in flight lie in different sets");
   constexpr int PER = (NL + STEPS - 1) / STEPS, FIRST = PER * AHEAD < NL ? PER * AHEAD : NL;
   v4f acc[IA][JB], T[JB];
 #pragma unroll
@@ -170,7 +176,7 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld,
     }
 #pragma unroll
     for (int i = 0; i < IA; ++i) {
-      const float held = fx[(i + RING - 1) % RING];  // the factor of the group before this one
+      const float held = fx[(i + IA - 1) % IA % RING];  // the factor of the group before this one
       if (i == IA - AHEAD) {
         // every read of this stage's buffers is done or in registers: they may be filled again
         wait_vm_lgkm0<0>();
@@ -180,8 +186,8 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld,
       const int part = (i + AHEAD) % IA;  // this group's share of the loads
       const int from = part * PER, to = part < STEPS ? (from + PER < NL ? from + PER : NL) : from;
       const int ahead = (i + AHEAD) % IA;
-      fa[(i + AHEAD) % RING] = get_a(i + AHEAD < IA ? ca : na, ahead);
-      fx[(i + AHEAD) % RING] = get_x(i + AHEAD < IA ? cx : nx, ahead);
+      fa[ahead % RING] = get_a(i + AHEAD < IA ? ca : na, ahead);
+      fx[ahead % RING] = get_x(i + AHEAD < IA ? cx : nx, ahead);
       fx[i % RING] *= sw;
       Half32 ha;
       if constexpr (FINE) ha = widen(fa[i % RING]);
@@ -307,31 +313,21 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld,
   wait_vm_lgkm0<0>();  // no load into LDS outlives the block, not the last ones without a range either
 }
 
-// HALVES: the tiles from `whole` on are cut into two of half as many rows, one block each
-template <int WM, int WN, int TI, int TJ, int KG, bool HALVES, int OUT>
-__global__ __launch_bounds__(64 * WM * WN * KG, TI * TJ == 1 ? 4 : 2) void k9_tiles(
+template <int WM, int WN, int IA, int TJ, int KG, int OUT>
+__global__ __launch_bounds__(64 * WM * WN * KG, IA * TJ == 2 ? 4 : 2) void k9_tiles(
     const uint8_t* __restrict__ qX, int64_t ld, const uint8_t* __restrict__ qW, Scales sc, Out o, uint32_t tiles_m,
-    uint32_t tiles_n, uint32_t whole, float* __restrict__ part, int64_t ldp) {
-  constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN, ROOM = KG * (BM < BN ? BM : BN) * 128;
-  __shared__ __attribute__((aligned(1024))) uint8_t la0[KG * BM * 128];
-  __shared__ __attribute__((aligned(1024))) uint8_t la1[KG * BM * 128];
+    uint32_t tiles_n, float* __restrict__ part, int64_t ldp) {
+  constexpr int BM = 16 * IA * WM, BN = 32 * TJ * WN, ROWS = tile_rows(WM, WN, IA), ROOM = KG * (ROWS < BN ? ROWS : BN) * 128;
+  __shared__ __attribute__((aligned(1024))) uint8_t la0[KG * ROWS * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t la1[KG * ROWS * 128];
   __shared__ __attribute__((aligned(1024))) uint8_t lb0[KG * BN * 128];
   __shared__ __attribute__((aligned(1024))) uint8_t lb1[KG * BN * 128];
   __shared__ __attribute__((aligned(16))) float lx0[KG * WM * WN * 64], lx1[KG * WM * WN * 64];
   uint32_t m, n;
-  if (!HALVES || blockIdx.x < whole) {
-    const uint32_t xcd = blockIdx.x & 7, t8 = whole >> 3, r8 = whole & 7;
-    tile_at(xcd * t8 + (xcd < r8 ? xcd : r8) + (blockIdx.x >> 3), tiles_m, tiles_n, m, n);
-    tile<WM, WN, TI, TJ, KG, ROOM, OUT>(qX, ld, qW, sc, o, (int64_t)m * BM, (int64_t)n * BN, part, ldp, la0, la1, lb0,
-                                        lb1, lx0, lx1);
-  } else if constexpr (HALVES) {
-    const uint32_t h = blockIdx.x - whole;
-    tile_at(whole + (h >> 1), tiles_m, tiles_n, m, n);
-    const int64_t m0 = (int64_t)m * BM + (h & 1) * (BM / 2);
-    if (m0 < o.M)
-      tile<WM, WN, TI / 2, TJ, KG, ROOM, OUT>(qX, ld, qW, sc, o, m0, (int64_t)n * BN, part, ldp, la0, la1, lb0, lb1,
-                                              lx0, lx1);
-  }
+  const uint32_t xcd = blockIdx.x & 7, t8 = gridDim.x >> 3, r8 = gridDim.x & 7;
+  tile_at(xcd * t8 + (xcd < r8 ? xcd : r8) + (blockIdx.x >> 3), tiles_m, tiles_n, m, n);
+  tile<WM, WN, IA, TJ, KG, ROOM, OUT>(qX, ld, qW, sc, o, (int64_t)m * BM, (int64_t)n * BN, part, ldp, la0, la1, lb0, lb1,
+                                      lx0, lx1);
 }
 
 // The second step of a K split: the parts' sums in order, then the bias.  A thread owns 8 columns.
@@ -526,26 +522,24 @@ __global__ __launch_bounds__(64 * FEW_NW) void k9_few_layer(const T* __restrict_
   }
 }
 
-template <int WM, int WN, int TI, int TJ, int KG, bool HALVES = false>
+template <int WM, int WN, int IA, int TJ, int KG>
 void launch_tiles(const Fp8Plan& p, int64_t ld, const uint8_t* qX, const uint8_t* qW, const Scales& sc, const Out& o, float* part,
                   hipStream_t st) {
-  constexpr int BM = 32 * TI * WM, BN = 32 * TJ * WN;
+  constexpr int BM = 16 * IA * WM, BN = 32 * TJ * WN;
   const uint32_t tm = (uint32_t)((o.M + BM - 1) / BM), tn = (uint32_t)((o.N + BN - 1) / BN);
-  const uint32_t whole = HALVES ? tm * tn - (uint32_t)p.halved : tm * tn;
-  const uint32_t blocks = whole + 2 * (tm * tn - whole);
-  const dim3 grid(blocks, (uint32_t)p.parts), block(64 * WM * WN * KG);
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, qX, ld, qW, sc, o, tm, tn, whole, part, p.ldp); };
-  if constexpr (TI * TJ <= 4)  // (tiles of 256 have no registers for f16 operands)
-    if (o.ydtype == 0) return go(k9_tiles<WM, WN, TI, TJ, KG, HALVES, 0>);
-  if (o.ydtype == 1) go(k9_tiles<WM, WN, TI, TJ, KG, HALVES, 1>);
-  else go(k9_tiles<WM, WN, TI, TJ, KG, HALVES, 2>);
+  const dim3 grid(tm * tn, (uint32_t)p.parts), block(64 * WM * WN * KG);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, qX, ld, qW, sc, o, tm, tn, part, p.ldp); };
+  if constexpr (IA * TJ <= 8)  // (tiles of 256 columns have no registers for f16 operands)
+    if (o.ydtype == 0) return go(k9_tiles<WM, WN, IA, TJ, KG, 0>);
+  if (o.ydtype == 1) go(k9_tiles<WM, WN, IA, TJ, KG, 1>);
+  else go(k9_tiles<WM, WN, IA, TJ, KG, 2>);
 }
 
 // ---- the choice of kernel
 //
 // By estimated time alone (us; S = blocks of 128 along K, c = workgroups that share a compute unit; a round of c takes
-// a[c] S + b[c], a launch once more const).  The lines are least squares over 220 drawn sizes at both output kinds (256
-// CUs, launches back to back, inputs in turn; M x K x N); over those the choice costs 1% more than the best of the seven.
+// a[c] S + b[c], a launch once more const).  The lines are least squares over 650 drawn sizes (256 CUs, launches back to
+// back, inputs in turn; M x K x N); over 500 others the choice costs 1.0% (bf16) and 0.4% (fp32) more than the best.
 // bf16 outputs, then fp32 ones (whose products in f16 take twice the MFMA time and the conversions besides):
 //   few     up to 32 tokens, the weights' read: 1x3072x18432 11.2, 32x3072x18432 15.0
 //   64      one K group: 333x1000x1111 5.8 (64 x 2: 6.1, 128: 8.9) / 6.8; 154x768x2304 5.1 (5.4, 7.0) / 6.1
@@ -554,21 +548,19 @@ void launch_tiles(const Fp8Plan& p, int64_t ld, const uint8_t* qX, const uint8_t
 //           17.2, 30.8, 34.6
 //   128     4608x3072x9216 150 (64: 200) / 252 (325)
 //   128 x 2 two K groups: 1024x4096x4096 24.6 (128: 27.8, 64: 29.4) / 40.4 (44.7, 46.3)
-//   256     4608x3072x9216 127 (128: 150), 4608x12288x3072 154 (195), 2048x1280x5120 22.4 (24.6); bf16 outputs only; a
-//           last round for at most half of the CUs runs as tiles of 128 x 256
-// Tiles of 256 that a last round leaves for at most half of the CUs, after at least one whole round
-int64_t halved_tiles(int64_t M, int64_t N, int cus) {
-  const int64_t T = ((M + 255) / 256) * ((N + 255) / 256), rest = T % cus;
-  return T > cus && 2 * rest <= cus ? rest : 0;
-}
-
+//   256     4096x4096x4096 59 (128: 73); bf16 outputs only
+//   224, 192  rows by 256 columns: where they leave a last round emptier or save one.  192: 3000x5000x3500 53 (256: 62, 224:
+//           57), 6670x9062x2561 181 (214, 198), 2048x1280x5120 20 (22.8, 22), but 4608x12288x3072 222; 224: that 150 (159),
+//           4608x3072x9216 124 (126, 192: 135), 4609x2196x5826 65 (69, 81).  Over 59 drawn sizes 256 alone costs 4.7% more.
+//           (Cutting the last round's tiles of 256 into halves gained 4% on those alone and lost 4% to 192 and 224.)
 struct Cost {
   double us;
-  int tile, groups, parts;
+  int rows, cols, groups, parts;
 };
 
 Cost tiles_cost(int64_t M, int64_t N, int S, int cus, int tile, int groups, bool fine) {
-  const double T = (double)((M + tile - 1) / tile) * (double)((N + tile - 1) / tile);
+  const int cols = tile > 128 ? 256 : tile;
+  const double T = (double)((M + tile - 1) / tile) * (double)((N + cols - 1) / cols);
   const double rounds = T / cus;
   double us = 0.0;
   auto by_line = [&](const double* a, const double* b, int most) {  // a[c - 1], b[c - 1]: c blocks on a CU
@@ -577,23 +569,29 @@ Cost tiles_cost(int64_t M, int64_t N, int S, int cus, int tile, int groups, bool
     if (rest > 0) us += a[(int)(rest + 0.999999) - 1] * S + b[(int)(rest + 0.999999) - 1];
   };
   // [0] bf16 outputs, [1] fp32
-  static const double a64[2][4] = {{0.352, 0.512, 0.552, 0.712}, {0.42, 0.661, 0.903, 1.115}},
-                      b64[2][4] = {{0.52, 1.59, 2.25, 3.67}, {0.17, 1.92, 3.27, 3.97}},
-                      a642[2][2] = {{0.251, 0.361}, {0.308, 0.534}}, b642[2][2] = {{0.0, 2.08}, {0.0, 2.58}},
+  static const double a64[2][4] = {{0.334, 0.504, 0.546, 0.719}, {0.414, 0.603, 0.834, 1.062}},
+                      b64[2][4] = {{0.0, 0.88, 1.95, 2.86}, {0.0, 1.4, 2.9, 3.34}},
+                      a642[2][2] = {{0.296, 0.342}, {0.324, 0.515}}, b642[2][2] = {{0.0, 2.44}, {0.0, 2.17}},
                       a644[2][1] = {{0.2}, {0.258}}, b644[2][1] = {{5.53}, {5.94}},
-                      a128[2][2] = {{0.523, 0.819}, {0.905, 1.567}}, b128[2][2] = {{3.6, 7.46}, {2.64, 8.89}},
-                      a1282[2][1] = {{0.401}, {0.779}}, b1282[2][1] = {{6.09}, {6.55}};
-  if (tile == 64 && groups == 1) by_line(a64[fine], b64[fine], 4), us += fine ? 3.2 : 2.7;
-  else if (tile == 64 && groups == 2) by_line(a642[fine], b642[fine], 2), us += fine ? 4.3 : 4.0;
+                      a128[2][2] = {{0.629, 0.939}, {0.914, 1.58}}, b128[2][2] = {{2.31, 4.45}, {2.89, 6.71}},
+                      a1282[2][1] = {{0.485}, {0.781}}, b1282[2][1] = {{6.83}, {9.38}};
+  // tiles of 256, 224 and 192 rows, one to a CU: a step of a round of up to 30% of the CUs, of all, and between the two
+  // along a line (the more of them work, the lower their clock)
+  static const double few256[3] = {1.049, 0.945, 0.752}, all256[3] = {1.555, 1.44, 1.3}, b256[3] = {8.15, 7.19, 6.53},
+                      once[3] = {1.53, 2.32, 1.97};
+  if (tile == 64 && groups == 1) by_line(a64[fine], b64[fine], 4), us += fine ? 3.2 : 2.84;
+  else if (tile == 64 && groups == 2) by_line(a642[fine], b642[fine], 2), us += fine ? 4.1 : 3.23;
   else if (tile == 64) by_line(a644[fine], b644[fine], 1);
-  else if (tile == 128 && groups == 1) by_line(a128[fine], b128[fine], 2), us += fine ? 1.9 : 0.6;
+  else if (tile == 128 && groups == 1) by_line(a128[fine], b128[fine], 2), us += fine ? 3.77 : 2.1;
   else if (tile == 128) by_line(a1282[fine], b1282[fine], 1);
   else {
+    const int h = (256 - tile) / 32;  // 256, 224, 192 rows
     const double full = (double)(int64_t)rounds, rest = rounds - full;
-    const bool halved = full > 0 && rest <= 0.5;
-    us = full * (1.067 * S + 8.3) + (rest == 0 ? 0.0 : (halved ? 0.78 : rest <= 0.625 ? 0.93 : 1.067) * S + 8.3);
+    const double u = rest <= 0.3 ? 0.0 : (rest - 0.3) / 0.7;
+    us = full * (all256[h] * S + b256[h]) + once[h];
+    if (rest > 0) us += ((1 - u) * few256[h] + u * all256[h]) * S + b256[h];
   }
-  return Cost{us, tile, groups, 1};
+  return Cost{us, tile, cols, groups, 1};
 }
 
 }  // namespace
@@ -602,13 +600,14 @@ Fp8Plan plan_fp8(int64_t M, int64_t K, int64_t N, bool fine) {
   const int cus = device_cus();
   const int64_t ld = i8_ld(K), ldp = (N + 7) / 8 * 8;
   const int S = (int)(ld / 128);
-  Cost best{1e30, 64, 1, 1};
+  Cost best{1e30, 64, 64, 1, 1};
   auto take = [&](const Cost& c) {
     if (c.us < best.us) best = c;
   };
   take(tiles_cost(M, N, S, cus, 64, 1, fine));
   take(tiles_cost(M, N, S, cus, 128, 1, fine));
-  if (!fine) take(tiles_cost(M, N, S, cus, 256, 1, fine));
+  if (!fine)
+    for (int rows : {256, 224, 192}) take(tiles_cost(M, N, S, cus, rows, 1, fine));
   const int64_t T64 = ((M + 63) / 64) * ((N + 63) / 64), T128 = ((M + 127) / 128) * ((N + 127) / 128);
   if (T128 <= cus) take(tiles_cost(M, N, S, cus, 128, 2, fine));
   if (T64 <= 2 * cus) take(tiles_cost(M, N, S, cus, 64, 2, fine));
@@ -621,9 +620,8 @@ Fp8Plan plan_fp8(int64_t M, int64_t K, int64_t N, bool fine) {
       take(c);
     }
   }
-  if (M <= 32) take(Cost{3.0 + (double)(N * ld) * 1e-6 * (0.11 + 0.009 * (double)M), 0, 1, 1});
-  Fp8Plan p{best.tile, best.groups, best.parts, ldp, 0, 0};
-  if (p.tile == 256) p.halved = halved_tiles(M, N, cus);
+  if (M <= 32) take(Cost{3.0 + (double)(N * ld) * 1e-6 * (0.11 + 0.009 * (double)M), 0, 16, 1, 1});
+  Fp8Plan p{best.rows, best.cols, best.groups, best.parts, ldp, 0};
   if (p.parts > 1) p.bytes = (size_t)p.parts * (size_t)M * (size_t)ldp * 4;
   return p;
 }
@@ -660,20 +658,21 @@ hipError_t launch_gemm_fp8(int64_t M, int64_t K, int64_t N, const uint8_t* qX, c
   const Out o{nullptr, nullptr, bias, Y, ldy, M, N, ydtype};
   const Scales sc{sX, sW, fp8_pad(M), fp8_blocks(K)};
   const Fp8Plan p = plan_fp8(M, K, N, ydtype == 0);
-  if (p.tile == 0) {
+  if (p.rows == 0) {
     const dim3 g((uint32_t)((N + 15) / 16)), b(64 * FEW_NW);
     if (M <= 16) hipLaunchKernelGGL(k9_few<1>, g, b, 0, st, qX, ld, qW, sc, o);
     else hipLaunchKernelGGL(k9_few<2>, g, b, 0, st, qX, ld, qW, sc, o);
     return hipGetLastError();
   }
   float* part = p.parts > 1 ? static_cast<float*>(ws) : nullptr;
-  if (p.tile == 256 && p.halved) launch_tiles<2, 4, 4, 2, 1, true>(p, ld, qX, qW, sc, o, part, st);
-  else if (p.tile == 256) launch_tiles<2, 4, 4, 2, 1>(p, ld, qX, qW, sc, o, part, st);
-  else if (p.tile == 128 && p.groups == 1) launch_tiles<2, 2, 2, 2, 1>(p, ld, qX, qW, sc, o, part, st);
-  else if (p.tile == 128) launch_tiles<2, 2, 2, 2, 2>(p, ld, qX, qW, sc, o, part, st);
-  else if (p.groups == 1) launch_tiles<2, 2, 1, 1, 1>(p, ld, qX, qW, sc, o, part, st);
-  else if (p.groups == 2) launch_tiles<2, 2, 1, 1, 2>(p, ld, qX, qW, sc, o, part, st);
-  else launch_tiles<2, 2, 1, 1, 4>(p, ld, qX, qW, sc, o, part, st);
+  if (p.rows == 256) launch_tiles<2, 4, 8, 2, 1>(p, ld, qX, qW, sc, o, part, st);
+  else if (p.rows == 224) launch_tiles<2, 4, 7, 2, 1>(p, ld, qX, qW, sc, o, part, st);
+  else if (p.rows == 192) launch_tiles<2, 4, 6, 2, 1>(p, ld, qX, qW, sc, o, part, st);
+  else if (p.rows == 128 && p.groups == 1) launch_tiles<2, 2, 4, 2, 1>(p, ld, qX, qW, sc, o, part, st);
+  else if (p.rows == 128) launch_tiles<2, 2, 4, 2, 2>(p, ld, qX, qW, sc, o, part, st);
+  else if (p.groups == 1) launch_tiles<2, 2, 2, 1, 1>(p, ld, qX, qW, sc, o, part, st);
+  else if (p.groups == 2) launch_tiles<2, 2, 2, 1, 2>(p, ld, qX, qW, sc, o, part, st);
+  else launch_tiles<2, 2, 2, 1, 4>(p, ld, qX, qW, sc, o, part, st);
   if (p.parts > 1)
     hipLaunchKernelGGL(k9_join, dim3((uint32_t)((M * (p.ldp / 8) + 255) / 256)), dim3(256), 0, st, part, p.parts, p.ldp, o);
   return hipGetLastError();

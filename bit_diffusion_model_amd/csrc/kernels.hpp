@@ -110,8 +110,13 @@ hipError_t launch_w8a8(int64_t M, int64_t K, int64_t N, const int8_t* qX, const 
 // E4M3 codes and scales of X [M][ldx] (xdtype 0 fp32, 1 bf16).
 hipError_t launch_quant_fp8(int64_t M, int64_t K, const void* X, int xdtype, int64_t ldx, uint8_t* qX, float* sX,
                             hipStream_t st);
-// How the product runs on the current device; the fields are W8A8Plan's (partial sums in fp32).
-typedef W8A8Plan Fp8Plan;
+// How the product runs on the current device: tiles of rows x cols (rows 0: the kernel for few tokens, 16 channels to a
+// block), K groups within a block, K parts, a row of the parts' fp32 sums and their bytes.
+struct Fp8Plan {
+  int rows, cols, groups, parts;
+  int64_t ldp;
+  size_t bytes;
+};
 Fp8Plan plan_fp8(int64_t M, int64_t K, int64_t N, bool fine);  // fine: for fp32 outputs
 // Whether the layer runs as one launch for few tokens (which quantizes inside), and that launch.
 bool few_layer_fp8(int64_t M, int64_t K);

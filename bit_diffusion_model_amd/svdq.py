@@ -1050,7 +1050,7 @@ class Fp8Linear:
         return out
 
     def plan(self, M: int, ydtype: int = F32):
-        """svdq_debug_fp8_plan: (tile, K groups, K parts, halved tiles) of the product of M rows."""
+        """svdq_debug_fp8_plan: (tile rows, tile columns, K groups, K parts) of the product of M rows."""
         p = (ctypes.c_int32 * 4)()
         _check(lib().svdq_debug_fp8_plan(self._ref, M, ydtype, p))
         return tuple(p)

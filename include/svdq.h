@@ -674,7 +674,8 @@ svdq_status svdq_layer_norm_backward(const svdq_layer_norm_desc* norm, int64_t B
  *     that run as halves}; the product of M rows, alone or in a layer.
  *   svdq_debug_group_norm_plan: plan = {1 where one launch serves the norm, 1 where the blocks' statistics are joined by
  *     a launch of their own, statistics blocks and output blocks per image}.
- *   svdq_debug_fp8_plan: as svdq_debug_w8a8_plan, for the block-scaled product into a svdq_dtype.
+ *   svdq_debug_fp8_plan: plan = {rows and columns of a tile (0, 16: the kernel for few tokens), K groups, K parts}; the
+ *     block-scaled product of M rows into a svdq_dtype.
  *   svdq_debug_layer_norm_plan: plan = {lanes that hold a row (16, 32 or 64), chunks of 8 values to a lane, waves to a row,
  *     blocks whose column sums the gradient joins for each gamma (1: no second launch)}.
  * EINVAL / EUNSUPPORTED as the calls themselves; host only, nothing is launched. */

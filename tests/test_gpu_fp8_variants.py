@@ -10,19 +10,24 @@ import pytest
 from bit_diffusion_model_amd import svdq
 from oracle import fp8 as o
 
-# (M, K, N): plans for fp32 and for bf16 outputs: (tile, K groups, K parts, halved tiles)
+# (M, K, N): plans for fp32 and for bf16 outputs: (rows and columns of a tile, K groups, K parts)
 VARIANTS = {
-    (9, 9001, 999): ((0, 1, 1, 0), (0, 1, 1, 0)),
-    (31, 2944, 200): ((0, 1, 1, 0), (0, 1, 1, 0)),
-    (333, 1000, 1111): ((64, 1, 1, 0), (64, 2, 1, 0)),
-    (501, 2100, 3001): ((64, 2, 1, 0), (64, 2, 1, 0)),
-    (200, 5000, 1023): ((64, 4, 4, 0), (64, 4, 1, 0)),
-    (70, 9001, 999): ((64, 4, 8, 0), (64, 4, 8, 0)),
-    (4090, 301, 2051): ((64, 1, 1, 0), (256, 1, 1, 0)),
-    (1029, 3100, 2999): ((128, 2, 1, 0), (128, 2, 1, 0)),
-    (8195, 650, 643): ((64, 1, 1, 0), (128, 1, 1, 0)),
-    (2500, 1000, 9301): ((128, 1, 1, 0), (256, 1, 1, 114)),  # the last tile row holds 196 rows: both of its halves
-    (2305, 1900, 9203): ((128, 1, 1, 0), (256, 1, 1, 104)),  # .. 1 row: the second half is empty
+    (9, 9001, 999): ((0, 16, 1, 1), (0, 16, 1, 1)),
+    (31, 2944, 200): ((0, 16, 1, 1), (0, 16, 1, 1)),
+    (333, 1000, 1111): ((64, 64, 1, 1), (64, 64, 1, 1)),
+    (501, 2100, 3001): ((64, 64, 1, 1), (64, 64, 2, 1)),
+    (32, 3000, 18432): ((64, 64, 2, 1), (64, 64, 2, 1)),
+    (200, 5000, 1023): ((64, 64, 4, 4), (64, 64, 4, 1)),
+    (70, 9001, 999): ((64, 64, 4, 8), (64, 64, 4, 8)),
+    (1029, 3100, 2999): ((128, 128, 2, 1), (128, 128, 2, 1)),
+    (8195, 650, 643): ((64, 64, 1, 1), (128, 128, 1, 1)),
+    (2500, 1000, 9301): ((128, 128, 1, 1), (128, 128, 1, 1)),
+    (4090, 301, 2051): ((64, 64, 1, 1), (192, 256, 1, 1)),
+    (2305, 1900, 9203): ((128, 128, 1, 1), (192, 256, 1, 1)),  # the last tile row holds 1 row
+    (2323, 1483, 5205): ((64, 64, 1, 1), (224, 256, 1, 1)),  # .. 83: four of its waves none
+    (4701, 2196, 2601): ((64, 64, 1, 1), (224, 256, 1, 1)),  # .. 221: its last wave half full
+    (2685, 1299, 5584): ((128, 128, 1, 1), (256, 256, 1, 1)),
+    (4090, 600, 4090): ((128, 128, 1, 1), (256, 256, 1, 1)),
 }
 TYPES = {"f32": svdq.F32, "bf16": svdq.BF16, "gelu": svdq.BF16_GELU}
 
