@@ -127,8 +127,8 @@ struct Chunks<T, 16, VEC> : Chunks<T, 32, VEC> {
   using Chunks<T, 32, VEC>::Chunks;
 };
 
-// Most waves of a block whose rows are held in NC chunks (at C = 16384)
-constexpr int norm_waves(int NC) { return NC <= 2 ? 16 : NC == 3 ? 11 : 8; }
+// Most waves of a block whose rows are held in NC chunks (hold_norm)
+constexpr int norm_waves(int NC) { return NC == 1 ? 4 : NC == 2 ? 13 : NC == 3 ? 10 : 8; }
 
 // OUT: 0 fp32, 1 bf16, 2 codes.  w waves to a row.
 // Y may be X: a row is loaded whole, by the team that stores it, before it is stored.
@@ -441,11 +441,14 @@ void by_chunks(int NC, F&& f) {
   (void)((NC == NCs ? (f(std::integral_constant<int, L>{}, std::integral_constant<int, NCs>{}), true) : false) || ...);
 }
 
-// Where the rows fill the card with few waves each, those that leave the fewest lanes idle; else more waves of one
-// chunk.
+// Few rows: one chunk a lane, so long as that is at most 4 waves; then two, and past 8192 values four, since a join of many
+// waves costs more than their loads save (bf16: 8 x 8192 in 16, 8, 4 waves 5.1, 4.1, 4.1 us; 300 x 3072 in 6, 3, 2: 4.65, 3.97,
+// 3.92; 400 x 1500 in 3, 2, 1: 3.66, 3.84, 3.69).
+// Else what leaves the fewest lanes idle in the fewest waves: 100000 x 320 by 16 lanes 34 us (64: 48), 100000 x 768 by 32 lanes
+// 60 (64 lanes: 88), 4608 x 3072 by 64 lanes of 3 chunks 13.4 (1: 23.0, 2: 14.8, 4: 14.0), 16384 x 2048 of 4 30 (1: 38, 2: 34).
 Hold hold_norm(int64_t M, int C) {
   const int one = (C + 511) / 512;  // waves of one chunk
-  if (M * one < 16 * (int64_t)device_cus()) return hold(C, one <= MAX_WAVES ? 1 : 2);
+  if (M * one < (C <= 1024 ? 16 : 8) * (int64_t)device_cus()) return hold(C, one <= 4 ? 1 : one <= MAX_WAVES ? 2 : 4);
   if (C <= 512) return Hold{16, (C + 127) / 128, 1};
   if (C <= 1024) return Hold{32, (C + 255) / 256, 1};
   Hold best = hold(C, 2);

@@ -33,7 +33,8 @@ TYPES = {"f32": svdq.F32, "bf16": svdq.BF16, "gelu": svdq.BF16_GELU}
 
 # (B, S, C): (lanes, chunks, waves to a row, blocks of the gradient)
 NORMS = {
-    (1, 5, 100): (16, 1, 1, 1), (1, 5, 200): (32, 1, 1, 1), (1, 5, 700): (64, 1, 2, 1), (1, 5, 9000): (64, 2, 9, 5),
+    (1, 5, 100): (16, 1, 1, 1), (1, 5, 200): (32, 1, 1, 1), (1, 5, 700): (64, 1, 2, 1), (1, 5, 2041): (64, 1, 4, 1),
+    (1, 5, 8001): (64, 2, 8, 5), (1, 5, 9000): (64, 4, 5, 5),
     (1, 5000, 100): (16, 1, 1, 79), (1, 5000, 250): (16, 2, 1, 157), (1, 5000, 300): (16, 3, 1, 157),
     (1, 5000, 500): (16, 4, 1, 157), (1, 5000, 700): (32, 3, 1, 209), (1, 5000, 1000): (32, 4, 1, 209),
     (1, 3000, 1300): (64, 3, 1, 200), (2, 1500, 2047): (64, 4, 1, 250), (1, 2100, 3001): (64, 3, 2, 210),
@@ -71,6 +72,7 @@ def test_every_row_has_its_lanes():
             step = 8 * lanes * waves
             assert step * chunks >= svdq.int8_ld(C) and 1 <= waves <= 16 and 512 * (waves - 1) < C
             assert (chunks - (2 if lanes == 64 else 1)) * step <= C
+            assert waves <= {1: 4, 2: 13, 3: 10, 4: 8}[chunks]  # what the kernels are compiled for
 
 
 def test_plan_refusals():
