@@ -6,7 +6,8 @@
 // Design (gfx950): bound by HBM (x read once, a byte per value written).  Blocks of 128 are independent, so a row
 // needs no join: 16 lanes hold a block, 8 values each, and meet by lane moves.  A workgroup takes 16 rows x 512
 // values, four rows a wave, all four loads in flight; the 64 scales meet in LDS and leave as four runs of 16 (the
-// scales' rows run along the tokens, which is how the product reads them).
+// scales' rows run along the tokens, which is how the product reads them).  4608 x 3072 bf16 9.2 us, 16384 x 2048 21.2: 4.7 and
+// 4.8 TB/s of what a large copy reaches 5.1.
 #include "fp8.hpp"
 #include "kernels.hpp"
 

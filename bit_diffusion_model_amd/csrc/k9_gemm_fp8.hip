@@ -5,8 +5,13 @@
 // fp32, then optionally GELU, rounded once to the output type.  qX comes as rows of ld bytes, sX as rows of Mp = M
 // rounded up to 4 along the tokens; qW in the fragment order of svdq_prepare_weights_int8: [N / 16][ld / 64] fragments
 // of 1 KB, lane l of a fragment holding channel l & 15 and the 16 codes k = 16 (l >> 4) .., N padded to 16 with zeros.
-// The matrix core takes 64 codes of K (32 x 32 tiles) or 128 (16 x 16) at once, 32 to a lane; a lane's 32 are two
-// 16-byte pieces of a fragment, the same pieces for both operands: a sum does not ask in which order k comes.
+// The matrix core takes 128 codes of K (a block) of 16 x 16 outputs at once, 32 to a lane; a lane's 32 are two 16-byte
+// pieces of a fragment, the same pieces for both operands: a sum does not ask in which order k comes.
+//
+// Accuracy: on E4M3 operands the matrix core lines up the products of 8 successive codes by the largest one and drops
+// what lies below 2^-13 of its binade (measured: 1.4e-5 to 6e-5 of a sum of random codes).  A bf16 output rounds by
+// 2^-8, so those come from it; fp32 outputs, and the few-token kernels of either type (bound by the weights' read), widen
+// the codes to f16, exactly, whose products are kept whole in the fp32 sum: twice the MFMA time and the conversions.
 #include <type_traits>
 
 #include "fp8.hpp"
@@ -61,16 +66,21 @@ struct Scales {
   int64_t Mp, blocks;  // length of a row of sX; blocks of 128 along K (a row of sW)
 };
 
-// ---- tiles: v_mfma_f32_32x32x64_f8f6f4, both operands through LDS
+// ---- tiles: v_mfma_f32_16x16x128_f8f6f4 (fp32 outputs: 4 v_mfma_f32_16x16x32_f16), both operands through LDS
 //
 // A block owns BM x BN outputs, WM x WN waves with IA groups of 16 tokens by TJ of 32 channels each, and walks K in stages
-// of 128 bytes, which are the scales' blocks.  Operands, swizzle, barrier and the order of tiles are the integer product's (kernel 6);
-// what differs is the sum: a stage's two MFMAs of a tile start from zero, and their 16 results a lane go to the tile's
-// sums by 16 FMAs with the one factor sX[token] sW[channel block], for the weights are the A operand, so that a lane is
-// one token, and a wave's channels lie in one block of 128.  The FMAs of a tile run while the next tile's MFMAs do (two
-// sets of results in turn, the last tile's FMAs under the next stage's first MFMAs).  The tokens' scales of a stage come
-// with its operands, by 4-byte loads into LDS (a wave's 64 lanes fetch the BM / waves scales that are its share); the
-// weights' stand in a register, lane s for stage s of 64, and are read out by lane.
+// of 128 bytes, which are the scales' blocks.  Loads into LDS, barrier and the order of tiles are the integer product's
+// (kernel 6); what differs is the sum: an MFMA starts from zero, and its 4 results a lane go to the tile's sums by 4 FMAs
+// with the one factor sX[token] sW[channel block], for the weights are the A operand, so that a lane is one token, and a
+// wave's channels lie in one block of 128.  The FMAs of a group of 16 tokens run under the next group's MFMAs, the last
+// group's under the next stage's first (MFMAs of 32 x 32 x 64 want two of them and 16 FMAs a tile, and registers for two
+// sets of results: 186 us against 178 at 4608 x 12288 x 3072).  Operands are read 2 or 3 groups before their use (165 for
+// 178), a stage's loads spread over its groups (159 for 163), the tokens' scales come with the operands, by 4-byte loads
+// into LDS (a wave's 64 lanes fetch the scales that are its share); the weights' stand in a register, lane s for stage s of
+// 64, and are read out by lane.
+// Bound (4608 x 12288 x 3072 bf16, 150 us, 2.3 POP/s; 4608 x 3072 x 9216 124, 2.1): the matrix cores are busy 77% of a
+// busy unit's cycles, and the clock falls to 1.85 - 2.05 GHz under them: without the FMAs it takes as long.  fp32 outputs
+// (512 x 9216 x 3072 45 us): the conversions, at half the vector rate, twice for each operand in tiles of 64.
 template <int WM, int WN, int IA, int TJ, int KG, int ROOM, int OUT>
 __device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld, const uint8_t* __restrict__ qW,
                                      const Scales& sc, const Out& o, int64_t m0, int64_t n0, float* __restrict__ part,
@@ -437,7 +447,8 @@ __global__ __launch_bounds__(64 * FEW_NW) void k9_few(const uint8_t* __restrict_
 // values each, so a workgroup does 128 of the M x nb at a time (one step up to 5 tokens of 3072 values), its first weights
 // on their way; codes and scales go to LDS, and each wave takes the NU blocks that are its share of K (b = wave, wave +
 // 8, ..) from there to registers.  Every workgroup repeats this (X is small and in L2), so it stays and takes `turns`
-// channel blocks, the next one's weights on their way while one's sums meet in LDS.
+// channel blocks, the next one's weights on their way while one's sums meet in LDS (a workgroup to each channel block, every
+// one of which quantizes: 24 us for 12 at 1x3072x18432; 57 MB at 4.7 TB/s).
 template <typename T, int NU>
 __global__ __launch_bounds__(64 * FEW_NW) void k9_few_layer(const T* __restrict__ X, int64_t ldx, int K, int64_t ld,
                                                             const uint8_t* __restrict__ qW, Scales sc, Out o, int turns) {
@@ -626,6 +637,9 @@ Fp8Plan plan_fp8(int64_t M, int64_t K, int64_t N, bool fine) {
   return p;
 }
 
+// Up to 256 blocks of X: with a bf16 output 1x3072x18432 takes 11.7 us in one launch and 13.0 in two, 10x3072x18432 13.0 and
+// 17.2, 1x768x768 3.6 and 5.2, 8x3072x9216 10.5 and 10.0; 12x4096x4096 (384 blocks) 9.0 and 8.8, 16x4096x16384 19.5 and 19.3.
+// A launch more is 3 us of the caller's time besides.
 bool few_layer_fp8(int64_t M, int64_t K) { return M <= 16 && K <= 4 * FEW_NW * 128 && M * fp8_blocks(K) <= 256; }
 
 hipError_t launch_few_layer_fp8(int64_t M, int64_t K, int64_t N, const void* X, int xdtype, int64_t ldx,

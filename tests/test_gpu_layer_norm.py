@@ -334,3 +334,22 @@ def test_block_forward_and_backward():
             assert torch.equal(got, ref)
         step(xs[2], dys[2])
         torch.cuda.synchronize()
+
+
+def test_example_runs_and_its_gradients():
+    """examples/modulated_block_fp8.py: norm, two layers and back through them; the codes' error of y and each gradient."""
+    import importlib.util
+    import os
+    import sys
+    from unittest import mock
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "modulated_block_fp8.py")
+    spec = importlib.util.spec_from_file_location("modulated_block_fp8", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    with mock.patch.object(sys, "argv", ["x", "--images", "2", "--rows", "77", "--channels", "320"]):
+        errors = m.main()
+    # a code is off by at most 2^-4 of its value, 2^-4 / sqrt(3) in the mean square; a product has two such operands, and y
+    # and each gradient come through two products and a GELU or its derivative at a value that is off by one product's error
+    assert sorted(errors) == ["dscale", "dshift", "dx", "y"]
+    assert max(errors.values()) < 3 * np.sqrt(2) * 2.0 ** -4 / np.sqrt(3)
