@@ -168,8 +168,8 @@ svdq_status svdq_debug_layer_norm_plan(const svdq_layer_norm_desc* norm, int64_t
   if (st != SVDQ_OK) return st;
   if (B < 1 || S < 1 || !plan) return fail(SVDQ_EINVAL, "B and S must be >= 1 and plan non-NULL");
   const LayerNormPlan p = plan_layer_norm(B * S, (int)norm->C);
-  const LayerNormGradPlan g = plan_layer_norm_grad(B, S, (int)norm->C, norm->image_stride != 0, true);
-  plan[0] = p.lanes, plan[1] = p.chunks, plan[2] = p.waves, plan[3] = (int32_t)g.parts;
+  const LayerNormGradPlan g = plan_layer_norm_grad(B, S, (int)norm->C, norm->image_stride != 0, true, true);
+  plan[0] = p.lanes, plan[1] = p.chunks, plan[2] = p.waves, plan[3] = g.cw ? -g.cw : (int32_t)g.parts;
   return ok();
 }
 
@@ -237,7 +237,7 @@ svdq_status svdq_norm_linear_forward_fp8(const svdq_layer_norm_desc* norm, const
 
 size_t svdq_layer_norm_backward_workspace_bytes(const svdq_layer_norm_desc* norm, int64_t B, int64_t S) {
   if (check_layer_norm(norm, B, S) != SVDQ_OK || B == 0 || S == 0) return 0;
-  return rup(plan_layer_norm_grad(B, S, (int)norm->C, norm->image_stride != 0, true).bytes);
+  return rup(plan_layer_norm_grad(B, S, (int)norm->C, norm->image_stride != 0, true, false).bytes);
 }
 
 svdq_status svdq_layer_norm_backward(const svdq_layer_norm_desc* norm, int64_t B, int64_t S, const void* dY,

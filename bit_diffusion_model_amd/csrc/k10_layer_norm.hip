@@ -12,12 +12,12 @@
 // M2 = sum d^2 - (sum d)^2 / n, so that neither a mean far from zero nor the rounding of p costs digits (a constant row
 // gives beta).  Waves join by the pairwise formula (Chan, Golub and LeVeque) about the first one's mean, at one barrier.
 // The columns' sums of the gradient stay in registers over a block's rows, the next row on its way while one is
-// computed; a block joins its teams in LDS and leaves one partial sum; a second launch adds the blocks'.  Every
-// order is fixed: no atomics.
+// computed; a block joins its teams in LDS and leaves one partial sum; a second launch adds the blocks'; for few rows
+// blocks of their own sum the columns in the same launch.  Every order is fixed: no atomics.
 // Measured: 65536 x 4096 fp32 425 us (5.05 TB/s, a large copy 5.1); 2 x 4608 x 3072 bf16, modulated, 27.8 (4.1 TB/s: the vector
 // units are busy two thirds of the time, 411 instructions a wave of 24 values a lane); 4608 x 3072 to codes 14.3 (593, busy
 // 77%; kernel 8 on a written y 9.2); gradient 2 x 4608 x 3072 bf16 39 (35 and the second launch's 4; 4.3 TB/s),
-// 3 x 333 x 1111 fp32 10.7 (7.6 + 3.1).
+// 3 x 333 x 1111 fp32 9.2 in one launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -247,21 +247,33 @@ __global__ __launch_bounds__(64 * norm_waves(NC)) void k10_norm(LayerNormArgs a,
   }
 }
 
-// The gradient.  Rows are in `images` runs of `len` (the images, or all rows as one run); a block takes rows
-// [blockIdx.x * per, + per) of run blockIdx.y and leaves its columns' sums in part[run][blockIdx.x][2][C], or with one
-// block to a run in dgamma and dbeta [run][C] themselves.  SUMS: whether they are wanted.
+// The gradient.  Rows are in `images` runs of `len` (the images, or all rows as one run); block `block` of `blocks` takes
+// rows [block * per, + per) of run blockIdx.y and leaves its columns' sums in part[run][block][2][C], or with one block to a
+// run in dgamma and dbeta [run][C] themselves.  SUMS: whether it does.
 // dX may be X or dY: a row is loaded whole, by the block that stores it, before it is stored.
+template <typename T, typename TD>
+struct GradArgs {
+  const TD* dY;
+  int64_t bsd, ldd;
+  const float *mean, *rstd;
+  T* dX;
+  int64_t bso, ldo;
+  float *part, *dgamma, *dbeta;
+};
+
 template <typename T, typename TD, int L, int NC, bool SUMS, bool VEC>
-__global__ __launch_bounds__(1024) void k10_grad(LayerNormArgs a, int w, int64_t len, int64_t per, const TD* dY,
-                                                int64_t bsd, int64_t ldd, const float* __restrict__ mean_in,
-                                                const float* __restrict__ rstd_in, T* dX, int64_t bso, int64_t ldo,
-                                                float* __restrict__ part, float* __restrict__ dgamma,
-                                                float* __restrict__ dbeta) {
+__device__ __forceinline__ void grad_rows(const LayerNormArgs& a, int w, int64_t len, int64_t per, const GradArgs<T, TD>& g,
+                                          uint32_t block, uint32_t blocks) {
+  const TD* dY = g.dY;
+  T* dX = g.dX;
+  const int64_t bsd = g.bsd, ldd = g.ldd, bso = g.bso, ldo = g.ldo;
+  const float *__restrict__ mean_in = g.mean, *__restrict__ rstd_in = g.rstd;
+  float *__restrict__ part = g.part, *__restrict__ dgamma = g.dgamma, *__restrict__ dbeta = g.dbeta;
   extern __shared__ float cols[];  // [teams][2][step * NC], where several meet
   __shared__ float2 meet[2][MAX_WAVES];
   const Seat<L> at(w);
   const int C = a.C, step = (L == 64 ? 64 * w : L) * 8;
-  const int64_t base = (int64_t)blockIdx.y * len, r0 = base + (int64_t)blockIdx.x * per;
+  const int64_t base = (int64_t)blockIdx.y * len, r0 = base + (int64_t)block * per;
   const int64_t r1 = r0 + per < base + len ? r0 + per : base + len;
   auto whole = [&](int j) { return L == 64 && (j + 1) * step <= C; };
   struct Row1 {
@@ -370,9 +382,9 @@ __global__ __launch_bounds__(1024) void k10_grad(LayerNormArgs a, int w, int64_t
         }
     }
     const int teams = L == 64 ? at.rpb : (int)(blockDim.x >> 6), wide = step * NC;
-    const int64_t run = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-    float* pg = gridDim.x > 1 ? part + run * 2 * C : dgamma ? dgamma + run * C : nullptr;
-    float* pb = gridDim.x > 1 ? part + run * 2 * C + C : dbeta ? dbeta + run * C : nullptr;
+    const int64_t run = (int64_t)blockIdx.y * blocks + block;
+    float* pg = blocks > 1 ? part + run * 2 * C : dgamma ? dgamma + run * C : nullptr;
+    float* pb = blocks > 1 ? part + run * 2 * C + C : dbeta ? dbeta + run * C : nullptr;
     const bool mine = L == 64 || (int)(threadIdx.x & 63) < L;  // one group of a wave's lanes has its sums
     if (teams == 1) {
 #pragma unroll
@@ -403,6 +415,79 @@ __global__ __launch_bounds__(1024) void k10_grad(LayerNormArgs a, int w, int64_t
       if (pb) pb[c] = b;
     }
   }
+}
+
+template <typename T, typename TD, int L, int NC, bool SUMS, bool VEC>
+__global__ __launch_bounds__(1024) void k10_grad(LayerNormArgs a, int w, int64_t len, int64_t per, GradArgs<T, TD> g) {
+  grad_rows<T, TD, L, NC, SUMS, VEC>(a, w, len, per, g, blockIdx.x, gridDim.x);
+}
+
+// The columns' sums of a run, cw = 16, 32 or 64 columns to a block and 64 / cw rows to a wave: the forward's mean and
+// rstd are known, so nothing of a row has to meet first.
+__device__ __forceinline__ float as_f32(float v) { return v; }
+__device__ __forceinline__ float as_f32(uint16_t bf16) { return __uint_as_float((uint32_t)bf16 << 16); }
+template <typename T, typename TD>
+__device__ __forceinline__ void grad_cols(const LayerNormArgs& a, int64_t len, const GradArgs<T, TD>& g, uint32_t block,
+                                          int cw) {
+  constexpr int U = 8;  // rows on their way
+  __shared__ float2 sums[MAX_WAVES][64];
+  const int C = a.C, lane = threadIdx.x & 63, c = (int)block * cw + (lane & (cw - 1)), slots = (int)blockDim.x / cw;
+  // the run's first row; within a run 32 bits of bytes reach (the launch sees to it)
+  const int64_t base = (int64_t)blockIdx.y * len;
+  const char* X = (const char*)(static_cast<const T*>(a.X) + (int64_t)blockIdx.y * a.bsx);
+  const char* D = (const char*)(g.dY + (int64_t)blockIdx.y * g.bsd);
+  const float *mean_in = g.mean + base, *rstd_in = g.rstd + base;
+  const uint32_t ldx = (uint32_t)a.ldx * sizeof(T), ldd = (uint32_t)g.ldd * sizeof(TD), rows = (uint32_t)len;
+  const uint32_t at = c < C ? c : 0;
+  float sg = 0.0f, sb = 0.0f;
+  for (uint32_t r = threadIdx.x / cw; r < rows; r += slots * U) {
+    T x[U];
+    TD d[U];
+    float mean[U], rstd[U];
+    const uint32_t ox = r * ldx + at * sizeof(T), od = r * ldd + at * sizeof(TD);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = r + u * slots < rows;  // else row r once more
+      x[u] = *reinterpret_cast<const T*>(X + (in ? ox + u * (slots * ldx) : ox));
+      d[u] = *reinterpret_cast<const TD*>(D + (in ? od + u * (slots * ldd) : od));
+      mean[u] = mean_in[in ? r + u * slots : r], rstd[u] = rstd_in[in ? r + u * slots : r];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float dv = r + u * slots < rows ? as_f32(d[u]) : 0.0f, z = (as_f32(x[u]) - mean[u]) * rstd[u];
+      if (r + u * slots < rows) sg = fmaf(dv, z, sg);
+      sb += dv;
+    }
+  }
+  auto add = [&](float v) {  // a wave's rows
+    if (cw == 16) {
+      const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+      v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if (cw <= 32) {
+      const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+      v = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+    }
+    return v;
+  };
+  sums[threadIdx.x >> 6][lane] = make_float2(add(sg), add(sb));
+  __syncthreads();
+  if ((int)threadIdx.x < cw && c < C) {
+    float2 s = sums[0][lane];
+    for (int i = 1; i < (int)(blockDim.x >> 6); ++i) s.x += sums[i][lane].x, s.y += sums[i][lane].y;
+    if (g.dgamma) g.dgamma[(int64_t)blockIdx.y * C + c] = s.x;
+    if (g.dbeta) g.dbeta[(int64_t)blockIdx.y * C + c] = s.y;
+  }
+}
+
+// Up to 1024 rows: dX and the columns' sums in one launch, by blocks of their own, which read x and dy once more (fp32
+// 16 x 1111 4.6 us, with a second launch 10.5; 400 x 1111 5.5, 9.0; 999 x 1111 9.6, 11.2; 999 x 3072 13.4, 15.8; 1400 x 3072
+// 17.6, 17.0)
+template <typename T, typename TD, int L, int NC, bool VEC>
+__global__ __launch_bounds__(1024) void k10_grad_apart(LayerNormArgs a, int w, int64_t len, int64_t per, GradArgs<T, TD> g,
+                                                      int cw, uint32_t col_blocks) {
+  if (blockIdx.x < col_blocks) grad_cols<T, TD>(a, len, g, blockIdx.x, cw);
+  else grad_rows<T, TD, L, NC, false, VEC>(a, w, len, per, g, blockIdx.x - col_blocks, gridDim.x - col_blocks);
 }
 
 // The blocks' partial sums of a run, added in a fixed order: 32 columns, 32 threads each.
@@ -515,7 +600,18 @@ LayerNormPlan plan_layer_norm(int64_t M, int C) {
   return LayerNormPlan{h.L, h.NC, h.w};
 }
 
-LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, bool sums) {
+// 16 columns to a block, or more where the card would have to take more than half of its units for them
+int columns_apart(int64_t len, int64_t runs, int C) {
+  const int64_t cus = device_cus();
+  if (len > 1024) return 0;
+  for (int cw : {16, 32, 64}) {
+    const int64_t blocks = runs * ((C + cw - 1) / cw);
+    if (blocks <= (cw == 64 ? cus * 3 / 4 : cus / 2)) return cw;
+  }
+  return 0;
+}
+
+LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, bool sums, bool apart) {
   const Hold h = hold(C, C <= 8192 ? 1 : 2);
   LayerNormGradPlan p;
   p.runs = each ? B : 1;
@@ -525,12 +621,16 @@ LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, b
   p.w = h.w;
   p.waves = MAX_WAVES / h.w * h.w;
   const int64_t rpb = h.L == 64 ? p.waves / h.w : p.waves * (64 / h.L);
-  // (up to 4 turns one block does them all: the second launch would take longer)
-  const int64_t most = p.len <= 4 * rpb ? 1 : (device_cus() + p.runs - 1) / p.runs;  // blocks to a run
+  p.cw = sums && apart ? columns_apart(p.len, p.runs, C) : 0;
+  p.cols = p.cw ? (uint32_t)((C + p.cw - 1) / p.cw) : 0;
+  // blocks of rows to a run: what the columns' blocks leave of the card; or, with the sums' second launch, the card, but one
+  // where that does it in 4 turns, which takes less than the second launch
+  const int64_t cus = device_cus(), left = cus / p.runs - p.cols;
+  const int64_t most = p.cw ? (left > 1 ? left : 1) : p.len <= 4 * rpb ? 1 : (cus + p.runs - 1) / p.runs;
   const int64_t turns = (p.len + rpb * most - 1) / (rpb * most);
   p.per = turns * rpb;
   p.parts = (uint32_t)((p.len + p.per - 1) / p.per);
-  p.bytes = sums && p.parts > 1 ? (size_t)p.runs * p.parts * 2 * (size_t)C * 4 : 0;
+  p.bytes = sums && !p.cw && p.parts > 1 ? (size_t)p.runs * p.parts * 2 * (size_t)C * 4 : 0;
   return p;
 }
 
@@ -539,12 +639,16 @@ hipError_t launch_layer_norm_grad(const LayerNormArgs& args, const void* dY, int
                                   float* dgamma, float* dbeta, void* ws, hipStream_t st) {
   const LayerNormArgs a = divisor(args);
   const bool sums = dgamma || dbeta;
-  const LayerNormGradPlan p = plan_layer_norm_grad(a.B, a.S, a.C, a.gs != 0, sums);
+  // the columns' blocks read x and dy beside those that write dX, at 32-bit offsets from a run's first row
+  const bool one_run = a.gs != 0 || a.B == 1 || (a.bsx == a.S * a.ldx && bsd == a.S * ldd);
+  const int64_t run_rows = a.gs != 0 ? a.S : a.B * a.S, most_ld = a.ldx > ldd ? a.ldx : ldd;
+  const bool apart = dX != a.X && dX != dY && one_run && run_rows * most_ld < ((int64_t)1 << 29);
+  const LayerNormGradPlan p = plan_layer_norm_grad(a.B, a.S, a.C, a.gs != 0, sums, apart);
   const Hold h = hold(a.C, a.C <= 8192 ? 1 : 2);
-  float* part = p.parts > 1 ? static_cast<float*>(ws) : nullptr;
-  const dim3 grid(p.parts, (uint32_t)p.runs), block(64 * p.waves);
+  float* part = p.bytes ? static_cast<float*>(ws) : nullptr;
+  const dim3 grid(p.cols + p.parts, (uint32_t)p.runs), block(64 * p.waves);
   const int teams = p.waves / h.w;
-  const size_t lds = sums && teams > 1 ? (size_t)teams * 2 * (h.L == 64 ? 64 * h.w : h.L) * 8 * 4 : 0;  // at most 64 KB
+  const size_t lds = sums && !p.cw && teams > 1 ? (size_t)teams * 2 * (h.L == 64 ? 64 * h.w : h.L) * 8 * 4 : 0;  // at most 64 KB
   const bool words = rows_aligned4(a.X, a.ldx, a.xdtype) && (a.xdtype == 0 || a.bsx % 2 == 0) &&
                      rows_aligned4(dY, ldd, ddtype) && (ddtype == 0 || bsd % 2 == 0);  // bf16 rows begin at words
   auto run = [&](auto l, auto c) {
@@ -552,12 +656,11 @@ hipError_t launch_layer_norm_grad(const LayerNormArgs& args, const void* dY, int
     auto typed = [&](auto tx, auto td) {
       typedef decltype(tx) T;
       typedef decltype(td) TD;
-      auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, block, lds, st, a, p.w, p.len, p.per, static_cast<const TD*>(dY), bsd, ldd, mean,
-                           rstd, static_cast<T*>(dX), bso, ldo, part, dgamma, dbeta);
-      };
+      const GradArgs<T, TD> g{static_cast<const TD*>(dY), bsd, ldd, mean, rstd, static_cast<T*>(dX), bso, ldo, part, dgamma, dbeta};
+      auto go = [&](auto kernel, auto... more) { hipLaunchKernelGGL(kernel, grid, block, lds, st, a, p.w, p.len, p.per, g, more...); };
       auto kind = [&](auto vec) {
-        if (sums) go(k10_grad<T, TD, L, NC, true, decltype(vec)::value>);
+        if (p.cw) go(k10_grad_apart<T, TD, L, NC, decltype(vec)::value>, p.cw, p.cols);
+        else if (sums) go(k10_grad<T, TD, L, NC, true, decltype(vec)::value>);
         else go(k10_grad<T, TD, L, NC, false, decltype(vec)::value>);
       };
       if constexpr (L == 64 && (sizeof(T) == 2 || sizeof(TD) == 2)) {

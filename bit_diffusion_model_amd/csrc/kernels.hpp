@@ -175,11 +175,11 @@ hipError_t launch_layer_norm_fp8(const LayerNormArgs& a, uint8_t* qX, float* sX,
 // `waves` waves, w to a row; bytes: workspace of the blocks' partial sums.
 struct LayerNormGradPlan {
   int64_t runs, len, per;
-  uint32_t parts;
-  int w, waves;
+  uint32_t parts, cols;  // blocks of rows; blocks that sum cw columns each (cw 0: the blocks of rows sum theirs)
+  int w, waves, cw;
   size_t bytes;
 };
-LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, bool sums);
+LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, bool sums, bool apart);  // apart: whether columns may be summed so
 // How the norm holds a row: `lanes` lanes (64: `waves` waves of them), `chunks` chunks of 8 values each.
 struct LayerNormPlan {
   int lanes, chunks, waves;

@@ -677,7 +677,8 @@ svdq_status svdq_layer_norm_backward(const svdq_layer_norm_desc* norm, int64_t B
  *   svdq_debug_fp8_plan: plan = {rows and columns of a tile (0, 16: the kernel for few tokens), K groups, K parts}; the
  *     block-scaled product of M rows into a svdq_dtype.
  *   svdq_debug_layer_norm_plan: plan = {lanes that hold a row (16, 32 or 64), chunks of 8 values to a lane, waves to a row,
- *     blocks whose column sums the gradient joins for each gamma (1: no second launch)}.
+ *     blocks whose column sums the gradient joins for each gamma (1: no second launch; -16, -32 or -64: none, blocks of
+ *     their own sum so many columns each), where dX is neither X nor dY and rows follow each other at one stride}.
  * EINVAL / EUNSUPPORTED as the calls themselves; host only, nothing is launched. */
 svdq_status svdq_debug_w8a8_plan(const svdq_int8_layer* layer, int64_t M, int32_t plan[4]);
 svdq_status svdq_debug_group_norm_plan(const svdq_group_norm_desc* norm, int64_t B, int64_t S, int32_t plan[4]);

@@ -31,14 +31,16 @@ VARIANTS = {
 }
 TYPES = {"f32": svdq.F32, "bf16": svdq.BF16, "gelu": svdq.BF16_GELU}
 
-# (B, S, C): (lanes, chunks, waves to a row, blocks of the gradient)
+# (B, S, C): (lanes, chunks, waves to a row, blocks of the gradient; negative: columns to a block of their own)
 NORMS = {
-    (1, 5, 100): (16, 1, 1, 1), (1, 5, 200): (32, 1, 1, 1), (1, 5, 700): (64, 1, 2, 1), (1, 5, 2041): (64, 1, 4, 1),
-    (1, 5, 8001): (64, 2, 8, 5), (1, 5, 9000): (64, 4, 5, 5),
+    (1, 5, 100): (16, 1, 1, -16), (1, 5, 200): (32, 1, 1, -16), (1, 5, 700): (64, 1, 2, -16), (1, 5, 2041): (64, 1, 4, -16),
+    (1, 5, 3001): (64, 2, 3, -32), (1, 5, 8001): (64, 2, 8, -64), (1, 5, 9000): (64, 4, 5, -64), (1, 5, 16383): (64, 4, 8, 5),
+    (1, 1023, 100): (16, 1, 1, -16), (1, 999, 1111): (64, 3, 1, -16), (2, 450, 2047): (64, 4, 1, -16), (1, 1000, 5003): (64, 2, 5, -64),
     (1, 5000, 100): (16, 1, 1, 79), (1, 5000, 250): (16, 2, 1, 157), (1, 5000, 300): (16, 3, 1, 157),
     (1, 5000, 500): (16, 4, 1, 157), (1, 5000, 700): (32, 3, 1, 209), (1, 5000, 1000): (32, 4, 1, 209),
     (1, 3000, 1300): (64, 3, 1, 200), (2, 1500, 2047): (64, 4, 1, 250), (1, 2100, 3001): (64, 3, 2, 210),
-    (1, 1000, 5003): (64, 2, 5, 250), (1, 600, 9001): (64, 3, 6, 200), (1, 300, 16383): (64, 4, 8, 150),
+    (1, 1100, 5003): (64, 2, 5, 220), (1, 600, 9001): (64, 3, 6, -64), (1, 1050, 9001): (64, 3, 6, 210),
+    (1, 300, 16383): (64, 4, 8, 150),
 }
 
 
@@ -156,3 +158,10 @@ def test_norm(B, S, C, dt, pad):
     if dt == "bf16":
         tol = tol + 2.0 ** -8 * ref.abs()
     assert ((dX.double() - ref).abs() <= tol).all()
+    # in place: the sums by the blocks of rows
+    out = dY.contiguous().clone()
+    dX2, dg2, db2 = ln.backward(out, X, stats, out=out)
+    assert dX2 is out and torch.equal(dX2, dX)
+    for got, t in ((dg2, dY.double() * z), (db2, dY.double())):
+        bound = 2.0 ** -24 * (B * S + 6) * t.abs().sum((0, 1)) + 1e-37
+        assert ((got.double() - t.sum((0, 1))).abs() <= bound).all()
