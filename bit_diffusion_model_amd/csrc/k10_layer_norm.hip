@@ -14,10 +14,10 @@
 // The columns' sums of the gradient stay in registers over a block's rows, the next row on its way while one is
 // computed; a block joins its teams in LDS and leaves one partial sum; a second launch adds the blocks'; for few rows
 // blocks of their own sum the columns in the same launch.  Every order is fixed: no atomics.
-// Measured: 65536 x 4096 fp32 425 us (5.05 TB/s, a large copy 5.1); 2 x 4608 x 3072 bf16, modulated, 27.8 (4.1 TB/s: the vector
-// units are busy two thirds of the time, 411 instructions a wave of 24 values a lane); 4608 x 3072 to codes 14.3 (593, busy
-// 77%; kernel 8 on a written y 9.2); gradient 2 x 4608 x 3072 bf16 39 (35 and the second launch's 4; 4.3 TB/s),
-// 3 x 333 x 1111 fp32 9.2 in one launch.
+// Measured: 65536 x 4096 fp32 420 us (5.1 TB/s, as a large copy); 2 x 4608 x 3072 bf16, modulated, 27 (4.2 TB/s; the vector
+// units are busy 57%, 411 instructions a wave of 24 values a lane); 4608 x 3072 to codes 14.3 (593, busy 73%; kernel 8 on a
+// written y 9.2); gradient 2 x 4608 x 3072 bf16 39 (34 and the second launch's 4; 4.4 TB/s), 3 x 333 x 1111 fp32 9.2 in one
+// launch.
 #include <algorithm>
 #include <type_traits>
 
