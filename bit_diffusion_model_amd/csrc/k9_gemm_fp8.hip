@@ -553,7 +553,7 @@ void launch_tiles(const Fp8Plan& p, int64_t ld, const uint8_t* qX, const uint8_t
 // a[c] S + b[c], a launch once more const).  The lines are least squares over 650 drawn sizes (256 CUs, launches back to
 // back, inputs in turn; M x K x N); over 500 others the choice costs 1.0% (bf16) and 0.4% (fp32) more than the best.
 // bf16 outputs, then fp32 ones (whose products in f16 take twice the MFMA time and the conversions besides):
-//   few     up to 32 tokens, the weights' read: 1x3072x18432 11.2, 32x3072x18432 15.0
+//   few     up to 32 tokens, the weights' read: 1x3072x18432 11.2, 32x3072x18432 15.0 (240 sizes: 1.0% over the best)
 //   64      one K group: 333x1000x1111 5.8 (64 x 2: 6.1, 128: 8.9) / 6.8; 154x768x2304 5.1 (5.4, 7.0) / 6.1
 //   64 x 2  two K groups: 512x9216x3072 30.3 (64: 39.9, 128 x 2: 39.9) / 45.3 (53.2, 65.7)
 //   64 x 4  four K groups, and K in parts of at least 8 blocks: 64x12288x3072 16.4 in 4 parts, 28.3 in one, 64 x 2 33.8 /
@@ -632,7 +632,10 @@ Fp8Plan plan_fp8(int64_t M, int64_t K, int64_t N, bool fine) {
       take(c);
     }
   }
-  if (M <= 32) take(Cost{3.0 + (double)(N * ld) * 1e-6 * (0.11 + 0.009 * (double)M), 0, 16, 1, 1});
+  if (M <= 32) {  // the weights' bytes, the workgroups' starts and a wave's steps along K; a second set of 16 tokens
+    const double more = M > 16, n = (double)N, k = (double)ld;
+    take(Cost{2.62 + n * k * 1e-6 * (0.132 + 0.11 * more) + n * 1e-3 * (0.053 + 0.111 * more) + k * 3.5e-4, 0, 16, 1, 1});
+  }
   Fp8Plan p{best.rows, best.cols, best.groups, best.parts, ldp, 0};
   if (p.parts > 1) p.bytes = (size_t)p.parts * (size_t)M * (size_t)ldp * 4;
   return p;

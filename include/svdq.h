@@ -564,8 +564,8 @@ svdq_status svdq_norm_linear_forward_int8(const svdq_group_norm_desc* norm, cons
  *             no other row's change.
  *   product   Y[m][n] = sum over blocks b (s_X[b][m] s_W[n / 128][b]) D_b + bias[n], D_b = sum over k in b of qX[m][k]
  *             qW[n][k] on the matrix core, all sums in fp32, then GELU if asked, rounded once to Y's type.  For fp32 Y
- *             the codes are multiplied as fp16 (exact).  For bf16 Y above 32 rows they are multiplied as they are, at twice
- *             the rate: the matrix core then aligns the products of 8 codes to the largest before it adds them, which
+ *             the codes are multiplied as fp16 (exact).  For bf16 Y of more than a few rows they are multiplied as they are,
+ *             at twice the rate: the matrix core then aligns the products of 8 codes to the largest before it adds them, which
  *             costs 1e-5 to 6e-5 of a sum, far below the rounding to bf16.  The factors s_X s_W have to stay within fp32.
  * E4M3 is the finite variant (bias 7, subnormals to 2^-9, largest 448, 0x7F and 0xFF NaN).  Rows of codes are
  * svdq_int8_ld(K) = K rounded up to 128 bytes long; the bytes past K are zero.  Scales of activations are
