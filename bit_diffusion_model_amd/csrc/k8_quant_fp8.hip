@@ -4,57 +4,40 @@
 // r = 448 / a; q = E4M3(x r).
 //
 // Design (gfx950): bound by HBM (x read once, a byte per value written).  Blocks of 128 are independent, so a row
-// needs no join: 16 lanes hold a block, 8 values each, and meet by lane moves.  A workgroup takes 16 rows x 512
-// values, four rows a wave, all four loads in flight; the 64 scales meet in LDS and leave as four runs of 16 (the
-// scales' rows run along the tokens, which is how the product reads them).  4608 x 3072 bf16 9.2 us, 16384 x 2048 21.2: 4.7 and
-// 4.8 TB/s of what a large copy reaches 5.1.
+// needs no join: 16 lanes hold a block, 8 values each, and meet by lane moves.  A wave takes 512 values of a row, a
+// workgroup four rows, whose scales lie side by side (the scales' rows run along the tokens, which is how the product
+// reads them).  4608 x 3072 bf16 8.9 us, 16384 x 2048 21: 4.8 TB/s of what a large copy reaches 5.1.  (Four rows a wave with
+// 64 scales joined in LDS, whole runs of 16: 9.3, and 2.9 against 2.1 at 154 x 768, 7.2 against 6.3 at 3000 x 3072, but
+// 32.0 against 33.4 at 4608 x 12288.)
 #include "fp8.hpp"
 #include "kernels.hpp"
 
 namespace svdq {
 namespace {
 
-constexpr int Q_ROWS = 16, Q_COLS = 512;
+constexpr int Q_ROWS = 4, Q_COLS = 512;
 
 template <typename T, bool VEC>
-__global__ __launch_bounds__(256) void k8_quant(const T* __restrict__ X, int64_t ldx, int64_t M, int K, uint32_t kts,
-                                                uint8_t* __restrict__ qX, int64_t ldq, float* __restrict__ sX,
-                                                int64_t Mp) {
-  __shared__ float sc[Q_COLS / 128][Q_ROWS];
+__global__ __launch_bounds__(64 * Q_ROWS) void k8_quant(const T* __restrict__ X, int64_t ldx, int64_t M, int K,
+                                                        uint32_t kts, uint8_t* __restrict__ qX, int64_t ldq,
+                                                        float* __restrict__ sX, int64_t Mp) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t rt = blockIdx.x / kts, kt = blockIdx.x - rt * kts;
-  const int64_t m0 = (int64_t)rt * Q_ROWS;
-  const int rows = (int)(M - m0 < Q_ROWS ? M - m0 : Q_ROWS);
+  const int64_t m = (int64_t)rt * Q_ROWS + wave;
+  if (m >= M) return;
   const int k = (int)kt * Q_COLS + 8 * lane;
-  typedef Row<T, VEC> RowX;
-  auto row = [&](int j) {  // past M: no range, zeros
-    const int r = wave + 4 * j;
-    return RowX(X + (m0 + (r < rows ? r : 0)) * ldx, r < rows ? K : 0);
-  };
-  typename RowX::Raw w[4];
+  const Row<T, VEC> x(X + m * ldx, K);
+  float v[8];
+  x.value(x.load(k), k, v);
+  uint32_t a = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = row(j).load(k);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = wave + 4 * j;
-    float v[8];
-    row(j).value(w[j], k, v);
-    uint32_t a = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a = umax(a, abs_bits(v[e]));
-    a = wave_umax<16>(a);
-    float s, f;
-    block_scale(a, s, f);
-    if ((lane & 15) == 0) sc[lane >> 4][r] = s;
-    if (r < rows && k < ldq)
-      *reinterpret_cast<uint2*>(qX + (m0 + r) * ldq + k) =
-          make_uint2(e4m3x4(v[0], v[1], v[2], v[3], f), e4m3x4(v[4], v[5], v[6], v[7], f));
-  }
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    const int b = (int)kt * (Q_COLS / 128) + (threadIdx.x >> 4), r = threadIdx.x & 15;
-    if (r < rows && (int64_t)b * 128 < ldq) sX[b * Mp + m0 + r] = sc[threadIdx.x >> 4][r];
-  }
+  for (int e = 0; e < 8; ++e) a = umax(a, abs_bits(v[e]));
+  a = wave_umax<16>(a);
+  float s, f;
+  block_scale(a, s, f);
+  if (k >= ldq) return;
+  if ((lane & 15) == 0) sX[(int64_t)(k >> 7) * Mp + m] = s;
+  *reinterpret_cast<uint2*>(qX + m * ldq + k) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3], f), e4m3x4(v[4], v[5], v[6], v[7], f));
 }
 
 template <typename T, bool VEC>
@@ -65,8 +48,8 @@ void launch(int64_t M, int64_t K, const T* X, int64_t ldx, uint8_t* qX, float* s
   for (int64_t m = 0; m < M; m += slab) {
     const int64_t rows = M - m < slab ? M - m : slab;
     const uint32_t grid = (uint32_t)((rows + Q_ROWS - 1) / Q_ROWS * kts);
-    hipLaunchKernelGGL((k8_quant<T, VEC>), dim3(grid), dim3(256), 0, st, X + m * ldx, ldx, rows, (int)K, (uint32_t)kts,
-                       qX + m * ldq, ldq, sX + m, Mp);
+    hipLaunchKernelGGL((k8_quant<T, VEC>), dim3(grid), dim3(64 * Q_ROWS), 0, st, X + m * ldx, ldx, rows, (int)K,
+                       (uint32_t)kts, qX + m * ldq, ldq, sX + m, Mp);
   }
 }
 
