@@ -14,9 +14,9 @@
 // The columns' sums of the gradient stay in registers over a block's rows, the next row on its way while one is
 // computed; a block joins its teams in LDS and leaves one partial sum; a second launch adds the blocks'; for few rows
 // blocks of their own sum the columns in the same launch.  Every order is fixed: no atomics.
-// Measured: 65536 x 4096 fp32 420 us (5.1 TB/s, as a large copy); 2 x 4608 x 3072 bf16, modulated, 27 (4.2 TB/s; the vector
-// units are busy 57%, 411 instructions a wave of 24 values a lane); 4608 x 3072 to codes 14.3 (593, busy 73%; kernel 8 on a
-// written y 9.2); gradient 2 x 4608 x 3072 bf16 39 (34 and the second launch's 4; 4.4 TB/s), 3 x 333 x 1111 fp32 9.2 in one
+// Measured: 65536 x 4096 fp32 420 us (5.1 TB/s, as a large copy); 2 x 4608 x 3072 bf16, modulated, 25 (4.5 TB/s; the vector
+// units are busy 66%, 385 instructions a wave of 24 values a lane); 4608 x 3072 to codes 13.2 (555, busy 82%; kernel 8 on a
+// written y 9.1); gradient 2 x 4608 x 3072 bf16 39 (34 and the second launch's 4; 4.4 TB/s), 3 x 333 x 1111 fp32 9.2 in one
 // launch.
 #include <algorithm>
 #include <type_traits>
@@ -534,7 +534,7 @@ void by_chunks(int NC, F&& f) {
 // waves costs more than their loads save (bf16: 8 x 8192 in 16, 8, 4 waves 5.1, 4.1, 4.1 us; 300 x 3072 in 6, 3, 2: 4.65, 3.97,
 // 3.92; 400 x 1500 in 3, 2, 1: 3.66, 3.84, 3.69).
 // Else what leaves the fewest lanes idle in the fewest waves: 100000 x 320 by 16 lanes 34 us (64: 48), 100000 x 768 by 32 lanes
-// 60 (64 lanes: 88), 4608 x 3072 by 64 lanes of 3 chunks 13.4 (1: 23.0, 2: 14.8, 4: 14.0), 16384 x 2048 of 4 30 (1: 38, 2: 34).
+// 60 (64 lanes: 88), 4608 x 3072 by 64 lanes of 3 chunks 12.8 (before gamma came one chunk ahead 13.4; 1: 23.0, 2: 14.8, 4: 14.0), 16384 x 2048 of 4 30 (1: 38, 2: 34).
 Hold hold_norm(int64_t M, int C) {
   const int one = (C + 511) / 512;  // waves of one chunk
   if (M * one < (C <= 1024 ? 16 : 8) * (int64_t)device_cus()) return hold(C, one <= 4 ? 1 : one <= MAX_WAVES ? 2 : 4);
