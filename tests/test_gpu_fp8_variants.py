@@ -33,6 +33,7 @@ TYPES = {"f32": svdq.F32, "bf16": svdq.BF16, "gelu": svdq.BF16_GELU}
 
 # (B, S, C): (lanes, chunks, waves to a row, blocks of the gradient; negative: columns to a block of their own)
 NORMS = {
+    (1, 5, 8): (16, 1, 1, -16), (1, 2000, 33): (16, 1, 1, 16), (2, 1500, 64): (16, 1, 1, 24), (1, 3000, 65): (16, 1, 1, 47),
     (1, 5, 100): (16, 1, 1, -16), (1, 5, 200): (32, 1, 1, -16), (1, 5, 700): (64, 1, 2, -16), (1, 5, 2041): (64, 1, 4, -16),
     (1, 5, 3001): (64, 2, 3, -32), (1, 5, 8001): (64, 2, 8, -64), (1, 5, 9000): (64, 4, 5, -64), (1, 5, 16383): (64, 4, 8, 5),
     (1, 1023, 100): (16, 1, 1, -16), (1, 999, 1111): (64, 3, 1, -16), (2, 450, 2047): (64, 4, 1, -16), (1, 1000, 5003): (64, 2, 5, -64),
