@@ -52,13 +52,15 @@ extern "C" svdq_status svdq_pack_weights_fp8(int64_t K, int64_t N, const uint16_
     for (int64_t c = 0; c < kb; ++c) {
       const int64_t k0 = c * kTile, k1 = std::min(K, k0 + kTile);
       double top = 0.0;
+      bool all = true;
       for (int64_t k = k0; k < k1; ++k)
         for (int64_t n = n0; n < n1; ++n) {
           const uint16_t bits = W[k * N + n];
-          if ((bits & 0x7F80u) == 0x7F80u) finite = false;
+          if ((bits & 0x7F80u) == 0x7F80u) all = false;
           top = std::max(top, std::fabs(bf16_value(bits)));
         }
-      const float s = (float)(top / 448.0);
+      if (!all) finite = false;
+      const float s = all ? (float)(top / 448.0) : 0.0f;  // no code is made of a NaN or an infinity: the block is zeros
       sW_out[b * kb + c] = s;
       for (int64_t n = n0; n < n1; ++n) {
         uint8_t* out = qW_out + n * ld + k0;
