@@ -638,10 +638,11 @@ LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, b
   const int64_t rpb = h.L == 64 ? p.waves / h.w : p.waves * (64 / h.L);
   p.cw = sums && apart ? columns_apart(p.len, p.runs, C) : 0;
   p.cols = p.cw ? (uint32_t)((C + p.cw - 1) / p.cw) : 0;
-  // blocks of rows to a run: what the columns' blocks leave of the card; or, with the sums' second launch, the card, but one
-  // where that does it in 4 turns, which takes less than the second launch
+  // blocks of rows to a run: what the columns' blocks leave of the card; else the card, but one where that does it in 4
+  // turns and there are sums, whose second launch takes more than that (without sums one block 6.5 us at 512 x 64 fp32, 7.5 at
+  // 64 x 400, the card's 3.2 and 3.8)
   const int64_t cus = device_cus(), left = cus / p.runs - p.cols;
-  const int64_t most = p.cw ? (left > 1 ? left : 1) : p.len <= 4 * rpb ? 1 : (cus + p.runs - 1) / p.runs;
+  const int64_t most = p.cw ? (left > 1 ? left : 1) : sums && p.len <= 4 * rpb ? 1 : (cus + p.runs - 1) / p.runs;
   const int64_t turns = (p.len + rpb * most - 1) / (rpb * most);
   p.per = turns * rpb;
   p.parts = (uint32_t)((p.len + p.per - 1) / p.per);
