@@ -1087,10 +1087,11 @@ class LayerNorm:
         if len(shapes) > 1 or any(len(s) not in (1, 2) or s[-1] != self.C for s in shapes):
             raise SvdqError(f"gamma and beta must both be [{self.C}] or [B][{self.C}]")
         shape = shapes.pop() if shapes else (self.C,)
-        self.images = shape[0] if len(shape) == 2 else 0  # images that have a weight of their own (0: one for all)
+        self._each = len(shape) == 2
+        self.images = shape[0] if self._each else 0  # images that have a weight of their own (one for all: 0)
         self._dev = _one_device((self.gamma, self.beta), "norm")
         self._c = _LayerNorm(self.C, self.eps, int(self.one_plus), _dptr(self.gamma), _dptr(self.beta),
-                             self.C if self.images else 0)
+                             self.C if self._each else 0)
         self._ref = ctypes.addressof(self._c)
 
     def _geometry(self, X, what="X"):
@@ -1100,7 +1101,7 @@ class LayerNorm:
         if n not in (2, 3) or shape[-1] != C or X.dtype not in _cfg[1] or (C > 1 and strides[-1] != 1):
             raise SvdqError(f"{what} must be an fp32 or bf16 [M][{C}] or [B][S][{C}] tensor with unit channel stride")
         B, bs = (shape[0], strides[0]) if n == 3 else (1, 0)
-        if self.images and self.images != B:
+        if self._each and self.images != B:
             raise SvdqError(f"gamma and beta are of {self.images} images, {what} of {B}")
         S, ld = shape[-2], strides[-2]
         return B, S, bs, ld if S > 1 or ld > C else C
@@ -1199,7 +1200,7 @@ class LayerNorm:
             _, _, bso, ldo = self._geometry(out, "out")
         dgamma = dbeta = ws = None
         if weights:
-            shape = (2, B, self.C) if self.images else (2, self.C)
+            shape = (2, B, self.C) if self._each else (2, self.C)
             dgamma, dbeta = X.new_empty(shape, dtype=torch.float32).unbind()
             n = 0 if workspace is not None else L.svdq_layer_norm_backward_workspace_bytes(self._ref, B, S)
             ws = torch.empty(n, dtype=torch.uint8, device=X.device) if n else workspace
