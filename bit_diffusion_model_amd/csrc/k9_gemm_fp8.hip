@@ -1,7 +1,7 @@
 // Kernel 9: the matrix product on E4M3 codes with a scale for each block of 128.
 //
 // Mathematics: y[m][n] = sum over blocks b of 128 along K of (sX[b][m] sW[n / 128][b]) D_b[m][n] + bias[n], D_b[m][n]
-// the sum of the block's 128 products of codes (exact products, added by the matrix core in fp32); blocks added in
+// the sum of the block's 128 products of codes as the matrix core adds them (see Accuracy); blocks added in
 // fp32, then optionally GELU, rounded once to the output type.  qX comes as rows of ld bytes, sX as rows of Mp = M
 // rounded up to 4 along the tokens; qW in the fragment order of svdq_prepare_weights_int8: [N / 16][ld / 64] fragments
 // of 1 KB, lane l of a fragment holding channel l & 15 and the 16 codes k = 16 (l >> 4) .., N padded to 16 with zeros.
@@ -9,8 +9,9 @@
 // pieces of a fragment, the same pieces for both operands: a sum does not ask in which order k comes.
 //
 // Accuracy: on E4M3 operands the matrix core takes the products of 8 successive codes together: with E the largest sum of
-// two codes' exponents, it drops from each product, toward zero, what lies below 2^(E - 13).  (The older 16x16x32 form on
-// E4M3 drops the same, bit for bit, at a third of the rate.)  Products within 7 binades of the largest lose nothing; so with
+// two codes' exponents (-6 of a subnormal code; zeros do not count), it drops from each product, toward zero, what lies
+// below 2^(E - 13): bit for bit so, and in the older 16x16x32 form, at a third of the rate, too.  Products of normal codes
+// within 7 binades of the largest lose nothing; so with
 // terms of random signs the loss is 1.3e-5 of the outputs' root mean square for codes of normals, 2.1e-5 with channels 30
 // times as large, 5e-5 to 6e-5 for codes of all binades alike, the same for one block and for 96; with terms of one sign
 // 2.4e-6 of the sum.  Rounding to bf16 costs 1.7e-3 in the root mean square, so bf16 outputs of tiles take that loss: 1.1%

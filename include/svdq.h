@@ -567,8 +567,8 @@ svdq_status svdq_norm_linear_forward_int8(const svdq_group_norm_desc* norm, cons
  *             and for bf16 Y of up to 32 rows that run without tiles, the codes are multiplied as fp16, whose products are
  *             exact and added in fp32.  For other bf16 Y they are multiplied as they are, at twice the rate: of 8
  *             successive products the matrix core then drops, from each and toward zero, what lies below 2^-13 of the
- *             power of two that the exponents of the largest product's codes give (7 2^-13 of sum |terms| at the very
- *             worst).  Where the terms' signs are random that is 1.3e-5 (codes of normals) to 6e-5 (codes of all binades
+ *             power of two that the exponents of the largest product's codes give, those of subnormal codes being -6 (7 2^-13 of
+ *             sum |terms| at the very worst, with codes below 2^-6 taken for that).  Where the terms' signs are random that is 1.3e-5 (codes of normals) to 6e-5 (codes of all binades
  *             alike) of the outputs' root mean square, whatever K, a thirtieth to a hundredth of what rounding to bf16
  *             costs; where they are all of one sign 2.4e-6 of the sum, toward zero.  An output that cancels to below a
  *             hundredth of the others is off by more than its own rounding, and a row's bf16 outputs may differ by this
