@@ -8,9 +8,11 @@
 // Design (gfx950): bound by HBM, x (and dy) read once: a row stays in registers, 8 values a lane and chunk, NC chunks.  A
 // row takes L = 8 (gradient), 16, 32 or 64 lanes, or a team of several waves: few waves of up to 4 chunks where there are rows enough
 // to fill the card, more waves of fewer chunks where there are not.
-// Statistics: a first mean p of the lanes' own group, then d = x - p, sum d and sum d^2: mean = p + sum d / n,
-// M2 = sum d^2 - (sum d)^2 / n, so that neither a mean far from zero nor the rounding of p costs digits (a constant row
-// gives beta).  Waves join by the pairwise formula (Chan, Golub and LeVeque) about the first one's mean, at one barrier.
+// Statistics: a first mean p of the lanes' own group, then d = x - p, sum d and sum d^2: mean = p + c, c = sum d / n,
+// M2 = sum d^2 - (sum d) c, so that neither a mean far from zero nor the rounding of p costs digits (a constant row gives
+// beta).  Waves join by the pairwise formula (Chan, Golub and LeVeque) about the first one's mean, at one barrier, from p and
+// c apart: the first means' differences are exact, and a mean rounded to fp32 before it is subtracted cost rstd 2.4e-5 at a
+// mean of 1e4 standard deviations.
 // The columns' sums of the gradient stay in registers over a block's rows, the next row on its way while one is
 // computed; a block joins its teams in LDS and leaves one partial sum; a second launch adds the blocks'; for few rows
 // blocks of their own sum the columns in the same launch.  Every order is fixed: no atomics.
@@ -199,17 +201,24 @@ __global__ __launch_bounds__(64 * norm_waves(NC), L == 64 && NC == 3 ? 6 : 1) vo
       s2 = fmaf(d, d, s2);
     });
   s1 = lane_sum<L>(s1), s2 = lane_sum<L>(s2);
-  float mean = p + s1 * rn, m2 = s2 - s1 * (s1 * rn);
+  const float c = s1 * rn;  // the mean is p + c
+  float mean = p + c, m2 = s2 - s1 * c;
   m2 = m2 < 0.0f ? 0.0f : m2;  // (a NaN passes)
   if (L == 64 && w > 1) {
-    if ((threadIdx.x & 63) == 0) meet[at.wave] = make_float4(mean, m2, n, 0.0f);
+    if ((threadIdx.x & 63) == 0) meet[at.wave] = make_float4(p, c, m2, n);
     __syncthreads();
     const float4* t = meet + at.team * w;
-    const float m0 = t[0].x;
-    float d = 0.0f, q = 0.0f;
-    for (int i = 1; i < w; ++i) d += t[i].z * (t[i].x - m0);
-    mean = m0 + d * rc;
-    for (int i = 0; i < w; ++i) q += t[i].y + t[i].z * (t[i].x - mean) * (t[i].x - mean);
+    // how far a wave's mean lies from the first one's: two small differences, not that of two rounded means
+    auto apart = [&](int i) { return (t[i].x - t[0].x) + (t[i].y - t[0].y); };
+    float d = 0.0f, q = t[0].z;
+    for (int i = 1; i < w; ++i) d = fmaf(t[i].w, apart(i), d);
+    d *= rc;
+    mean = t[0].x + (t[0].y + d);
+    q = fmaf(t[0].w * d, d, q);
+    for (int i = 1; i < w; ++i) {
+      const float e = apart(i) - d;
+      q += fmaf(t[i].w * e, e, t[i].z);
+    }
     m2 = q;
   }
   const float rstd = inv_sqrt(m2 * rc + a.eps);
