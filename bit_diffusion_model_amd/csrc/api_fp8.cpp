@@ -80,7 +80,8 @@ svdq_status layer_norm_args(const svdq_layer_norm_desc* n, int64_t B, int64_t S,
                             int64_t bsx, int64_t ldx, LayerNormArgs& a) {
   svdq_status st = check_in(X, xdtype, ldx, n->C);
   if (st != SVDQ_OK || (st = check_images("X", B, S, n->C, bsx, ldx, true)) != SVDQ_OK) return st;
-  a = LayerNormArgs{B, S, (int)n->C, n->one_plus != 0, n->eps, n->gamma, n->beta, n->image_stride, X, xdtype, B > 1 ? bsx : 0, ldx, 0, 0};
+  a = LayerNormArgs{B, S, (int)n->C, n->one_plus != 0, n->eps, n->gamma, n->beta, n->image_stride,
+                    X, xdtype, B > 1 ? bsx : 0, ldx, 0, 0};
   return SVDQ_OK;
 }
 

@@ -12,11 +12,10 @@ constexpr int64_t fp8_blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block
 // The scales of a block of K: one row of M values, padded so that every row is 16-byte aligned.
 constexpr int64_t fp8_pad(int64_t M) { return (M + 3) / 4 * 4; }
 
-typedef int v8i_t __attribute__((ext_vector_type(8)));
-
 // A block's scale s = a / 448 and the factor r = 448 / a of its codes (both IEEE quotients: the first by a product and one
-// correction with the exact residual, which gives the correctly rounded one for every a), from the bits of its largest magnitude; a is floored at 2^-96 (zeros get zero codes, r stays finite).  A block that holds a NaN or an
-// infinity gets a NaN scale and r = 0, so that its codes are 0 and the row's outputs NaN.
+// correction with the exact residual, which gives the correctly rounded one for every a), from the bits of its largest
+// magnitude; a is floored at 2^-96 (zeros get zero codes, r stays finite).  A block that holds a NaN or an infinity gets a
+// NaN scale and r = 0, so that its codes are 0 and the row's outputs NaN.
 __device__ __forceinline__ void block_scale(uint32_t abits, float& s, float& r) {
   const bool bad = abits >= 0x7F800000u;
   const float a = __uint_as_float(umax(abits, 0x0F800000u));  // 2^-96

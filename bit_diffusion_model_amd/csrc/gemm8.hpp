@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "int8.hpp"
+#include "vec.hpp"
 
 namespace svdq {
 
@@ -19,12 +20,6 @@ template <int N>
 __device__ __forceinline__ void wait_vm_lgkm0() {
   static_assert(N >= 0 && N < 64, "counter range");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-  const b2 v = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, v);
 }
 
 struct Out {
@@ -42,11 +37,8 @@ __device__ __forceinline__ void store1(const Out& o, int64_t m, int64_t n, float
   else static_cast<__bf16*>(o.Y)[m * o.ldy + n] = (__bf16)(o.ydtype == 2 ? gelu5(y) : y);
 }
 
-// Sixteen bytes at any output's address: the memory takes them at every alignment (rows of an odd
-// length included: 4141x1408x4274 fp32 95 us by single outputs, 50 so)
-typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
-
-// Eight outputs n .. n + 7 (n a multiple of 8) of row m.  WHOLE: all of them lie within Y; else
+// Eight outputs n .. n + 7 (n a multiple of 8) of row m, by stores of sixteen bytes at any output's address (rows of an odd
+// length included: 4141x1408x4274 fp32 95 us by single outputs, 50 so).  WHOLE: all of them lie within Y; else
 // channels may lie past N.  OUT: 0 fp32, 1 bf16, 2 bf16 of GELU.
 template <int OUT, bool WHOLE>
 __device__ __forceinline__ void store8(const Out& o, int64_t m, int64_t n, const float y[8]) {
@@ -56,9 +48,9 @@ __device__ __forceinline__ void store8(const Out& o, int64_t m, int64_t n, const
     if (whole) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const u32x4_2 w = {__float_as_uint(y[4 * h]), __float_as_uint(y[4 * h + 1]), __float_as_uint(y[4 * h + 2]),
-                           __float_as_uint(y[4 * h + 3])};
-        reinterpret_cast<u32x4_2*>(p)[h] = w;
+        const u32x4a w = {__float_as_uint(y[4 * h]), __float_as_uint(y[4 * h + 1]), __float_as_uint(y[4 * h + 2]),
+                          __float_as_uint(y[4 * h + 3])};
+        reinterpret_cast<u32x4a*>(p)[h] = w;
       }
     } else {
 #pragma unroll
@@ -67,12 +59,12 @@ __device__ __forceinline__ void store8(const Out& o, int64_t m, int64_t n, const
     }
   } else {
     uint16_t* p = static_cast<uint16_t*>(o.Y) + m * o.ldy + n;
-    u32x4_2 w;
+    u32x4a w;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      w[e] = OUT == 2 ? bf16_pair(gelu5(y[2 * e]), gelu5(y[2 * e + 1])) : bf16_pair(y[2 * e], y[2 * e + 1]);
+      w[e] = OUT == 2 ? pack_bf16(gelu5(y[2 * e]), gelu5(y[2 * e + 1])) : pack_bf16(y[2 * e], y[2 * e + 1]);
     if (whole) {
-      *reinterpret_cast<u32x4_2*>(p) = w;
+      *reinterpret_cast<u32x4a*>(p) = w;
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)

@@ -11,7 +11,8 @@ namespace svdq {
 
 // Row reads without branches, so that all of a row's loads can be issued before the first is
 // waited for.  A Row covers K values from p; load(k) starts the read of values k .. k+7 and
-// value() turns it into fp32; what lies at or past K reads as 0 (the buffer's range); inner() does where all eight lie before K.
+// value() turns it into fp32; what lies at or past K reads as 0 (the buffer's range); inner() does where all eight lie
+// before K.
 // VEC: p is 4-byte aligned (16-byte loads need no more).  A bf16 row that may begin in the middle
 // of a word is read from the word's start, 20 bytes for 8 values, and shifted.  Only whole aligned
 // words are read: the first and the last may hold a neighbour's value, never an unmapped byte, and

@@ -6,8 +6,8 @@
 // dbeta = sum over rows dy.
 //
 // Design (gfx950): bound by HBM, x (and dy) read once: a row stays in registers, 8 values a lane and chunk, NC chunks.  A
-// row takes L = 8 (gradient), 16, 32 or 64 lanes, or a team of several waves: few waves of up to 4 chunks where there are rows enough
-// to fill the card, more waves of fewer chunks where there are not.
+// row takes L = 8 (gradient), 16, 32 or 64 lanes, or a team of several waves: few waves of up to 4 chunks where there are
+// rows enough to fill the card, more waves of fewer chunks where there are not.
 // Statistics: a first mean p of the lanes' own group, then d = x - p, sum d and sum d^2: mean = p + c, c = sum d / n,
 // M2 = sum d^2 - (sum d) c, so that neither a mean far from zero nor the rounding of p costs digits (a constant row gives
 // beta).  Waves join by the pairwise formula (Chan, Golub and LeVeque) about the first one's mean, at one barrier, from p and
@@ -340,8 +340,9 @@ __device__ __forceinline__ void grad_rows(const LayerNormArgs& a, int w, int64_t
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int k = 8 * at.li + j * step;
+      // (zeros past the row and past the last row: nothing of theirs is added)
       if (whole(j)) x.inner(cur.x[j], z[j]), dy.inner(cur.d[j], d[j]);
-      else x.value(cur.x[j], k, z[j]), dy.value(cur.d[j], k, d[j]);  // zeros past the row and past the last row: nothing of theirs is added
+      else x.value(cur.x[j], k, z[j]), dy.value(cur.d[j], k, d[j]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) z[j][e] = (z[j][e] - cur.mean) * cur.rstd;
       within(whole(j) && (L < 64 || on), k, on ? C : 0, [&](int e, bool in) {
@@ -552,10 +553,11 @@ void by_chunks(int NC, F&& f) {
 }
 
 // Few rows: one chunk a lane, so long as that is at most 4 waves; then two, and past 8192 values four, since a join of many
-// waves costs more than their loads save (bf16: 8 x 8192 in 16, 8, 4 waves 5.1, 4.1, 4.1 us; 300 x 3072 in 6, 3, 2: 4.65, 3.97,
-// 3.92; 400 x 1500 in 3, 2, 1: 3.66, 3.84, 3.69).
-// Else what leaves the fewest lanes idle in the fewest waves: 100000 x 320 by 16 lanes 34 us (64: 48), 100000 x 768 by 32 lanes
-// 60 (64 lanes: 88), 4608 x 3072 by 64 lanes of 3 chunks 12.8 (before gamma came one chunk ahead 13.4; 1: 23.0, 2: 14.8, 4: 14.0), 16384 x 2048 of 4 30 (1: 38, 2: 34).
+// waves costs more than their loads save (bf16: 8 x 8192 in 16, 8, 4 waves 5.1, 4.1, 4.1 us; 300 x 3072 in 6, 3, 2: 4.65,
+// 3.97, 3.92; 400 x 1500 in 3, 2, 1: 3.66, 3.84, 3.69).
+// Else what leaves the fewest lanes idle in the fewest waves: 100000 x 320 by 16 lanes 34 us (64: 48), 100000 x 768 by 32
+// lanes 60 (64 lanes: 88), 4608 x 3072 by 64 lanes of 3 chunks 12.8 (before gamma came one chunk ahead 13.4; 1: 23.0, 2:
+// 14.8, 4: 14.0), 16384 x 2048 of 4 30 (1: 38, 2: 34).
 Hold hold_norm(int64_t M, int C) {
   const int one = (C + 511) / 512;  // waves of one chunk
   if (M * one < (C <= 1024 ? 16 : 8) * (int64_t)device_cus()) return hold(C, one <= 4 ? 1 : one <= MAX_WAVES ? 2 : 4);
@@ -607,7 +609,8 @@ hipError_t launch(const LayerNormArgs& args, void* Y, int64_t bsy, int64_t ldy, 
 }
 
 hipError_t launch_join(const float* part, uint32_t parts, int64_t runs, int C, float* dgamma, float* dbeta, hipStream_t st) {
-  hipLaunchKernelGGL(k10_join, dim3((uint32_t)((C + 31) / 32), (uint32_t)runs), dim3(32 * JOIN), 0, st, part, (int)parts, C, dgamma, dbeta);
+  const dim3 grid((uint32_t)((C + 31) / 32), (uint32_t)runs);
+  hipLaunchKernelGGL(k10_join, grid, dim3(32 * JOIN), 0, st, part, (int)parts, C, dgamma, dbeta);
   return hipGetLastError();
 }
 
@@ -676,7 +679,8 @@ hipError_t launch_layer_norm_grad(const LayerNormArgs& args, const void* dY, int
   float* part = p.bytes ? static_cast<float*>(ws) : nullptr;
   const dim3 grid(p.cols + p.parts, (uint32_t)p.runs), block(64 * p.waves);
   const int teams = p.waves / h.w;
-  const size_t lds = sums && !p.cw && teams > 1 ? (size_t)teams * 2 * (h.L == 64 ? 64 * h.w : h.L) * 8 * 4 : 0;  // at most 64 KB
+  const int lanes = h.L == 64 ? 64 * h.w : h.L;
+  const size_t lds = sums && !p.cw && teams > 1 ? (size_t)teams * 2 * lanes * 8 * 4 : 0;  // at most 64 KB
   const bool words = rows_aligned4(a.X, a.ldx, a.xdtype) && (a.xdtype == 0 || a.bsx % 2 == 0) &&
                      rows_aligned4(dY, ldd, ddtype) && (ddtype == 0 || bsd % 2 == 0);  // bf16 rows begin at words
   auto run = [&](auto l, auto c) {
@@ -684,8 +688,11 @@ hipError_t launch_layer_norm_grad(const LayerNormArgs& args, const void* dY, int
     auto typed = [&](auto tx, auto td) {
       typedef decltype(tx) T;
       typedef decltype(td) TD;
-      const GradArgs<T, TD> g{static_cast<const TD*>(dY), bsd, ldd, mean, rstd, static_cast<T*>(dX), bso, ldo, part, dgamma, dbeta};
-      auto go = [&](auto kernel, auto... more) { hipLaunchKernelGGL(kernel, grid, block, lds, st, a, p.w, p.len, p.per, g, more...); };
+      const GradArgs<T, TD> g{static_cast<const TD*>(dY), bsd, ldd, mean, rstd, static_cast<T*>(dX), bso, ldo,
+                              part, dgamma, dbeta};
+      auto go = [&](auto kernel, auto... more) {
+        hipLaunchKernelGGL(kernel, grid, block, lds, st, a, p.w, p.len, p.per, g, more...);
+      };
       auto kind = [&](auto vec) {
         if (p.cw) go(k10_grad_apart<T, TD, L, NC, decltype(vec)::value>, p.cw, p.cols);
         else if (sums) go(k10_grad<T, TD, L, NC, true, decltype(vec)::value>);

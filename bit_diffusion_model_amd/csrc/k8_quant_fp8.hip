@@ -37,7 +37,8 @@ __global__ __launch_bounds__(64 * Q_ROWS) void k8_quant(const T* __restrict__ X,
   block_scale(a, s, f);
   if (k >= ldq) return;
   if ((lane & 15) == 0) sX[(int64_t)(k >> 7) * Mp + m] = s;
-  *reinterpret_cast<uint2*>(qX + m * ldq + k) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3], f), e4m3x4(v[4], v[5], v[6], v[7], f));
+  *reinterpret_cast<uint2*>(qX + m * ldq + k) =
+      make_uint2(e4m3x4(v[0], v[1], v[2], v[3], f), e4m3x4(v[4], v[5], v[6], v[7], f));
 }
 
 template <typename T, bool VEC>

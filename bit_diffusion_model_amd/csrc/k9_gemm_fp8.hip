@@ -11,14 +11,14 @@
 // Accuracy: on E4M3 operands the matrix core takes the products of 8 successive codes together: with E the largest sum of
 // two codes' exponents (-6 of a subnormal code; zeros do not count), it drops from each product, toward zero, what lies
 // below 2^(E - 13): bit for bit so, and in the older 16x16x32 form, at a third of the rate, too.  Products of normal codes
-// within 7 binades of the largest lose nothing; so with
-// terms of random signs the loss is 1.3e-5 of the outputs' root mean square for codes of normals, 2.1e-5 with channels 30
-// times as large, 5e-5 to 6e-5 for codes of all binades alike, the same for one block and for 96; with terms of one sign
-// 2.4e-6 of the sum.  Rounding to bf16 costs 1.7e-3 in the root mean square, so bf16 outputs of tiles take that loss: 1.1%
-// of them round the other way (1.7% with those channels, 3.3% of all binades alike, 0.05% of one sign), and what cancels to
-// below a hundredth of the others is off by more than its rounding.  fp32 outputs, and the few-token kernels of either type (bound by the
-// weights' read), widen the codes to f16, exactly, whose products are kept whole in the fp32 sum (1e-8 to 9e-8 of the root
-// mean square): twice the MFMA time and the conversions (4608 x 3072 x 9216 252 us for 124).
+// within 7 binades of the largest lose nothing; so with terms of random signs the loss is 1.3e-5 of the outputs' root mean
+// square for codes of normals, 2.1e-5 with channels 30 times as large, 5e-5 to 6e-5 for codes of all binades alike, the
+// same for one block and for 96; with terms of one sign 2.4e-6 of the sum.  Rounding to bf16 costs 1.7e-3 in the root mean
+// square, so bf16 outputs of tiles take that loss: 1.1% of them round the other way (1.7% with those channels, 3.3% of all
+// binades alike, 0.05% of one sign), and what cancels to below a hundredth of the others is off by more than its rounding.
+// fp32 outputs, and the few-token kernels of either type (bound by the weights' read), widen the codes to f16, exactly,
+// whose products are kept whole in the fp32 sum (1e-8 to 9e-8 of the root mean square): twice the MFMA time and the
+// conversions (4608 x 3072 x 9216 252 us for 124).
 #include <type_traits>
 
 #include "fp8.hpp"
@@ -44,8 +44,10 @@ __device__ __forceinline__ v4f mfma16(v8i a, v8i b, v4f c) {
 typedef _Float16 v8hf __attribute__((ext_vector_type(8)));
 struct Half32 { v8hf v[4]; };
 __device__ __forceinline__ v8hf widen8(int a, int b) {
-  const h2 p = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false), q = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
-  const h2 r = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false), t = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
+  const h2 p = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false);
+  const h2 q = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
+  const h2 r = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false);
+  const h2 t = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
   return v8hf{p.x, p.y, q.x, q.y, r.x, r.y, t.x, t.y};
 }
 __device__ __forceinline__ Half32 widen(v8i c) {
@@ -139,8 +141,9 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld,
     const int s = k * KG + g;
     const uint32_t on = s < nst ? 0xFFFFFFFFu : 0u;
     if (n < NA) {
-      dma16(make_rsrc(qX + m0 * ld, (rows * (uint32_t)ld) & on), a + g * AB + (wave + NW * n) * 1024, va[n], (uint32_t)(s0 + s) * 128);
-    } else if (n < NA + NB) {  // channel block c of the tile: 16 ld bytes from the one before it, 2 KB (two fragments) per stage
+      dma16(make_rsrc(qX + m0 * ld, (rows * (uint32_t)ld) & on), a + g * AB + (wave + NW * n) * 1024, va[n],
+            (uint32_t)(s0 + s) * 128);
+    } else if (n < NA + NB) {  // channel block c: 16 ld bytes from the one before it, 2 KB (two fragments) per stage
       dma16(make_rsrc(qW + n0 * ld, (blocks * 16 * (uint32_t)ld) & on), b + g * BB + (wave + NW * (n - NA)) * 1024, vb[n - NA],
             (uint32_t)(s0 + s) * 2048);
     } else {
@@ -152,7 +155,8 @@ __device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld,
   // Token operands in registers; how many groups ahead they are read; a stage's loads go out over STEPS groups, PER in each,
   // the first AHEAD of them behind the barrier, the others in the next stage
   // (7 groups a stage: with 4 sets of registers, group i in set i & 3, only two groups are ahead without meeting)
-  constexpr int RING = IA == 6 ? 3 : IA > 2 ? 4 : 2, AHEAD = IA % 8 == 0 ? 3 : IA > 2 ? 2 : 1, STEPS = IA > 4 ? 5 : IA > 2 ? 3 : 1;
+  constexpr int RING = IA == 6 ? 3 : IA > 2 ? 4 : 2, AHEAD = IA % 8 == 0 ? 3 : IA > 2 ? 2 : 1;
+  constexpr int STEPS = IA > 4 ? 5 : IA > 2 ? 3 : 1;
   static_assert(IA % RING == 0 || (IA % RING == 3 && AHEAD == 2), "the groups in flight lie in different sets");
   constexpr int PER = (NL + STEPS - 1) / STEPS, FIRST = PER * AHEAD < NL ? PER * AHEAD : NL;
   v4f acc[IA][JB], T[JB];
@@ -426,8 +430,10 @@ __global__ __launch_bounds__(64 * FEW_NW) void k9_few(const uint8_t* __restrict_
       for (int h = 0; h < 2; ++h) {
         w[u][h] = *reinterpret_cast<const uint4*>(wl + in * 2048 + h * 1024);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          x[u][t][h] = buf_load16(rX, at < nb ? (uint32_t)at * 128 + h * 64 + (uint32_t)(16 * t) * (uint32_t)ld + xoff : kNoLoad);
+        for (int t = 0; t < NT; ++t) {
+          const uint32_t off = (uint32_t)at * 128 + h * 64 + (uint32_t)(16 * t) * (uint32_t)ld + xoff;
+          x[u][t][h] = buf_load16(rX, at < nb ? off : kNoLoad);
+        }
       }
       c[u] = at < nb ? sw[in] : 0.0f;
 #pragma unroll
@@ -481,9 +487,10 @@ __global__ __launch_bounds__(64 * FEW_NW) void k9_few_layer(const T* __restrict_
   };
   for (int j0 = wave * 16; j0 == wave * 16 || j0 < jobs; j0 += FEW_NW * 16) {
     const int j = j0 + m, row = j / nb, k0 = (j - row * nb) * 128 + 16 * l4;
+    const T* x = X + (j < jobs ? row : 0) * ldx;
     Vec<T, 8> raw[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) raw[q] = load8(X + (j < jobs ? row : 0) * ldx, k0 + (q >> 1) * 64 + (q & 1) * 8, j < jobs ? K : 0);
+    for (int q = 0; q < 4; ++q) raw[q] = load8(x, k0 + (q >> 1) * 64 + (q & 1) * 8, j < jobs ? K : 0);
     if (j0 == wave * 16) load_w(cb0);
     if (j0 >= jobs) break;
     float v[32], s, r;
@@ -542,8 +549,8 @@ __global__ __launch_bounds__(64 * FEW_NW) void k9_few_layer(const T* __restrict_
 }
 
 template <int WM, int WN, int IA, int TJ, int KG>
-void launch_tiles(const Fp8Plan& p, int64_t ld, const uint8_t* qX, const uint8_t* qW, const Scales& sc, const Out& o, float* part,
-                  hipStream_t st) {
+void launch_tiles(const Fp8Plan& p, int64_t ld, const uint8_t* qX, const uint8_t* qW, const Scales& sc, const Out& o,
+                  float* part, hipStream_t st) {
   constexpr int BM = 16 * IA * WM, BN = 32 * TJ * WN;
   const uint32_t tm = (uint32_t)((o.M + BM - 1) / BM), tn = (uint32_t)((o.N + BN - 1) / BN);
   const dim3 grid(tm * tn, (uint32_t)p.parts), block(64 * WM * WN * KG);
@@ -661,7 +668,7 @@ hipError_t launch_few_layer_fp8(int64_t M, int64_t K, int64_t N, const void* X, 
   // as many workgroups as the card holds (two to a unit), and no more turns than that takes
   const int64_t ld = i8_ld(K), cbs = (N + 15) / 16, most = 2 * (int64_t)device_cus(), turns = (cbs + most - 1) / most;
   const dim3 g((uint32_t)((cbs + turns - 1) / turns)), b(64 * FEW_NW);
-  const size_t lds = (size_t)(M * sc.blocks) * 132;  // at most 66 KB
+  const size_t lds = (size_t)(M * sc.blocks) * 132;  // at most 33 KB: up to 256 blocks run here
   auto typed = [&](auto x) {
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, g, b, lds, st, x, ldx, (int)K, ld, qW, sc, o, (int)turns); };
     typedef typename std::remove_const<typename std::remove_pointer<decltype(x)>::type>::type T;

@@ -179,7 +179,8 @@ struct LayerNormGradPlan {
   int w, waves, cw;
   size_t bytes;
 };
-LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, bool sums, bool apart);  // apart: whether columns may be summed so
+// each: whether images have their own sums; sums: whether any are asked for; apart: whether columns may have their own blocks
+LayerNormGradPlan plan_layer_norm_grad(int64_t B, int64_t S, int C, bool each, bool sums, bool apart);
 // How the norm holds a row: `lanes` lanes (64: `waves` waves of them), `chunks` chunks of 8 values each.
 struct LayerNormPlan {
   int lanes, chunks, waves;

@@ -1118,8 +1118,8 @@ class LayerNorm:
         return X.new_empty((2, X.numel() // self.C), dtype=torch.float32).unbind()
 
     def plan(self, B: int, S: int):
-        """svdq_debug_layer_norm_plan: (lanes, chunks, waves to a row, blocks that the gradient's sums are joined from or, negative,
-        columns to a block that sums them)."""
+        """svdq_debug_layer_norm_plan: (lanes, chunks, waves to a row, blocks that the gradient's sums are joined from or,
+        negative, columns to a block that sums them)."""
         p = (ctypes.c_int32 * 4)()
         _check(lib().svdq_debug_layer_norm_plan(self._ref, B, S, p))
         return tuple(p)

@@ -567,13 +567,14 @@ svdq_status svdq_norm_linear_forward_int8(const svdq_group_norm_desc* norm, cons
  *             and for bf16 Y of up to 32 rows that run without tiles, the codes are multiplied as fp16, whose products are
  *             exact and added in fp32.  For other bf16 Y they are multiplied as they are, at twice the rate: of 8
  *             successive products the matrix core then drops, from each and toward zero, what lies below 2^-13 of the
- *             power of two that the exponents of the largest product's codes give, those of subnormal codes being -6 (7 2^-13 of
- *             sum |terms| at the very worst, with codes below 2^-6 taken for that).  Where the terms' signs are random that is 1.3e-5 (codes of normals) to 6e-5 (codes of all binades
- *             alike) of the outputs' root mean square, whatever K, a thirtieth to a hundredth of what rounding to bf16
- *             costs; where they are all of one sign 2.4e-6 of the sum, toward zero.  An output that cancels to below a
- *             hundredth of the others is off by more than its own rounding, and a row's bf16 outputs may differ by this
- *             loss between numbers of rows that run on different kernels (svdq_debug_fp8_plan).  Ask for fp32 Y where
- *             whole sums matter.  The factors s_X s_W have to stay within fp32.
+ *             power of two that the exponents of the largest product's codes give, those of subnormal codes being -6
+ *             (7 2^-13 of sum |terms| at the very worst, with codes below 2^-6 taken for that).  Where the terms' signs
+ *             are random that is 1.3e-5 (codes of normals) to 6e-5 (codes of all binades alike) of the outputs' root mean
+ *             square, whatever K, a thirtieth to a hundredth of what rounding to bf16 costs; where they are all of one
+ *             sign 2.4e-6 of the sum, toward zero.  An output that cancels to below a hundredth of the others is off by
+ *             more than its own rounding, and a row's bf16 outputs may differ by this loss between numbers of rows that
+ *             run on different kernels (svdq_debug_fp8_plan).  Ask for fp32 Y where whole sums matter.  The factors
+ *             s_X s_W have to stay within fp32.
  * E4M3 is the finite variant (bias 7, subnormals to 2^-9, largest 448, 0x7F and 0xFF NaN).  Rows of codes are
  * svdq_int8_ld(K) = K rounded up to 128 bytes long; the bytes past K are zero.  Scales of activations are
  * [ceil(K / 128)][Mp] fp32, Mp = M rounded up to 4 (what lies past M is neither written nor used); of weights
@@ -625,8 +626,8 @@ svdq_status svdq_linear_forward_fp8(const svdq_fp8_layer* layer, int64_t M, cons
 /* ------------------------------------------ layer norm and its gradient ---- */
 /* X [B][S][C] (image, row, channel; row stride ldx, image stride bsx, in elements).  Per row: mean and biased variance
  * in fp32 (sums of differences to a first mean, joined pairwise: no cancellation however far the mean lies from zero); z
- * = (x - mean) rstd, rstd = 1 / sqrt(var + eps); y = z w + beta, one rounding an operation, w = gamma, or 1 + gamma where one_plus is 1 (the
- * scale and shift of a modulated norm).  gamma and beta [C] serve all rows (image_stride 0), or image b those at
+ * = (x - mean) rstd, rstd = 1 / sqrt(var + eps); y = z w + beta, one rounding an operation, w = gamma, or 1 + gamma where
+ * one_plus is 1 (the scale and shift of a modulated norm).  gamma and beta [C] serve all rows (image_stride 0), or image b those at
  * b image_stride.  A NaN or an infinity makes its row's outputs NaN and no other row's; sums of values and of squared
  * differences have to stay within fp32.  Images of X (and dY) are apart, or one and the same (stride 0).  Limits: C <=
  * 16384, B <= 65535, B S < 2^31, row strides < 2^31, image strides < 2^46 (EUNSUPPORTED beyond). */
