@@ -19,10 +19,10 @@
 // The columns' sums of the gradient stay in registers over a block's rows, the next row on its way while one is
 // computed; a block joins its teams in LDS and leaves one partial sum; a second launch adds the blocks'; for few rows
 // blocks of their own sum the columns in the same launch.  Every order is fixed: no atomics.
-// Measured: 65536 x 4096 fp32 420 us (5.1 TB/s, as a large copy); 2 x 4608 x 3072 bf16, modulated, 25 (4.5 TB/s; the vector
-// units are busy 66%, 385 instructions a wave of 24 values a lane); 4608 x 3072 to codes 13.2 (555, busy 82%; kernel 8 on a
-// written y 9.1); gradient 2 x 4608 x 3072 bf16 39 (34 and the second launch's 4; 4.4 TB/s), 3 x 333 x 1111 fp32 9.2 in one
-// launch.
+// Measured: 65536 x 4096 fp32 427 us (5.0 TB/s, as a large copy); 2 x 4608 x 3072 bf16, modulated, 25 (4.6 TB/s; the vector
+// units are busy 62%, 383 instructions a wave of 24 values a lane); 4608 x 3072 to codes 12.9 (553, busy 81%; 16 behind a
+// product that has lowered the clock; kernel 8 on a written y 8.6); gradient 2 x 4608 x 3072 bf16 39 (35 and the second
+// launch's 4; 4.3 TB/s), 3 x 333 x 1111 fp32 9.2 in one launch.
 #include <algorithm>
 #include <type_traits>
 

@@ -6,9 +6,10 @@
 // Design (gfx950): bound by HBM (x read once, a byte per value written).  Blocks of 128 are independent, so a row
 // needs no join: 16 lanes hold a block, 8 values each, and meet by lane moves.  A wave takes 512 values of a row, a
 // workgroup four rows, whose scales lie side by side (the scales' rows run along the tokens, which is how the product
-// reads them).  4608 x 3072 bf16 8.9 us, 16384 x 2048 21: 4.8 TB/s of what a large copy reaches 5.1.  (Four rows a wave with
-// 64 scales joined in LDS, whole runs of 16: 9.3, and 2.9 against 2.1 at 154 x 768, 7.2 against 6.3 at 3000 x 3072, but
-// 32.0 against 33.4 at 4608 x 12288.)
+// reads them).  4608 x 3072 bf16 8.6 us (10.5 behind a product that has lowered the clock and filled the caches), 16384 x
+// 2048 21: 4.8 TB/s of what a large copy reaches 5.1.  (Four rows a wave with 64 scales joined in LDS, whole runs of 16,
+// measured in turn: 9.3 against 8.9, and 2.9 against 2.1 at 154 x 768, 7.2 against 6.3 at 3000 x 3072, but 32.0 against 33.4
+// at 4608 x 12288.)
 #include "fp8.hpp"
 #include "kernels.hpp"
 

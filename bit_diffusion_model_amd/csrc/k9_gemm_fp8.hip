@@ -87,10 +87,12 @@ struct Scales {
 // 178), a stage's loads spread over its groups (159 for 163), the tokens' scales come with the operands, by 4-byte loads
 // into LDS (a wave's 64 lanes fetch the scales that are its share); the weights' stand in a register, lane s for stage s of
 // 64, and are read out by lane.
-// Bound (4608 x 12288 x 3072 bf16, 150 us, 2.3 POP/s; 4608 x 3072 x 9216 124, 2.1): power.  The matrix cores are busy 64%
-// of the cycles on 252 units in tiles of 224 rows (77% on 216 units in tiles of 256) and the clock falls to 1.95 GHz
-// (1.81); without the FMAs it takes as long.  fp32 outputs (512 x 9216 x 3072 45 us): the conversions, at half the vector
-// rate, twice for each operand in tiles of 64 (vector units busy 58%, matrix cores 35%).
+// Bound.  4608 x 12288 x 3072 bf16, 150 to 160 us, 2.2 POP/s: power.  The matrix cores are busy 64% of the cycles on 252
+// units in tiles of 224 rows (77% on 216 units in tiles of 256) and the clock falls to 1.95 GHz (1.81); without the FMAs it
+// takes as long.  At K = 3072 the share of a round that nothing overlaps, a tile's first loads and its stores, 7.2 us for
+// 34.6 of work: 4608 x 3072 x 9216 124 to 128 us, 2.1 POP/s, the matrix cores busy 58%; 4608 x 3072 x 12288 with GELU 180 to
+// 200, 52%.  fp32 outputs (512 x 9216 x 3072 46 us): the conversions, at half the vector rate, twice for each operand in
+// tiles of 64 (vector units busy 58%, matrix cores 35%).
 template <int WM, int WN, int IA, int TJ, int KG, int ROOM, int OUT>
 __device__ __forceinline__ void tile(const uint8_t* __restrict__ qX, int64_t ld, const uint8_t* __restrict__ qW,
                                      const Scales& sc, const Out& o, int64_t m0, int64_t n0, float* __restrict__ part,
